@@ -18,6 +18,11 @@
  * scores):
  *      dsa_select_pools    top pools per row under (score DESC, pool ASC)
  *      dsa_expand_selection  pools to tokens, plus the visible tail
+ * and, for a batch of requests each with its own number of new tokens:
+ *      dsa_plan_rows       the requests' block tables grown or shrunk from a free
+ *                          list, and every row's metadata, from the lengths
+ *      dsa_mla_chunk_fp8   dense causal attention of the new tokens over the paged
+ *                          latent cache (no selection)
  * Sources (spark_model documentation):
  * the "glm5next_dsa/layer.rs" source page (module header: decode data flow
  * and its traps; decode_k: latent write, per-row metadata, one attend for all
@@ -54,7 +59,7 @@
 extern "C" {
 #endif
 
-#define DSA_ABI_VERSION 4
+#define DSA_ABI_VERSION 5
 #define DSA_LATENT_DIM 512
 
 typedef enum dsa_status {
@@ -76,8 +81,10 @@ enum {
     DSA_DEVERR_ARENA = 5,     /* idx_base invalid, or rows of one group differ in base  */
     DSA_DEVERR_POSITION = 6,  /* positions[r] != seq_lens[r]-1, or slot != table slot   */
     DSA_DEVERR_TIMEOUT = 7,   /* a bounded wait inside a kernel gave up                 */
-    DSA_DEVERR_BEHIND = 8     /* a sequence's indexer keys stop short of its length:
+    DSA_DEVERR_BEHIND = 8,    /* a sequence's indexer keys stop short of its length:
                                  rows were never written (lockstep with the KV cache)  */
+    DSA_DEVERR_ROWS = 9,      /* a sequence's rows lie outside the row buffers          */
+    DSA_DEVERR_FREE = 10      /* free list too short for the blocks wanted, or too full  */
 };
 
 /*
@@ -412,6 +419,131 @@ int32_t dsa_dense_mm_splits(int32_t n_out, int32_t k, int32_t num_sms);
 /* Workspace bytes dsa_dense_mm_bf16 needs on the current device for a weight
  * of n_out x k (0 when it needs none or on bad arguments). */
 size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
+
+/*
+ * Row plan of a batch of requests: block tables grown and shrunk from a free
+ * list, and the per-row metadata of the step (dsa_rows: positions, slots,
+ * seq_lens, block_table; "glm5next_dsa/layer.rs", decode_k, the K-row
+ * attn_metadata), built on the device from the requests' lengths.  The pages
+ * take the tables from their host scheduler; this is the same step for
+ * callers whose lengths are device data.
+ * Request s has L = seq_lens[s] tokens once the step's n = new_tokens[s] new
+ * ones are counted, and holds h = held_in[s] blocks, the first h entries of
+ * its table row.  need = ceil(L / block_size).
+ *   - need < h (a finished request, L = 0, or a rejected verify's tokens): its
+ *     entries need .. h-1 go back to the free list, in order, requests in
+ *     order.  The table keeps the stale ids there.
+ *   - need > h: entries h .. need-1 are taken from the free list.
+ * The free list is a stack: free_blocks[0 .. F), F = free_in[0].  The blocks
+ * given back (Rtot of them) are pushed first, then requests in order pop theirs
+ * from the top.  A request is refused when the blocks wanted up to and
+ * including its own exceed F + Rtot: the blocks it wanted become -1 in its
+ * table, it keeps h blocks, its rows are empty, and DSA_DEVERR_FREE is recorded.
+ *   held_out[s] = need (h if refused), free_out[0] = blocks left on the stack.
+ * Rows: request s owns rows row_start[s] .. row_start[s+1]-1, n of them; its
+ * row i has
+ *   positions = L-n+i, seq_lens = positions+1, row_seq = s,
+ *   slots = table[positions / block_size] * block_size + positions % block_size,
+ *   block_table row = the request's need blocks, then -1 up to max_blocks_per_seq
+ * An empty row has position 0, seq_len 0, slot -1 and a table row of -1.  Rows
+ * from row_start[seqs] on are left as they were.
+ * A request with n outside [0, min(L, rows)], need > max_blocks_per_seq or h
+ * outside [0, max_blocks_per_seq] is recorded (DSA_DEVERR_SEQ_LEN, with s as
+ * the row) and changes nothing; its n rows, if 0 <= n <= rows, are empty.
+ * Rows past `rows` are not written (DSA_DEVERR_ROWS).  F outside [0,
+ * free_capacity] is recorded (DSA_DEVERR_FREE) and counts as 0; blocks that
+ * would not fit free_capacity are dropped (DSA_DEVERR_FREE).
+ * held_out may be held_in and free_out may be free_in (the state is then kept
+ * in place and the call can be captured and replayed); they must not overlap
+ * otherwise.  With separate buffers a repeated call gives the same result.
+ * free_out[1] must be 0 before the first call and is 0 after each; calls that
+ * share a state or output buffer must not overlap on the GPU.
+ * Limits: seqs <= DSA_PLAN_MAX_SEQS, rows <= 65535, seqs *
+ * max_blocks_per_seq, block_size * max_blocks_per_seq < 2^31
+ * (DSA_ERR_UNSUPPORTED).
+ */
+#define DSA_PLAN_MAX_SEQS 8192
+typedef struct dsa_plan {
+    const int32_t *seq_lens;     /* [seqs] tokens, the new ones included                */
+    const int32_t *new_tokens;   /* [seqs] rows wanted                                   */
+    const int32_t *held_in;      /* [seqs] blocks held before                            */
+    int32_t *held_out;           /* [seqs] blocks held after                             */
+    int32_t *block_table;        /* request s at block_table + s*bt_stride (in place)    */
+    int32_t *free_blocks;        /* [free_capacity] stack of free block ids (in place)   */
+    const int32_t *free_in;      /* [1] ids on the stack before                          */
+    int32_t *free_out;           /* [2] ids on the stack after, and a word kept at 0     */
+    int32_t *row_start;          /* [seqs + 1] out                                       */
+    uint32_t *positions;         /* [rows] out                                           */
+    int64_t *slots;              /* [rows] out                                           */
+    int32_t *row_lens;           /* [rows] out: seq_lens of the rows                     */
+    int32_t *row_table;          /* row r at row_table + r*row_bt_stride, out; may be NULL */
+    int32_t *row_seq;            /* [rows] out; may be NULL                              */
+    int32_t seqs;
+    int32_t rows;                /* rows the row buffers hold                            */
+    int32_t max_blocks_per_seq;  /* entries of a table row                               */
+    int32_t bt_stride;           /* elements between the requests' table rows            */
+    int32_t row_bt_stride;       /* elements between the rows' table rows                */
+    int32_t block_size;
+    int32_t free_capacity;
+    int32_t reserved;            /* 0                                                    */
+} dsa_plan;
+dsa_status dsa_plan_rows(const dsa_plan *plan, void *stream);
+
+/*
+ * Per-request metadata of dsa_mla_chunk_fp8, all device pointers (as written
+ * by dsa_plan_rows, or by the caller).  Request s has seq_lens[s] tokens in the
+ * cache; its new ones, the last row_start[s+1] - row_start[s] of them, are the
+ * rows row_start[s] .. row_start[s+1]-1 of q and out.
+ */
+typedef struct dsa_seqs {
+    const int32_t *seq_lens;     /* [seqs]                                               */
+    const int32_t *row_start;    /* [seqs + 1], not decreasing                           */
+    const int32_t *block_table;  /* request s at block_table + s*bt_stride               */
+    int32_t max_blocks_per_seq;
+    int32_t bt_stride;           /* >= max_blocks_per_seq                                */
+    int32_t block_size;          /* > 0                                                  */
+    int32_t seqs;                /* >= 1                                                 */
+} dsa_seqs;
+
+/*
+ * Attention of each request's new tokens over its paged latent cache: dense
+ * and causal, absorbed NoPE MLA as in dsa_mla_decode_fp8 ("glm5next_dsa/
+ * layer.rs", module header trap 4 and decode_k: K and V are the same latent
+ * pool, slot = block*block_size + pos%block_size), which it equals when that
+ * call's selection holds every visible token.  Row i of request s (n rows, L =
+ * seq_lens[s]) and head h, over the tokens j < L - n + i + 1:
+ *   Khat_j = e4m3(pool[slot(j)]) * kv_scale
+ *   z_j    = sm_scale * (q[row][h] . Khat_j)
+ *   out[row][h] = sum_j softmax(z)_j * Khat_j        (bf16, latent space)
+ *   lse[row][h] = log sum_j exp(z_j)                  (fp32, optional)
+ * The latents of the new tokens are written first (dsa_latent_write).  A token
+ * whose block is missing (negative, or past the pool) is left out and recorded
+ * (DSA_DEVERR_BLOCK); a row that sees no token gets out = 0 and lse = -inf.  What
+ * the pool holds at tokens a row does not see, NaN codes included, never
+ * reaches the row.  A request whose rows lie outside [0, rows)
+ * (DSA_DEVERR_ROWS), or with rows and seq_lens[s] < n or above
+ * max_blocks_per_seq * block_size (DSA_DEVERR_SEQ_LEN), is skipped, its rows
+ * left as they were (the recorded row is s).  Rows of no request are left as
+ * they were.
+ *   q   [rows][heads][latent_dim] bf16       pool [nslots][latent_dim] FP8
+ *   out [rows][heads][latent_dim] bf16       lse  [rows][heads] fp32 or NULL
+ * latent_dim must be 512; heads a multiple of 16 up to 4096; rows <= 65535;
+ * seqs <= DSA_PLAN_MAX_SEQS; nslots and block_size * max_blocks_per_seq below
+ * 2^31 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and out 16-byte aligned; out
+ * must not overlap q or the pool.  The workspace holds
+ * dsa_chunk_workspace_bytes(rows, heads) bytes, 256-byte aligned
+ * (DSA_ERR_WORKSPACE otherwise), needs no initial value, and belongs to the call
+ * until its work completes: calls that may overlap on the GPU (other streams,
+ * two captured graphs) need one each.
+ */
+dsa_status dsa_mla_chunk_fp8(const dsa_seqs *seqs, const uint16_t *q, const uint8_t *pool,
+                             int64_t nslots, int32_t rows, int32_t heads, int32_t latent_dim,
+                             float kv_scale, float sm_scale, uint16_t *out, float *lse_or_null,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of dsa_mla_chunk_fp8 on the current device (0 on bad
+ * arguments). */
+size_t dsa_chunk_workspace_bytes(int32_t rows, int32_t heads);
 
 /*
  * Read the sticky device error word of the current device: *code_out is the

@@ -18,7 +18,7 @@ LATENT_DIM = 512
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error",
            4: "device-side error recorded", 5: "workspace missing or too small"}
 DEVERR = {0: "none", 1: "seq_len", 2: "slot", 3: "select", 4: "block", 5: "arena",
-          6: "position", 7: "timeout", 8: "behind"}
+          6: "position", 7: "timeout", 8: "behind", 9: "rows", 10: "free"}
 
 
 class DsaError(RuntimeError):
@@ -33,6 +33,24 @@ class Rows(ctypes.Structure):
                 ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("max_blocks_per_seq", ctypes.c_int32), ("bt_stride", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
+class Plan(ctypes.Structure):
+    """dsa_plan: one dsa_plan_rows call's buffers and sizes (see make_plan)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "seq_lens", "new_tokens", "held_in", "held_out", "block_table", "free_blocks", "free_in",
+        "free_out", "row_start", "positions", "slots", "row_lens", "row_table", "row_seq")]
+        + [(n, ctypes.c_int32) for n in (
+            "seqs", "rows", "max_blocks_per_seq", "bt_stride", "row_bt_stride", "block_size",
+            "free_capacity", "reserved")])
+
+
+class Seqs(ctypes.Structure):
+    """dsa_seqs: per-request metadata, all device pointers (see make_seqs)."""
+    _fields_ = [("seq_lens", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_blocks_per_seq", ctypes.c_int32),
+                ("bt_stride", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("seqs", ctypes.c_int32)]
 
 
 _lib = None
@@ -67,6 +85,8 @@ def load() -> ctypes.CDLL:
         "dsa_indexer_write": [RP, P, P, P, f32, P, P, P, P, i64, i32, P, i32, P],
         "dsa_select_pools": [RP, P, i32, P, i32, i32, i32, P, P],
         "dsa_expand_selection": [RP, P, i32, i32, P, i32, P],
+        "dsa_plan_rows": [ctypes.POINTER(Plan), P],
+        "dsa_mla_chunk_fp8": [ctypes.POINTER(Seqs), P, P, i64, i32, i32, i32, f32, f32, P, P, P, sz, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -78,6 +98,8 @@ def load() -> ctypes.CDLL:
     lib.dsa_noalloc_scratch_bytes.restype = sz
     lib.dsa_dense_mm_workspace_bytes.argtypes = [i32, i32]
     lib.dsa_dense_mm_workspace_bytes.restype = sz
+    lib.dsa_chunk_workspace_bytes.argtypes = [i32, i32]
+    lib.dsa_chunk_workspace_bytes.restype = sz
     lib.dsa_bt_entries_needed.argtypes = [i64, i64, i64]
     lib.dsa_bt_entries_needed.restype = i64
     lib.dsa_status_string.argtypes = [ctypes.c_int]
@@ -306,6 +328,141 @@ def dsa_dense_mm_bf16(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
 
 def dsa_dense_mm_workspace_bytes(n: int, k: int) -> int:
     return int(load().dsa_dense_mm_workspace_bytes(int(n), int(k)))
+
+
+def _on_device(tensors: dict, device: int | None = None) -> int:
+    """The one CUDA device that every tensor given is on."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if device is None:
+            device = t.device.index
+        if t.device.index != device:
+            raise ValueError(f"{name}: on cuda:{t.device.index}, expected cuda:{device}")
+    return device
+
+
+def _current(device: int) -> None:
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"the buffers are on cuda:{device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _shaped(t: torch.Tensor | None, shape: tuple, name: str) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _table(t: torch.Tensor, rows: int, name: str) -> tuple[int, int, int]:
+    """(pointer, entries of a row, elements between rows) of a table whose rows
+    are contiguous; the rows themselves may be a strided slice of a wider one."""
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1:
+        raise ValueError(f"{name}: expected int32 [{rows}, blocks], got {t.dtype} {tuple(t.shape)}")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: expected contiguous rows, got strides {t.stride()}")
+    return t.data_ptr(), t.shape[1], t.stride(0) if rows > 1 else t.shape[1]
+
+
+_BITS32 = (torch.int32, torch.uint32)
+
+
+def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.Tensor,
+              held_out: torch.Tensor, block_table: torch.Tensor, block_size: int,
+              free_blocks: torch.Tensor, free_in: torch.Tensor, free_out: torch.Tensor,
+              row_start: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+              row_lens: torch.Tensor, row_table: torch.Tensor | None = None,
+              row_seq: torch.Tensor | None = None) -> Plan:
+    """Argument block of dsa_plan_rows over a server's buffers, built once and
+    used every step.  int32 except slots (int64): seq_lens, new_tokens, held_in,
+    held_out [S]; block_table [S, max_blocks]; free_blocks [capacity]; free_in
+    [1 or 2]; free_out [2] (its second word starts at 0); row_start [S + 1];
+    positions (or uint32), slots, row_lens, row_seq [R]; row_table [R,
+    max_blocks].  held_out may be held_in and free_out free_in (state kept in
+    place).  The plan keeps the tensors alive."""
+    S, R = seq_lens.shape[0], positions.shape[0]
+    named = dict(seq_lens=seq_lens, new_tokens=new_tokens, held_in=held_in, held_out=held_out,
+                 block_table=block_table, free_blocks=free_blocks, free_in=free_in,
+                 free_out=free_out, row_start=row_start, positions=positions, slots=slots,
+                 row_lens=row_lens, row_table=row_table, row_seq=row_seq)
+    device = _on_device(named)
+    for name in ("seq_lens", "new_tokens", "held_in", "held_out"):
+        _shaped(named[name], (S,), name)
+    for name in ("positions", "slots", "row_lens", "row_seq"):
+        _shaped(named[name], (R,), name)
+    _shaped(row_start, (S + 1,), "row_start")
+    _shaped(free_out, (2,), "free_out")
+    if free_in.dim() != 1 or free_in.shape[0] not in (1, 2):
+        raise ValueError(f"free_in: expected shape (1,) or (2,), got {tuple(free_in.shape)}")
+    if free_blocks.dim() != 1:
+        raise ValueError(f"free_blocks: expected one dimension, got {tuple(free_blocks.shape)}")
+    plan = Plan()
+    for name, t in named.items():
+        if name in ("block_table", "row_table"):
+            continue
+        want = torch.int64 if name == "slots" else torch.int32
+        if name == "positions" and t.dtype in _BITS32:
+            want = t.dtype
+        setattr(plan, name, _ptr(t, want, name))
+    plan.block_table, plan.max_blocks_per_seq, plan.bt_stride = _table(block_table, S, "block_table")
+    if row_table is not None:
+        plan.row_table, width, plan.row_bt_stride = _table(row_table, R, "row_table")
+        if width != plan.max_blocks_per_seq:
+            raise ValueError(f"row_table: expected {plan.max_blocks_per_seq} entries a row, got {width}")
+    plan.seqs, plan.rows, plan.block_size = S, R, int(block_size)
+    plan.free_capacity = free_blocks.shape[0]
+    plan.tensors, plan.device = named, device
+    return plan
+
+
+def dsa_plan_rows(plan: Plan, stream=None) -> None:
+    """The requests' block tables grown and shrunk from the free list, and the
+    rows' metadata, into the plan's buffers."""
+    _current(plan.device)
+    _check("dsa_plan_rows", load().dsa_plan_rows(ctypes.byref(plan), _stream(stream)))
+
+
+def make_seqs(seq_lens: torch.Tensor, row_start: torch.Tensor, block_table: torch.Tensor,
+              block_size: int) -> Seqs:
+    """Build dsa_seqs from device tensors: seq_lens int32 [S], row_start int32
+    [S + 1], block_table int32 [S, max_blocks].  The struct keeps them alive."""
+    S = seq_lens.shape[0]
+    seqs = Seqs()
+    seqs.device = _on_device(dict(seq_lens=seq_lens, row_start=row_start, block_table=block_table))
+    _shaped(seq_lens, (S,), "seq_lens")
+    _shaped(row_start, (S + 1,), "row_start")
+    seqs.seq_lens = _ptr(seq_lens, torch.int32, "seq_lens")
+    seqs.row_start = _ptr(row_start, torch.int32, "row_start")
+    seqs.block_table, seqs.max_blocks_per_seq, seqs.bt_stride = _table(block_table, S, "block_table")
+    seqs.block_size, seqs.seqs = int(block_size), S
+    seqs.tensors = (seq_lens, row_start, block_table)
+    return seqs
+
+
+def dsa_mla_chunk_fp8(seqs: Seqs, q: torch.Tensor, pool: torch.Tensor, kv_scale: float,
+                      sm_scale: float, out: torch.Tensor, lse: torch.Tensor | None,
+                      workspace: torch.Tensor, stream=None) -> None:
+    """Dense causal attention of each request's new tokens over its paged latent
+    cache: q, out [R, heads, 512] bf16, pool [slots, 512] FP8 codes (uint8), lse
+    [R, heads] fp32 or None, workspace of dsa_chunk_workspace_bytes(R, heads)."""
+    _on_device(dict(q=q, pool=pool, out=out, lse=lse, workspace=workspace), seqs.device)
+    _current(seqs.device)
+    if q.dim() != 3 or pool.dim() != 2 or pool.shape[1] != q.shape[2]:
+        raise ValueError(f"shapes q {tuple(q.shape)}, pool {tuple(pool.shape)}")
+    rows, heads, dim = q.shape
+    _shaped(out, (rows, heads, dim), "out")
+    _shaped(lse, (rows, heads), "lse")
+    st = load().dsa_mla_chunk_fp8(ctypes.byref(seqs), _ptr(q, torch.uint16, "q"),
+                                  _ptr(pool, torch.uint8, "pool"), pool.shape[0], rows, heads, dim,
+                                  kv_scale, sm_scale, _ptr(out, torch.uint16, "out"),
+                                  _ptr(lse, torch.float32, "lse"), _ptr(workspace, None, "workspace"),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("dsa_mla_chunk_fp8", st)
+
+
+def dsa_chunk_workspace_bytes(rows: int, heads: int) -> int:
+    return int(load().dsa_chunk_workspace_bytes(int(rows), int(heads)))
 
 
 def dsa_workspace_bytes(rows: int, heads: int, topk: int) -> int:

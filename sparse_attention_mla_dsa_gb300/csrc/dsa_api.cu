@@ -453,6 +453,71 @@ dsa_status dsa_dense_mm_bf16(const uint16_t* a, const uint16_t* b, void* c, int3
   return launched(launch_dense_mm(p, wmap, amap, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
+  if (plan == nullptr) return DSA_ERR_INVALID_ARG;
+  const dsa_plan& p = *plan;
+  if (p.seq_lens == nullptr || p.new_tokens == nullptr || p.held_in == nullptr ||
+      p.held_out == nullptr || p.block_table == nullptr || p.free_blocks == nullptr ||
+      p.free_in == nullptr || p.free_out == nullptr || p.row_start == nullptr ||
+      p.positions == nullptr || p.slots == nullptr || p.row_lens == nullptr)
+    return DSA_ERR_INVALID_ARG;
+  if (p.seqs < 1 || p.rows < 1 || p.max_blocks_per_seq < 1 || p.block_size < 1 ||
+      p.bt_stride < p.max_blocks_per_seq || p.free_capacity < 1 || p.reserved != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (p.row_table != nullptr && p.row_bt_stride < p.max_blocks_per_seq) return DSA_ERR_INVALID_ARG;
+  if (p.seqs > DSA_PLAN_MAX_SEQS || p.rows > 65535) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p.seqs) * p.max_blocks_per_seq > INT32_MAX ||
+      static_cast<int64_t>(p.block_size) * p.max_blocks_per_seq > INT32_MAX)
+    return DSA_ERR_UNSUPPORTED;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  PlanRowsParams k{};
+  k.p = p;
+  k.err = dev->err;
+  return launched(launch_plan_rows(k, dev->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_chunk_workspace_bytes(int32_t rows, int32_t heads) {
+  if (rows < 1 || rows > 65535 || heads < 16 || heads % 16 != 0 || heads > 4096) return 0;
+  return 256;
+}
+
+dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint8_t* pool,
+                             int64_t nslots, int32_t rows, int32_t heads, int32_t latent_dim,
+                             float kv_scale, float sm_scale, uint16_t* out, float* lse_or_null,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (seqs == nullptr || seqs->seq_lens == nullptr || seqs->row_start == nullptr ||
+      seqs->block_table == nullptr || q == nullptr || pool == nullptr || out == nullptr)
+    return DSA_ERR_INVALID_ARG;
+  if (seqs->seqs < 1 || rows < 1 || nslots < 1 || seqs->block_size < 1 ||
+      seqs->max_blocks_per_seq < 1 || seqs->bt_stride < seqs->max_blocks_per_seq)
+    return DSA_ERR_INVALID_ARG;
+  if (latent_dim != DSA_LATENT_DIM || nslots > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (heads < 16 || heads % 16 != 0 || heads > 4096) return DSA_ERR_UNSUPPORTED;
+  if (rows > 65535 || seqs->seqs > DSA_PLAN_MAX_SEQS) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq > INT32_MAX)
+    return DSA_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < dsa_chunk_workspace_bytes(rows, heads) ||
+      !aligned(workspace, 256))
+    return DSA_ERR_WORKSPACE;
+  ChunkParams p{};
+  p.seqs = *seqs;
+  p.q = q;
+  p.pool = pool;
+  p.nslots = nslots;
+  p.out = out;
+  p.lse = lse_or_null;
+  p.err = dev->err;
+  p.rows = rows;
+  p.heads = heads;
+  p.kv_scale = kv_scale;
+  p.sm_scale = sm_scale;
+  return launched(launch_mla_chunk(p, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_get_error(int32_t* code_out, int32_t* row_out, int32_t* count_out, int32_t reset) {
   const DeviceInfo* dev = device_info();
   if (dev == nullptr) return DSA_ERR_CUDA;

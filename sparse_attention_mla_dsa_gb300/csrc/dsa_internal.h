@@ -183,4 +183,26 @@ void mla_decode_tc_bind_workspace(DecodeParams& p, void* workspace);
 cudaError_t launch_mla_decode_tc(const DecodeParams& p, const CUtensorMap& pmap,
                                  cudaStream_t stream);
 
+struct PlanRowsParams {
+  dsa_plan p;
+  int* err;
+};
+// num_sms bounds the grid only; the results do not depend on it.
+cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t stream);
+
+struct ChunkParams {
+  dsa_seqs seqs;
+  const uint16_t* q;
+  const uint8_t* pool;
+  int64_t nslots;
+  uint16_t* out;
+  float* lse;
+  int* err;
+  int32_t rows;
+  int32_t heads;
+  float kv_scale;
+  float sm_scale;
+};
+cudaError_t launch_mla_chunk(const ChunkParams& p, cudaStream_t stream);
+
 }  // namespace dsa

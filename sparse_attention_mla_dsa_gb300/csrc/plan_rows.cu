@@ -1,0 +1,258 @@
+// plan_rows.cu -- block tables and row metadata of a batch of requests, made
+// on the device from the requests' lengths.
+//
+// "glm5next_dsa/layer.rs", decode_k: the K-row attn_metadata (positions, slots,
+// seq_lens, block tables at stable addresses) that every call of the path reads.
+//
+// With a_s = max(0, need_s - held_s) blocks wanted and r_s = max(0, held_s -
+// need_s) given back, everything follows from three prefix sums over the
+// requests (rows, a, r): the k-th block taken is element F + Rtot - 1 - k of the
+// free stack with the given-back blocks on top, whichever request takes it, and
+// a given-back block is found by a binary search of r's prefix sum.  So no CTA
+// waits for another: each loads the three arrays (12 bytes a request, from L2),
+// scans them in shared memory and writes its share of the rows, and a table
+// entry that another CTA appends is computed, not read.  Only the state kept in
+// place (held, the stack's count) has to change after every CTA has read it:
+// the CTA that takes the last ticket writes it.
+#include "dsa_device.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+// Row-table entries per CTA that are worth another CTA's scan of the requests.
+constexpr int kEntriesPerCta = 8192;
+
+struct Shared {
+  int warp_sum[3][kWarps];
+  int taken;  // blocks taken from the stack by the requests that are served
+  int last;
+};
+
+// Exclusive scan over the CTA of three values at once; `total` their sums.
+__device__ __forceinline__ void scan3(const int (&v)[3], int (&ex)[3], int (&total)[3], Shared* sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int x = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh->warp_sum[k][warp] = x;
+    ex[k] = x - v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int w = lane < kWarps ? sh->warp_sum[k][lane] : 0;
+    int x = w;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    ex[k] += __shfl_sync(0xFFFFFFFFu, x - w, warp);
+    total[k] = __shfl_sync(0xFFFFFFFFu, x, kWarps - 1);
+  }
+  __syncthreads();
+}
+
+// The requests' prefix sums in shared memory, [seqs + 1] each.
+struct Scan {
+  int* rows;   // first row
+  int* want;   // blocks wanted by the requests before
+  int* back;   // blocks given back by the requests before
+  int* held;   // blocks held before the call
+  int* need;   // blocks needed after it; -1: invalid request
+};
+
+// Index of the last entry of the exclusive prefix `a` [n + 1] that is <= x,
+// among the requests (0 <= x < a[n]): the request that x falls into.
+__device__ __forceinline__ int find(const int* a, int n, int x) {
+  int lo = 0, hi = n;  // a[lo] <= x < a[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParams kp) {
+  extern __shared__ int smem[];
+  __shared__ Shared sh;
+  const dsa_plan& p = kp.p;
+  const int n = p.seqs, tid = threadIdx.x, lane = tid & 31;
+  Scan sc;
+  sc.rows = smem;
+  sc.want = sc.rows + n + 1;
+  sc.back = sc.want + n + 1;
+  sc.held = sc.back + n + 1;
+  sc.need = sc.held + n + 1;
+  const bool first = blockIdx.x == 0;
+  grid_dep_launch();
+  grid_dep_wait();  // the lengths and the state may come from the kernel before
+
+  if (tid == 0) sh.taken = 0;
+  int carry[3] = {0, 0, 0};
+  for (int s0 = 0; s0 < n; s0 += kThreads) {
+    const int s = s0 + tid;
+    int v[3] = {0, 0, 0};
+    int held = 0, need = -1;
+    if (s < n) {
+      const int len = p.seq_lens[s], fresh = p.new_tokens[s];
+      held = p.held_in[s];
+      const int64_t blocks = (static_cast<int64_t>(len) + p.block_size - 1) / p.block_size;
+      const bool rows_ok = fresh >= 0 && fresh <= p.rows;
+      if (rows_ok && fresh <= len && blocks <= p.max_blocks_per_seq && held >= 0 &&
+          held <= p.max_blocks_per_seq) {
+        need = static_cast<int>(blocks);
+        v[1] = max(0, need - held);
+        v[2] = max(0, held - need);
+      } else if (first) {
+        record_error(kp.err, DSA_DEVERR_SEQ_LEN, s);
+      }
+      v[0] = rows_ok ? fresh : 0;
+    }
+    int ex[3], total[3];
+    scan3(v, ex, total, &sh);
+    if (s < n) {
+      sc.rows[s] = carry[0] + ex[0];
+      sc.want[s] = carry[1] + ex[1];
+      sc.back[s] = carry[2] + ex[2];
+      sc.held[s] = held;
+      sc.need[s] = need;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) carry[k] += total[k];
+  }
+  const int nrows = carry[0], nback = carry[2];
+  if (tid == 0) {
+    sc.rows[n] = carry[0];
+    sc.want[n] = carry[1];
+    sc.back[n] = carry[2];
+  }
+  int stack = p.free_in[0];
+  if (stack < 0 || stack > p.free_capacity) {
+    if (first && tid == 0) record_error(kp.err, DSA_DEVERR_FREE, -1);
+    stack = 0;
+  }
+  const int64_t avail = static_cast<int64_t>(stack) + nback;
+  __syncthreads();
+  // The largest amount wanted that the stack covers: what leaves it.
+  for (int s = tid; s < n; s += kThreads) {
+    const int upto = sc.want[s + 1];
+    if (upto <= avail) {
+      if (upto > sc.want[s]) atomicMax(&sh.taken, upto);
+    } else if (first && upto > sc.want[s]) {
+      record_error(kp.err, DSA_DEVERR_FREE, s);
+    }
+  }
+  // Every thread of this CTA has read held_in and free_in; the last CTA to get
+  // here writes their successors.
+  if (tid == 0) {
+    __threadfence();
+    sh.last = atomicAdd(&p.free_out[1], 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  const int taken = sh.taken;
+  const int kept = max(0, nback - taken);  // given-back blocks that stay on the stack
+  auto refused = [&](int s) { return sc.want[s + 1] > avail && sc.want[s + 1] > sc.want[s]; };
+  // The k-th block taken.
+  auto pop = [&](int k) -> int {
+    const int64_t at = avail - 1 - k;
+    if (at < stack) return p.free_blocks[at];
+    const int i = static_cast<int>(at - stack);
+    const int s = find(sc.back, n, i);
+    return p.block_table[static_cast<int64_t>(s) * p.bt_stride + sc.need[s] + (i - sc.back[s])];
+  };
+  // Entry b < need of request s's table after the call.
+  auto entry = [&](int s, int b) -> int {
+    if (b < sc.held[s]) return p.block_table[static_cast<int64_t>(s) * p.bt_stride + b];
+    return pop(sc.want[s] + (b - sc.held[s]));
+  };
+
+  if (sh.last) {
+    for (int s = tid; s < n; s += kThreads)
+      p.held_out[s] = sc.need[s] < 0 || refused(s) ? sc.held[s] : sc.need[s];
+    if (tid == 0) {
+      int64_t left = avail - taken;
+      if (left > p.free_capacity) {
+        record_error(kp.err, DSA_DEVERR_FREE, -1);
+        left = p.free_capacity;
+      }
+      p.free_out[0] = static_cast<int>(left);
+      p.free_out[1] = 0;
+    }
+  }
+  if (first) {
+    for (int s = tid; s <= n; s += kThreads) p.row_start[s] = sc.rows[s];
+    if (tid == 0 && nrows > p.rows) record_error(kp.err, DSA_DEVERR_ROWS, find(sc.rows, n, p.rows));
+  }
+
+  const int gwarp = blockIdx.x * kWarps + (tid >> 5), nwarps = gridDim.x * kWarps;
+  // The requests' own tables and the stack, one warp a request.
+  for (int s = gwarp; s < n; s += nwarps) {
+    const int held = sc.held[s], need = sc.need[s];
+    int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride;
+    if (need < 0) continue;  // an invalid request's `held` bounds nothing
+    const bool no = refused(s);
+    for (int b = held + lane; b < need; b += 32) row[b] = no ? -1 : pop(sc.want[s] + (b - held));
+    for (int b = need + lane; b < held; b += 32) {
+      const int i = sc.back[s] + (b - need);
+      if (i < kept && static_cast<int64_t>(stack) + i < p.free_capacity) p.free_blocks[stack + i] = row[b];
+    }
+  }
+  // The rows.
+  const int out_rows = min(nrows, p.rows);
+  for (int r = blockIdx.x * kThreads + tid; r < out_rows; r += gridDim.x * kThreads) {
+    const int s = find(sc.rows, n, r);
+    const bool live = sc.need[s] >= 0 && !refused(s);
+    int pos = 0;
+    int64_t slot = -1;
+    if (live) {
+      pos = p.seq_lens[s] - (sc.rows[s + 1] - r);
+      slot = static_cast<int64_t>(entry(s, pos / p.block_size)) * p.block_size + pos % p.block_size;
+    }
+    p.positions[r] = static_cast<uint32_t>(pos);
+    p.slots[r] = slot;
+    p.row_lens[r] = live ? pos + 1 : 0;
+    if (p.row_seq != nullptr) p.row_seq[r] = s;
+  }
+  if (p.row_table == nullptr) return;
+  for (int r = gwarp; r < out_rows; r += nwarps) {
+    const int s = find(sc.rows, n, r);
+    const int need = refused(s) ? 0 : max(0, sc.need[s]);
+    int32_t* row = p.row_table + static_cast<int64_t>(r) * p.row_bt_stride;
+    for (int b = lane; b < p.max_blocks_per_seq; b += 32) row[b] = b < need ? entry(s, b) : -1;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = 5 * (static_cast<size_t>(p.p.seqs) + 1) * sizeof(int);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t entries = static_cast<int64_t>(p.p.rows) *
+                          (p.p.row_table != nullptr ? p.p.max_blocks_per_seq : 16);
+  int64_t ctas = (entries + kEntriesPerCta - 1) / kEntriesPerCta;
+  if (ctas > num_sms) ctas = num_sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
+}
+
+}  // namespace dsa
