@@ -528,8 +528,8 @@ typedef struct dsa_seqs {
  *   q   [rows][heads][latent_dim] bf16       pool [nslots][latent_dim] FP8
  *   out [rows][heads][latent_dim] bf16       lse  [rows][heads] fp32 or NULL
  * latent_dim must be 512; heads a multiple of 16 up to 4096; rows <= 65535;
- * seqs <= DSA_PLAN_MAX_SEQS; nslots and block_size * max_blocks_per_seq below
- * 2^31 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and out 16-byte aligned; out
+ * seqs <= DSA_PLAN_MAX_SEQS; nslots below 2^31; block_size *
+ * max_blocks_per_seq at most 2^30 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and out 16-byte aligned; out
  * must not overlap q or the pool.  The workspace holds
  * dsa_chunk_workspace_bytes(rows, heads) bytes, 256-byte aligned
  * (DSA_ERR_WORKSPACE otherwise), needs no initial value, and belongs to the call

@@ -479,7 +479,9 @@ dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
 
 size_t dsa_chunk_workspace_bytes(int32_t rows, int32_t heads) {
   if (rows < 1 || rows > 65535 || heads < 16 || heads % 16 != 0 || heads > 4096) return 0;
-  return 256;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return 0;
+  return mla_chunk_workspace_bytes(dev->num_sms / 2);
 }
 
 dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint8_t* pool,
@@ -495,7 +497,7 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   if (latent_dim != DSA_LATENT_DIM || nslots > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   if (heads < 16 || heads % 16 != 0 || heads > 4096) return DSA_ERR_UNSUPPORTED;
   if (rows > 65535 || seqs->seqs > DSA_PLAN_MAX_SEQS) return DSA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq > INT32_MAX)
+  if (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq > (1LL << 30))
     return DSA_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
   const DeviceInfo* dev = device_info();
@@ -503,19 +505,35 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   if (workspace == nullptr || workspace_bytes < dsa_chunk_workspace_bytes(rows, heads) ||
       !aligned(workspace, 256))
     return DSA_ERR_WORKSPACE;
+  auto encode = encode_tiled();
+  if (encode == nullptr) return DSA_ERR_CUDA;
   ChunkParams p{};
   p.seqs = *seqs;
   p.q = q;
-  p.pool = pool;
   p.nslots = nslots;
   p.out = out;
   p.lse = lse_or_null;
   p.err = dev->err;
+  p.wait_ns = wait_limit_ns();
   p.rows = rows;
   p.heads = heads;
   p.kv_scale = kv_scale;
   p.sm_scale = sm_scale;
-  return launched(launch_mla_chunk(p, static_cast<cudaStream_t>(stream)));
+  p.pairs = dev->num_sms / 2;
+  p.box_rows = mla_chunk_box_rows(seqs->block_size);
+  // Latent pool [nslots][512] bytes; boxes of 128 bytes (the swizzle span) by
+  // box_rows rows, or one for gathers; rows outside the pool read as zero.
+  CUtensorMap map;
+  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(DSA_LATENT_DIM), static_cast<cuuint64_t>(nslots)};
+  cuuint64_t gstride[1] = {static_cast<cuuint64_t>(DSA_LATENT_DIM)};
+  cuuint32_t box[2] = {128, p.box_rows > 0 ? static_cast<cuuint32_t>(p.box_rows) : 1u};
+  cuuint32_t estride[2] = {1, 1};
+  CUresult cr = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pool), gdim,
+                       gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
+  return launched(launch_mla_chunk(p, map, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_get_error(int32_t* code_out, int32_t* row_out, int32_t* count_out, int32_t reset) {

@@ -193,16 +193,25 @@ cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t 
 struct ChunkParams {
   dsa_seqs seqs;
   const uint16_t* q;
-  const uint8_t* pool;
   int64_t nslots;
   uint16_t* out;
   float* lse;
+  float* part_o;     // workspace: [pairs][2][128][512] FP32 unnormalised output of a part
+  float* part_ml;    // workspace: [pairs][2][128] (max, sum)
   int* err;
+  uint64_t wait_ns;
   int32_t rows;
   int32_t heads;
+  int32_t pairs;     // pairs of CTAs that share the work
+  int32_t box_rows;  // pool rows of one copy; 0: four rows gathered
   float kv_scale;
   float sm_scale;
 };
-cudaError_t launch_mla_chunk(const ChunkParams& p, cudaStream_t stream);
+int mla_chunk_box_rows(int block_size);
+size_t mla_chunk_workspace_bytes(int pairs);
+// `map` describes the latent pool [nslots][512] bytes for 128-byte x box_rows
+// copies (1-row boxes where they are gathered).
+cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, void* workspace,
+                             cudaStream_t stream);
 
 }  // namespace dsa
