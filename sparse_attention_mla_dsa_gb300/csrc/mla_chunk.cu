@@ -38,39 +38,42 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 320;        // warp 0 copies, warp 1 MMA or forwards, warps 2-9 softmax
-constexpr int kSoftmaxThreads = 256;
-constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 640;        // warp 0 copies K, 1 issues MMAs, 2 copies V, 4-19 softmax
+constexpr int kSoftmaxWarp0 = 4;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kItem = 128;           // lines of an item (MMA M over the pair)
 constexpr int kLines = 64;           // lines of a CTA
 constexpr int kTile = 256;           // tokens of a tile
-constexpr int kChunks = 8;           // ring of 16 KB: a tile's K is four of them, its V four
+constexpr int kTok = 32;             // tokens of a softmax thread
+constexpr int kChunks = 8;           // 16 KB each: 0..3 a tile's K (128 dims), 4..7 its V (64 tokens)
 constexpr uint32_t kChunkBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [term][128-dim block][64 lines][128 B]
 constexpr uint32_t kPBytes = 32768;  // [term][128-token half][64 lines][128 B]
-constexpr uint32_t kRingOff = kQBytes + kPBytes;
-constexpr uint32_t kCtlOff = kRingOff + kChunks * kChunkBytes;
+constexpr uint32_t kChunkOff = kQBytes + kPBytes;
+constexpr uint32_t kCtlOff = kChunkOff + kChunks * kChunkBytes;
 constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
-constexpr int kMasks = 4;            // tiles whose token masks are kept
-constexpr float kPMaxLog2 = 8.75f;   // a weight 2^(z - m) stays below 2^8.75 < 448
-constexpr float kPResetLog2 = 8.0f;  // a new maximum maps to 2^8
+constexpr int kMasks = 8;            // tiles whose token masks are kept
+constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
+constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
 constexpr int kMergeLines = 8;       // lines of a merge CTA, a warp each
 
 struct __align__(16) Ctl {
-  uint64_t full[kChunks], empty[kChunks];
-  uint64_t peer_full[kChunks];       // leader: the other CTA's copies have landed
+  uint64_t full[kChunks];            // leader: the copies of both CTAs have landed
+  uint64_t empty[kChunks];
   uint64_t sfull[2], sfree[2], mask_ready[kMasks];
-  uint64_t pready, odone, qready, drain;
-  uint64_t mask[kMasks][4];          // a bit for each token of a tile: there is a latent
+  uint64_t pready, odone, qready, vseen, drain;
+  uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
+  uint32_t fills[kChunks], peer_fills[kChunks];  // fills begun of each chunk; the other CTA's
   uint32_t tmem_base;
   int abort_flag;
   float qexp[kLines];
-  float red[4][kLines];
+  float red[8][kLines];
 };
-constexpr uint32_t kSmemBytes = kCtlOff + sizeof(Ctl) + 1024;  // + alignment slack
-static_assert(kSmemBytes + 64 <= 227 * 1024, "shared memory budget (and find_place's own)");
+constexpr uint32_t kSmemBytes = kCtlOff + sizeof(Ctl);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
 // ------------------------------------------------------------------ schedule
 struct SeqInfo {
@@ -128,11 +131,11 @@ struct Place {
 
 // Finds tile `target(total)` of the call: every thread sums a run of requests,
 // the CTA scans the sums, and the thread whose run holds it walks to it.
-// `scratch`: kN + 2 int64 of shared memory.  Returns seq -1 past the end.
+// `scratch`: kN int64 and a Place of shared memory.  Returns seq -1 past the end.
 template <int kN, typename Target>
 __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Target target,
                                             int64_t* scratch, bool report) {
-  __shared__ Place found;
+  Place& found = *reinterpret_cast<Place*>(scratch + kN);
   const int tid = threadIdx.x, n = p.seqs.seqs, run = (n + kN - 1) / kN;
   const int s0 = min(n, tid * run), s1 = min(n, s0 + run);
   int64_t sum = 0;
@@ -349,20 +352,22 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const float* v) {
 }
 
 // ------------------------------------------------------------------ copies
-// A box of the latent pool: 128 bytes (column x) of the rows from y on.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y) {
+// A box of the latent pool, 128 bytes (column x) of the rows from y on, into
+// this CTA's shared memory; its bytes count on the leader's barrier `bar`.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 // Four rows of 128 bytes each.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
-                                            int32_t y0, int32_t y1, int32_t y2, int32_t y3) {
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                            const int32_t* y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
       : "memory");
 }
 
@@ -371,15 +376,33 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
   return out;
 }
-__device__ __forceinline__ uint16_t e5m2x2(float lo, float hi) {
-  uint16_t out;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
-  return out;
-}
 __device__ __forceinline__ float2 e4m3x2_decode(uint16_t codes) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(codes));
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
+}
+// Two softmax weights (fp16, already times 256) as E4M3 codes and the E5M2
+// codes of their remainders, which fp16 holds exactly.
+__device__ __forceinline__ void split_weights(uint32_t h2, uint16_t& hi, uint16_t& lo) {
+  uint32_t d2, r2;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h2));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d2) : "h"(hi));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r2) : "r"(h2), "r"(d2));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r2));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 // The bytes of w that are E4M3 NaN codes, zeroed.
 __device__ __forceinline__ uint32_t zero_nan4(uint32_t w) {
@@ -387,165 +410,172 @@ __device__ __forceinline__ uint32_t zero_nan4(uint32_t w) {
   return w & ~nan;
 }
 
-__device__ __forceinline__ void softmax_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+// Barriers of the eight softmax warps that have the same 32 lines (ids 1, 2).
+__device__ __forceinline__ void line_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kSoftmaxThreads / 2) : "memory");
 }
-__device__ __forceinline__ bool softmax_sync_or(bool pred) {
+__device__ __forceinline__ bool line_sync_or(int group, bool pred) {
   uint32_t out;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(out)
-      : "r"(pred ? 1u : 0u), "n"(kSoftmaxThreads)
+      : "r"(pred ? 1u : 0u), "r"(1 + group), "n"(kSoftmaxThreads / 2)
       : "memory");
   return out != 0;
 }
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 3, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
 
 // ------------------------------------------------------------------ roles
-// Copies of both operands of every tile of the range, in the order in which the
-// MMAs take them: K(0), then K(t+1), V(t) of each segment.  A token group (a box
-// of box_rows tokens inside one block, or four tokens gathered) belongs to one
-// lane, which looks its block up and issues its copies.
-__device__ __forceinline__ void produce(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* ring,
-                                        int lane, uint32_t rank, Walk w) {
-  const int bs = p.seqs.block_size;
-  const int h = p.box_rows;             // 8..64, or 0: gathers
-  uint32_t c = 0;                       // chunk counter
-  uint32_t tiles = 0;
-  bool ok = true;
-  // Rows of this lane's token groups: [tile parity][...]
-  int32_t at[2][8];
-  // chunk c's slot is free, and its bytes are expected
-  auto open = [&]() {
-    if (c >= kChunks) ok = warp_wait(ctl, &ctl->empty[c % kChunks], (c / kChunks - 1) & 1, lane, p);
-    if (ok && lane == 0) mbar_arrive_expect_tx(&ctl->full[c % kChunks], kChunkBytes);
-    __syncwarp();
-  };
-  Segment g;
-  while (ok && next_segment(p, w, g)) {
-    const int32_t* bt = p.seqs.block_table + static_cast<int64_t>(g.seq) * p.seqs.bt_stride;
-    const int end = item_end(p, g.q, g.item);
-    auto lookup = [&](int t, int32_t (&rows)[8]) {
-      const int t0 = t * kTile;
-      uint8_t* mask = reinterpret_cast<uint8_t*>(ctl->mask[tiles % kMasks]);
-      bool missing = false;
-      if (h > 0) {
-        const int tok = t0 + lane * h;
-        int32_t row = -1;
-        int there = 0;
-        if (lane * h < kTile) {
-          if (tok < end) {
-            const int64_t first = static_cast<int64_t>(bt[tok / bs]) * bs + tok % bs;
-            if (first >= 0 && first < p.nslots) {
-              row = static_cast<int32_t>(first);
-              there = static_cast<int>(min(static_cast<int64_t>(h), p.nslots - first));
-            }
-            missing = there < min(h, end - tok);
+// Where a tile's token groups (a box of box_rows tokens inside one block, or
+// four tokens gathered) are in the pool: a group is one lane's, which looks its
+// block up and issues its copies.  Absent tokens are at row nslots, past the end.
+struct Rows {
+  int32_t at[8];   // [0]: the box's first row; gathers: tokens 4l.. and 128 + 4l..
+};
+// kMask: also the tile's token mask, and the error of a missing block.
+template <bool kMask>
+__device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, int end, int t, int lane,
+                                       uint32_t rank, uint32_t* mask_words) {
+  const int bs = p.seqs.block_size, h = p.box_rows, t0 = t * kTile;
+  const int32_t* bt = p.seqs.block_table + static_cast<int64_t>(g.seq) * p.seqs.bt_stride;
+  uint8_t* mask = reinterpret_cast<uint8_t*>(mask_words);
+  const int32_t none = static_cast<int32_t>(p.nslots);
+  Rows r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.at[i] = none;
+  bool missing = false;
+  if (h > 0) {
+    const int tok = t0 + lane * h;
+    int there = 0;
+    if (lane * h < kTile) {
+      if (tok < end) {
+        const int64_t first = static_cast<int64_t>(bt[tok / bs]) * bs + tok % bs;
+        if (first >= 0 && first < p.nslots) {
+          r.at[0] = static_cast<int32_t>(first);
+          there = static_cast<int>(min(static_cast<int64_t>(h), p.nslots - first));
+        }
+        missing = there < min(h, end - tok);
+      }
+      if constexpr (kMask)
+        for (int i = 0; i < h; i += 8)
+          mask[(lane * h + i) >> 3] = there >= i + 8 ? 0xFF : there <= i ? 0 : static_cast<uint8_t>((1 << (there - i)) - 1);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = t0 + (k * 32 + lane) * 4 + i;
+        if (tok < end) {
+          const int64_t slot = static_cast<int64_t>(bt[tok / bs]) * bs + tok % bs;
+          if (slot >= 0 && slot < p.nslots) {
+            r.at[k * 4 + i] = static_cast<int32_t>(slot);
+            bits |= 1u << i;
+          } else {
+            missing = true;
           }
-          for (int i = 0; i < h; i += 8)
-            mask[(lane * h + i) >> 3] = there >= i + 8 ? 0xFF : there <= i ? 0 : static_cast<uint8_t>((1 << (there - i)) - 1);
-        }
-        rows[0] = row >= 0 ? row : static_cast<int32_t>(p.nslots);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t bits = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = t0 + (k * 32 + lane) * 4 + i;
-            int32_t row = static_cast<int32_t>(p.nslots);
-            if (tok < end) {
-              const int64_t slot = static_cast<int64_t>(bt[tok / bs]) * bs + tok % bs;
-              if (slot >= 0 && slot < p.nslots) {
-                row = static_cast<int32_t>(slot);
-                bits |= 1u << i;
-              } else {
-                missing = true;
-              }
-            }
-            rows[k * 4 + i] = row;
-          }
-          const uint32_t other = __shfl_down_sync(0xFFFFFFFFu, bits, 1);
-          if ((lane & 1) == 0) mask[(k * 32 + lane) >> 1] = static_cast<uint8_t>(bits | (other << 4));
         }
       }
-      if (missing && rank == 0) record_error(p.err, DSA_DEVERR_BLOCK, g.seq);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->mask_ready[tiles % kMasks]);
-      ++tiles;
-    };
-    auto load_k = [&](const int32_t (&rows)[8]) {
-      for (int d = 0; d < 4 && ok; ++d) {
-        open();
-        if (!ok) return;
-        const uint32_t dst = smem_u32(ring + (c % kChunks) * kChunkBytes);
-        uint64_t* bar = &ctl->full[c % kChunks];
-        if (h > 0) {
-          const int tok = lane * h - static_cast<int>(rank) * 128;
-          if (tok >= 0 && tok < 128) tma_box(dst + tok * 128, &map, bar, d * 128, rows[0]);
-        } else {
-          tma_gather4(dst + lane * 512, &map, bar, d * 128, rank ? rows[4] : rows[0], rank ? rows[5] : rows[1],
-                      rank ? rows[6] : rows[2], rank ? rows[7] : rows[3]);
-        }
-        ++c;
+      if constexpr (kMask) {
+        const uint32_t other = __shfl_down_sync(0xFFFFFFFFu, bits, 1);
+        if ((lane & 1) == 0) mask[(k * 32 + lane) >> 1] = static_cast<uint8_t>(bits | (other << 4));
       }
-    };
-    auto load_v = [&](const int32_t (&rows)[8]) {
-      const int x0 = static_cast<int>(rank) * 256;
-      for (int v = 0; v < 4 && ok; ++v) {
-        open();
-        if (!ok) return;
-        const uint32_t dst = smem_u32(ring + (c % kChunks) * kChunkBytes);
-        uint64_t* bar = &ctl->full[c % kChunks];
-        if (h > 0) {
-          const int tok = lane * h - v * 64;
-          if (tok >= 0 && tok < 64)
-            for (int n = 0; n < 2; ++n) tma_box(dst + n * 8192 + tok * 128, &map, bar, x0 + n * 128, rows[0]);
-        } else if ((lane >> 4) == (v & 1)) {
-          const bool up = v >= 2;
-          for (int n = 0; n < 2; ++n)
-            tma_gather4(dst + n * 8192 + (lane & 15) * 512, &map, bar, x0 + n * 128, up ? rows[4] : rows[0],
-                        up ? rows[5] : rows[1], up ? rows[6] : rows[2], up ? rows[7] : rows[3]);
-        }
-        ++c;
-      }
-    };
-    lookup(g.begin, at[0]);
-    load_k(at[0]);
-    for (int t = g.begin; t < g.end && ok; ++t) {
-      if (t + 1 < g.end) {
-        lookup(t + 1, at[1]);
-        load_k(at[1]);
-      }
-      if (ok) load_v(at[0]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) at[0][i] = at[1][i];
     }
   }
-  // Never leave with a copy in flight (already complete unless a wait gave up).
-  if (lane == 0)
-    for (uint32_t i = c > kChunks ? c - kChunks : 0; i < c; ++i)
-      mbar_wait(&ctl->full[i % kChunks], (i / kChunks) & 1, kDrainWaitNs);
+  if (kMask && missing && rank == 0) record_error(p.err, DSA_DEVERR_BLOCK, g.seq);
+  return r;
+}
+
+// Warps 0 and 2.  kV false: this CTA's 128 tokens of every tile's K, in chunks of
+// 128 dims.  kV true: its 256 dims of every tile's V, in chunks of 64 tokens.
+// Each has its own four chunks, taken again as soon as the tile before is done
+// with them (one warp alone fills a chunk: a barrier's parity says nothing to a
+// warp that may be two fills behind).
+template <bool kV>
+__device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* chunks,
+                                     int lane, uint32_t rank, Walk w) {
+  constexpr int kFirst = kV ? 4 : 0;
+  uint32_t looked = 0, tiles = 0;
+  Segment g;
+  while (next_segment(p, w, g)) {
+    const int end = item_end(p, g.q, g.item);
+    // K: also leaves the tile's mask and brings its latents into L2.
+    auto look = [&](int t) {
+      const Rows r = lookup<!kV>(p, g, end, t, lane, rank, kV ? nullptr : ctl->mask[looked % kMasks]);
+      if constexpr (!kV) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->mask_ready[looked % kMasks]);
+        ++looked;
+        const int tok = lane * p.box_rows - static_cast<int>(rank) * 128;
+        if (p.box_rows > 0 && tok >= 0 && tok < 128 && r.at[0] < p.nslots)
+          for (int d = 0; d < 4; ++d) tma_prefetch_l2_2d(&map, d * 128, r.at[0]);
+      }
+      return r;
+    };
+    Rows next = look(g.begin);
+    for (int t = g.begin; t < g.end; ++t, ++tiles) {
+      const Rows r = next;
+      if (t + 1 < g.end) next = look(t + 1);   // before the waits of this tile
+      for (int i = 0; i < 4; ++i) {
+        const int slot = kFirst + i;
+        if (tiles > 0 && !warp_wait(ctl, &ctl->empty[slot], (tiles - 1) & 1, lane, p)) return;
+        if (lane == 0) {
+          ctl->fills[slot] = tiles + 1;
+          // the leader expects the bytes of both CTAs
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 2 * kChunkBytes);
+        }
+        __syncwarp();
+        const uint32_t dst = smem_u32(chunks + slot * kChunkBytes), bar = map_to(&ctl->full[slot], 0);
+        if constexpr (!kV) {
+          if (p.box_rows > 0) {
+            const int tok = lane * p.box_rows - static_cast<int>(rank) * 128;
+            if (tok >= 0 && tok < 128) tma_box(dst + tok * 128, &map, bar, i * 128, r.at[0]);
+          } else {
+            int32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = rank ? r.at[4 + k] : r.at[k];
+            tma_gather4(dst + lane * 512, &map, bar, i * 128, y);
+          }
+        } else {
+          const int x0 = static_cast<int>(rank) * 256;
+          if (p.box_rows > 0) {
+            const int tok = lane * p.box_rows - i * 64;
+            if (tok >= 0 && tok < 64)
+              for (int b = 0; b < 2; ++b) tma_box(dst + b * 8192 + tok * 128, &map, bar, x0 + b * 128, r.at[0]);
+          } else if ((lane >> 4) == (i & 1)) {
+            int32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = i >= 2 ? r.at[4 + k] : r.at[k];
+            for (int b = 0; b < 2; ++b)
+              tma_gather4(dst + b * 8192 + (lane & 15) * 512, &map, bar, x0 + b * 128, y);
+          }
+        }
+      }
+    }
+  }
 }
 
 // Leader, one thread: the MMAs of both CTAs.
-__device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint32_t q0, uint32_t p0, uint32_t ring0,
+__device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint32_t q0, uint32_t p0, uint32_t chunk0,
                                            uint32_t tmem, Walk w) {
-  uint32_t c = 0, ns = 0, no = 0, nq = 0;   // chunks, S and O tiles issued, segments
+  uint32_t ns = 0, no = 0, nq = 0;   // S and O tiles issued, segments
   bool ok = true;
-  auto chunk = [&]() {
-    const uint32_t s = c % kChunks, par = (c / kChunks) & 1;
-    ok = ok && wait_one(ctl, &ctl->full[s], par, p) && wait_one(ctl, &ctl->peer_full[s], par, p);
+  auto chunk = [&](int slot, uint32_t tile) {
+    ok = ok && wait_one(ctl, &ctl->full[slot], tile & 1, p);
     tc_fence_after();
-    return ring0 + s * kChunkBytes;
+    return chunk0 + slot * kChunkBytes;
   };
   auto issue_s = [&]() {
     if (ns >= 2) ok = ok && wait_one(ctl, &ctl->sfree[ns & 1], ((ns - 2) >> 1) & 1, p);
     const uint32_t d = tmem + kSCol + (ns & 1) * 128;
     for (int b = 0; b < 4 && ok; ++b) {
-      const uint32_t k0 = chunk();
+      const uint32_t k0 = chunk(b, ns);
       if (!ok) return;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
@@ -553,8 +583,7 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
         for (int term = 0; term < 2; ++term)
           mma_pair(d, umma_desc_sw128_kmajor(q0 + (term * 4 + b) * 8192 + kk * 32),
                    umma_desc_sw128_kmajor(k0 + kk * 32), idesc_f8(false, false), (b | kk | term) != 0 ? 1u : 0u);
-      commit_pair(&ctl->empty[c % kChunks]);
-      ++c;
+      commit_pair(&ctl->empty[b]);
     }
     commit_pair(&ctl->sfull[ns & 1]);
     ++ns;
@@ -562,7 +591,7 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
   auto issue_o = [&](bool first) {
     ok = ok && wait_one(ctl, &ctl->pready, no & 1, p);
     for (int v = 0; v < 4 && ok; ++v) {
-      const uint32_t v0 = chunk();
+      const uint32_t v0 = chunk(4 + v, no);
       if (!ok) return;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
@@ -574,8 +603,7 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
                      umma_desc_sw128_kmajor(p0 + term * 16384 + (v >> 1) * 8192 + (v & 1) * 64 + kk * 32),
                      desc_mnmajor(v0 + n * 8192 + kk * 4096), idesc_f8(term != 0, true),
                      first && (v | kk | term) == 0 ? 0u : 1u);
-      commit_pair(&ctl->empty[c % kChunks]);
-      ++c;
+      commit_pair(&ctl->empty[4 + v]);
     }
     commit_pair(&ctl->odone);
     ++no;
@@ -597,18 +625,10 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
   mbar_wait(&ctl->drain, 0, kDrainWaitNs);
 }
 
-// The other CTA, one thread: tells the leader that its copies have landed.
-__device__ __forceinline__ void forward(const ChunkParams& p, Ctl* ctl, int64_t tiles) {
-  const int64_t n = tiles * kChunks;
-  for (int64_t c = 0; c < n; ++c) {
-    if (!wait_one(ctl, &ctl->full[c % kChunks], (c / kChunks) & 1, p)) return;
-    arrive_at(map_to(&ctl->peer_full[c % kChunks], 0));
-  }
-}
-
 // Q of the segment's 64 lines of this CTA: q * 2^s = hi + lo, s a power of two a
-// line that puts its largest |q| in [128, 256).  Warp w converts lines w, w+8,
-// ...; lane l dims 16l..16l+15.  Lines past the request's last are zero.
+// line that puts its largest |q| in [128, 256), negated where the logits' scale
+// is negative (so that it never is in the softmax).  Warp w converts lines w, w +
+// 16, ...; lane l dims 16l..16l+15.  Lines past the request's last are zero.
 __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_t* qop, const Segment& g, int line0,
                                           int sw, int lane) {
   constexpr int kPer = kLines / kSoftmaxWarps;
@@ -624,6 +644,7 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
       qb[j] = ld_dep_u4(src + 1);
     }
   }
+  const float sz = p.sm_scale * p.kv_scale * 1.4426950408889634f;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = sw + j * kSoftmaxWarps;
@@ -647,10 +668,14 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
     int e = 0;
     if (finite && amax > 0.0f) frexpf(amax, &e);  // amax < 2^e
     const int sh = max(-126, min(126, 8 - e));
-    const float scale = ldexpf(1.0f, sh);
-    // A line with an infinity or a NaN gives NaN logits, as its formula does.
-    if (lane == 0)
-      ctl->qexp[i] = finite ? p.sm_scale * p.kv_scale * 1.4426950408889634f * ldexpf(1.0f, -sh) : NAN;
+    const float scale = copysignf(ldexpf(1.0f, sh), sz);
+    if (lane == 0) {
+      // Never 0, which times a masked -inf would be NaN.  A line with an
+      // infinity or a NaN gives NaN logits, as its formula does.
+      float f = fabsf(sz) * ldexpf(1.0f, -sh);
+      if (f < 1e-37f) f = 1e-37f;
+      ctl->qexp[i] = finite ? f : NAN;
+    }
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -673,27 +698,33 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
 
 // Softmax, and everything else that is not a copy or an MMA.  A thread has one
 // line: lane i and lane 64 + i of tensor memory hold its logits of the tile's
-// first and second 128 tokens (its output's first and second 256 dims), and two
-// warps share a quarter of the lanes, so four threads have a line.
-__device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t* qop, uint8_t* pop, uint8_t* ring,
+// first and second 128 tokens (its output's first and second 256 dims), and four
+// warps share a quarter of the lanes, so eight threads have a line.
+__device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t* qop, uint8_t* pop, uint8_t* chunks,
                                         uint32_t tmem, int warp, int lane, uint32_t rank, int pair, Walk w) {
-  const int sw = warp - 2, quarter = warp & 3, ch = sw >> 2;
-  const int half = quarter >> 1;
-  const int i = (quarter & 1) * 32 + lane;              // line of this CTA
-  const int part = half * 2 + ch;
+  const int sw = warp - kSoftmaxWarp0, quarter = warp & 3, sub = sw >> 2;
+  const int half = quarter >> 1, group = quarter & 1;
+  const int i = group * 32 + lane;                      // line of this CTA
+  const int part = half * 4 + sub;
   const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-  const uint32_t ocol = tmem + lane_base + ch * 128;    // this thread's output columns
+  const uint32_t ocol = tmem + lane_base + sub * 64;    // this thread's 64 output columns
   const uint32_t sfree0 = map_to(&ctl->sfree[0], 0), sfree1 = map_to(&ctl->sfree[1], 0);
   const uint32_t pready = map_to(&ctl->pready, 0), qready = map_to(&ctl->qready, 0);
-  uint32_t ns = 0, c = 0;                               // tiles done, chunks before this tile's V
+  const uint32_t vseen1 = map_to(&ctl->vseen, 1);
+  uint32_t ns = 0, nv = 0;                              // tiles done, masked tiles
   bool ok = true;
-  Segment g;
-  while (next_segment(p, w, g)) {
-    const int line0 = g.item * kItem + static_cast<int>(rank) * kLines;
-    convert_q(p, ctl, qop, g, line0, sw, lane);
+  Segment g, next;
+  bool more = next_segment(p, w, next);
+  if (more) {
+    convert_q(p, ctl, qop, next, next.item * kItem + static_cast<int>(rank) * kLines, sw, lane);
     fence_proxy_async_smem();
-    softmax_sync();                                     // qexp
+    __syncwarp();
     if (lane == 0) arrive_at(qready);
+    softmax_sync();                                     // qexp
+  }
+  while (more) {
+    g = next;
+    const int line0 = g.item * kItem + static_cast<int>(rank) * kLines;
     const float scale = ctl->qexp[i];
     const int last = g.q.lines - 1;
     const int sees = g.q.ctx + min(line0 + i, last) / p.heads + 1;                 // tokens of this line
@@ -701,46 +732,45 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
     float m = -INFINITY, l = 0.0f;
     for (int t = g.begin; t < g.end; ++t, ++ns) {
       const int b = ns & 1;
-      const int tok0 = t * kTile + half * 128 + ch * 64;
-      // chunks of this segment before V(t): K(begin) .. K(min(t + 1, end - 1)), V(begin) .. V(t - 1)
-      const uint32_t vchunk = c + 4 * (min(t + 1, g.end - 1) - g.begin + 1) + 4 * (t - g.begin);
-      float z[64];
+      const int tok0 = t * kTile + half * 128 + sub * kTok;
+      float z[kTok];
       if (ok) ok = warp_wait(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
       if (ok) ok = warp_wait(ctl, &ctl->mask_ready[ns % kMasks], (ns / kMasks) & 1, lane, p);
       bool exceed = false;
       float mx = -INFINITY;
       if (ok) {
         tc_fence_after();
-        tmem_load32(tmem + lane_base + kSCol + b * 128 + ch * 64, z);
-        tmem_load32(tmem + lane_base + kSCol + b * 128 + ch * 64 + 32, z + 32);
-        const uint64_t there = ctl->mask[ns % kMasks][part];
+        tmem_load32(tmem + lane_base + kSCol + b * 128 + sub * kTok, z);
+        const uint32_t there = ctl->mask[ns % kMasks][part];
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(b ? sfree1 : sfree0);
-        const int visible = sees - tok0;                // of this thread's 64 tokens
-        if (visible >= 64 && there == ~0ull) {
+        const int visible = sees - tok0;                // of this thread's tokens
+        const uint32_t seen = there & (visible >= kTok ? ~0u : visible <= 0 ? 0u : (1u << visible) - 1u);
+        if (seen != ~0u) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) z[k] *= scale;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) z[k] = (k < visible && ((there >> k) & 1)) ? z[k] * scale : -INFINITY;
+          for (int k = 0; k < kTok; ++k) z[k] = (seen >> k) & 1u ? z[k] : -INFINITY;
         }
-        float mk[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mk[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-        for (int k = 0; k < 64; ++k) mk[k & 3] = fmaxf(mk[k & 3], z[k]);
-        mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
+        for (int k = 4; k < kTok; k += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mk[u] = fmaxf(fmaxf(mk[u], z[k + u]), k + 4 + u < kTok ? z[k + 4 + u] : -INFINITY);
+        mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * scale;
+        if (seen == 0) mx = -INFINITY;                  // (NaN where the scale is)
         exceed = mx > m + kPMaxLog2;
       }
       bool o_idle = ns == 0;                            // the MMAs that read P and add to O are done
-      if (softmax_sync_or(exceed)) {
+      if (line_sync_or(group, exceed)) {
         ctl->red[part][i] = mx;
-        softmax_sync();
-        const float tm = fmaxf(fmaxf(ctl->red[0][i], ctl->red[1][i]), fmaxf(ctl->red[2][i], ctl->red[3][i]));
+        line_sync(group);
+        float tm = ctl->red[0][i];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) tm = fmaxf(tm, ctl->red[k][i]);
         float alpha = 1.0f;
         if (tm > m + kPMaxLog2) {
-          const float mn = tm - kPResetLog2;
-          alpha = exp2f(m - mn);                        // 0 while nothing was added
-          m = mn;
+          alpha = ex2(m - tm);                          // 0 while nothing was added
+          m = tm;
           l *= alpha;
         }
         if (ok && t > g.begin && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
@@ -749,7 +779,7 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < 128; k += 32) {
+            for (int k = 0; k < 64; k += 32) {
               float v[32];
               tmem_load32(ocol + k, v);
 #pragma unroll
@@ -760,56 +790,65 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
         }
-        softmax_sync();                                 // red[] has been read
+        line_sync(group);                               // red[] has been read
       }
-      uint32_t hw[16], lw[16];
+      uint32_t hw[kTok / 4], lw[kTok / 4];
       if (ok) {
-        const float base = m == -INFINITY ? 0.0f : m;   // nothing seen yet: every p is 0
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};        // of the tile first: a long tail of small weights
+        const float base = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every weight is 0
+        float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};   // of the tile first: a long tail of small weights
 #pragma unroll                                          // would be rounded away against a large running sum
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < kTok / 4; ++k) {
           uint16_t hc[2], lc[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float a0 = exp2f(z[4 * k + 2 * u] - base), a1 = exp2f(z[4 * k + 2 * u + 1] - base);
-            hc[u] = e4m3x2(a0, a1);
-            const float2 hv = e4m3x2_decode(hc[u]);
-            lc[u] = e5m2x2(a0 - hv.x, a1 - hv.y);
-            sum[2 * u] += a0;
-            sum[2 * u + 1] += a1;
+            const float2 x = fma2(make_float2(z[4 * k + 2 * u], z[4 * k + 2 * u + 1]), make_float2(scale, scale),
+                                  make_float2(base, base));
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[u].x += e.x;
+            sum[u].y += e.y;
+            uint32_t h2;
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(e.y), "f"(e.x));
+            const __half2 s2 = __hmul2(*reinterpret_cast<const __half2*>(&h2), __float2half2_rn(kPScale));
+            split_weights(*reinterpret_cast<const uint32_t*>(&s2), hc[u], lc[u]);
           }
           hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
           lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (!o_idle) ok = warp_wait(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
       }
       if (ok) {
         uint8_t* row = pop + half * 8192 + i * 128;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = ((ch * 4 + k) ^ (i & 7)) * 16;
+        for (int k = 0; k < 2; ++k) {
+          const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
           *reinterpret_cast<uint4*>(row + at) = make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]);
           *reinterpret_cast<uint4*>(row + 16384 + at) =
               make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
         }
-        // Tokens that a line of the item does not see have weight 0 there, which
-        // a NaN latent would turn into NaN: such codes are zeroed (a line that
-        // sees one has a NaN weight, so its output is NaN all the same).
-        const int from = all_see - t * kTile;
-        if (from < kTile) {
-          for (int v = max(0, from) / 64; v < 4 && ok; ++v) {
-            const uint32_t slot = (vchunk + v) % kChunks;
-            ok = warp_wait(ctl, &ctl->full[slot], ((vchunk + v) / kChunks) & 1, lane, p);
-            if (!ok) break;
-            const int r0 = max(0, from - v * 64), units = (64 - r0) * 16;  // rows r0..63 x 2 blocks x 8
-            uint4* base = reinterpret_cast<uint4*>(ring + slot * kChunkBytes);
-            for (int u = sw * 32 + lane; u < units; u += kSoftmaxThreads) {
-              uint4* q4 = base + (u & 1) * 512 + r0 * 8 + (u >> 1);
-              const uint4 x = *q4;
-              const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
-              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
-            }
+      }
+      // Tokens that a line of the item does not see have weight 0 there, which a
+      // NaN latent would turn into NaN: such codes are zeroed in V (a line that
+      // sees one has a NaN weight, so its output is NaN all the same).  The
+      // leader, whose barriers say when V has landed in both CTAs, tells the other.
+      const int from = max(0, all_see - t * kTile);
+      if (from < kTile) {
+        if (rank == 0) {
+          for (int v = 0; v < 4 && ok; ++v)
+            ok = warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
+          if (ok && sw == 0 && lane == 0) arrive_at(vseen1);
+        } else if (ok) {
+          ok = warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
+        }
+        ++nv;
+        for (int v = from / 64; v < 4 && ok; ++v) {
+          const int r0 = max(0, from - v * 64), units = (64 - r0) * 16;  // rows r0..63 x 2 blocks x 8
+          uint4* base = reinterpret_cast<uint4*>(chunks + (4 + v) * kChunkBytes);
+          for (int u = sw * 32 + lane; u < units; u += kSoftmaxThreads) {
+            uint4* q4 = base + (u & 1) * 512 + r0 * 8 + (u >> 1);
+            const uint4 x = *q4;
+            const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
+            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
           }
         }
       }
@@ -820,25 +859,35 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
         if (lane == 0) arrive_at(pready);
       }
     }
-    c += 8 * (g.end - g.begin);
 
-    // The line's sum in a fixed order, then its output.
+    // Every S of the segment is complete: the next one's Q takes its place
+    // while the last P V runs, and its first S runs beside the epilogue.
+    more = next_segment(p, w, next);
     ctl->red[part][i] = l;
-    softmax_sync();
-    const float lt = (ctl->red[0][i] + ctl->red[1][i]) + (ctl->red[2][i] + ctl->red[3][i]);
-    softmax_sync();
+    softmax_sync();                                     // l; qexp has been read
+    if (more) {
+      convert_q(p, ctl, qop, next, next.item * kItem + static_cast<int>(rank) * kLines, sw, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_at(qready);
+    }
+    // The line's sum in a fixed order, then its output.
+    float lt = ctl->red[0][i];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) lt += ctl->red[k][i];
+    softmax_sync();                                     // red[] has been read; the next qexp is there
     if (ok) ok = warp_wait(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
     if (!ok) continue;
     tc_fence_after();
     const bool whole = g.begin == 0 && g.end == g.tiles;
     const int line = line0 + i;
     const int64_t gline = static_cast<int64_t>(g.q.row0) * p.heads + line;
-    const int d0 = half * 256 + ch * 128;
+    const int d0 = half * 256 + sub * 64;
     // slot 0: the item began in an earlier range, 1: it goes on in a later one
     const int64_t pline = (static_cast<int64_t>(pair) * 2 + (g.begin > 0 ? 0 : 1)) * kItem + rank * kLines + i;
-    const float inv = m != -INFINITY ? p.kv_scale / lt : (lt != lt ? lt : 0.0f);
+    const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
 #pragma unroll 1
-    for (int k = 0; k < 128; k += 32) {
+    for (int k = 0; k < 64; k += 32) {
       float v[32];
       tmem_load32(ocol + k, v);
       if (line <= last) {
@@ -871,11 +920,11 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_chunk_kernel(const __grid_constant__ CUtensorMap map, const ChunkParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;           // (no static shared memory: it begins on a 1024-byte boundary)
   uint8_t* qop = smem;
   uint8_t* pop = smem + kQBytes;
-  uint8_t* ring = smem + kRingOff;
+  uint8_t* chunks = smem + kChunkOff;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + kCtlOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cta_rank();
@@ -885,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int k = 0; k < kChunks; ++k) {
       mbar_init(&ctl->full[k], 1);
       mbar_init(&ctl->empty[k], 1);
-      mbar_init(&ctl->peer_full[k], 1);
+      ctl->fills[k] = 0;
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(&ctl->sfull[k], 1);
@@ -895,6 +944,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->pready, 2 * kSoftmaxWarps);
     mbar_init(&ctl->qready, 2 * kSoftmaxWarps);
     mbar_init(&ctl->odone, 1);
+    mbar_init(&ctl->vseen, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -923,20 +973,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    produce(map, p, ctl, ring, lane, rank, w);
+    copy<false>(map, p, ctl, chunks, lane, rank, w);
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (rank == 0) issue_mmas(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(ring), tmem, w);
-      else forward(p, ctl, w.left);
-    }
+    if (lane == 0 && rank == 0) issue_mmas(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
     __syncwarp();
-  } else {
-    softmax(p, ctl, qop, pop, ring, tmem, warp, lane, rank, pair, w);
+  } else if (warp == 2) {
+    copy<true>(map, p, ctl, chunks, lane, rank, w);
+  } else if (warp >= kSoftmaxWarp0) {
+    softmax(p, ctl, qop, pop, chunks, tmem, warp, lane, rank, pair, w);
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();     // neither CTA leaves while the other may still signal it or its MMAs run
+  if (rank == 1 && tid < kChunks)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "r"(ctl->fills[tid]) : "memory");
+  cluster_sync();
+  // No CTA leaves with a copy of either in flight.  All are complete unless a
+  // wait gave up; then one CTA may have begun a slot's copies that the other
+  // has not, and the bytes that will not come are made up for.
+  if (rank == 0 && tid < kChunks) {
+    const uint32_t mine = ctl->fills[tid], other = ctl->peer_fills[tid], n = max(mine, other);
+    if (mine > other)
+      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&ctl->full[tid])), "r"(kChunkBytes) : "memory");
+    else if (other > mine)
+      mbar_arrive_expect_tx(&ctl->full[tid], kChunkBytes);
+    if (n > 0) mbar_wait(&ctl->full[tid], (n - 1) & 1, kDrainWaitNs);
+  }
+  __syncthreads();
+  cluster_sync();     // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -947,7 +1011,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // that the boundary between ranges x and x + 1 falls into, if that is the
 // item's first; block y: eight of its lines, a warp each.
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
-  __shared__ int64_t scratch[kMergeThreads];
+  __shared__ int64_t scratch[kMergeThreads + sizeof(Place) / 8];
   const int boundary = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_launch();
   const Place at = find_place<kMergeThreads>(p, p.pairs, [&](int64_t per) { return per * boundary; }, scratch, false);
@@ -981,7 +1045,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const Ch
 #pragma unroll 2
     for (int u = 0; u < parts; ++u) {
       const float2 x = ld_dep_f2(ml + pline(u));
-      const float wgt = exp2f(x.x - m);
+      const float wgt = ex2(x.x - m);
       const float4* src = reinterpret_cast<const float4*>(p.part_o + pline(u) * 512) + lane;
       l += wgt * x.y;
 #pragma unroll
@@ -997,7 +1061,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const Ch
       }
     }
   }
-  const float inv = nan ? NAN : (m != -INFINITY ? p.kv_scale / l : 0.0f);
+  const float inv = nan ? NAN : (m != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
   const int64_t gline = static_cast<int64_t>(q.row0) * p.heads + line;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
