@@ -38,7 +38,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 640;        // warp 0 copies K, 1 issues MMAs, 2 copies V, 4-19 softmax
+constexpr int kThreads = 640;        // warps 0, 2 copy K, V; 1, 3 issue S, O; 4-19 softmax
 constexpr int kSoftmaxWarp0 = 4;
 constexpr int kSoftmaxWarps = 16;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
@@ -64,7 +64,7 @@ struct __align__(16) Ctl {
   uint64_t full[kChunks];            // leader: the copies of both CTAs have landed
   uint64_t empty[kChunks];
   uint64_t sfull[2], sfree[2], mask_ready[kMasks];
-  uint64_t pready, odone, qready, vseen, drain;
+  uint64_t pready, odone, qready, vseen, drain[2];
   uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
   uint32_t fills[kChunks], peer_fills[kChunks];  // fills begun of each chunk; the other CTA's
   uint32_t tmem_base;
@@ -249,20 +249,18 @@ __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// Arrival on a barrier of either CTA.  The data it announces is read by MMAs
+// (written for them by fence.proxy.async) or is none, so the order within this
+// CTA is enough; a release to the cluster costs ~1,700 clocks of the softmax's
+// 4,200 a tile, and an acquire from it ~200 (it invalidates the L1).
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same for data that threads of the other CTA read.
+__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(32u)
-      : "memory");
-  return ok != 0;
-}
+__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ bool aborted(Ctl* c) {
   return *reinterpret_cast<volatile int*>(&c->abort_flag) != 0;
 }
@@ -272,19 +270,22 @@ __device__ __forceinline__ void set_abort(Ctl* c) {
     asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(map_to(&c->abort_flag, r)), "r"(1) : "memory");
 }
 // Bounded wait of one thread; a timeout is recorded and marks the pair.
-__device__ __forceinline__ bool wait_one(Ctl* c, uint64_t* bar, uint32_t parity, const ChunkParams& p) {
-  if (p.wait_ns >= kShortWaitNs && try_wait_cluster(bar, parity)) return true;
+__device__ __noinline__ bool wait_polls(Ctl* c, uint64_t* bar, uint32_t parity, int* err, uint64_t limit_ns) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1; i < (1u << 30); ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if ((i & 15u) == 0 || p.wait_ns < kShortWaitNs) {
+    if (mbar_try_wait_hint(bar, parity, limit_ns < kShortWaitNs ? 32 : kSuspendHintNs)) return true;
+    if ((i & 15u) == 0 || limit_ns < kShortWaitNs) {
       if (aborted(c)) return false;
-      if (global_ns() - t0 > p.wait_ns) break;
+      if (global_ns() - t0 > limit_ns) break;
     }
   }
-  record_error(p.err, DSA_DEVERR_TIMEOUT, -1);
+  record_error(err, DSA_DEVERR_TIMEOUT, -1);
   set_abort(c);
   return false;
+}
+__device__ __forceinline__ bool wait_one(Ctl* c, uint64_t* bar, uint32_t parity, const ChunkParams& p) {
+  if (p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
+  return wait_polls(c, bar, parity, p.err, p.wait_ns);
 }
 __device__ __forceinline__ bool warp_wait(Ctl* c, uint64_t* bar, uint32_t parity, int lane, const ChunkParams& p) {
   int ok = 1;
@@ -293,23 +294,29 @@ __device__ __forceinline__ bool warp_wait(Ctl* c, uint64_t* bar, uint32_t parity
 }
 
 // ------------------------------------------------------------------ tensor core
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr) {
-  // 128 contiguous bytes of MN per K row, K rows 128 B apart, the next 8 of
-  // them 1024 B on; a CTA's share of MN is one 128-byte span.
-  return umma_desc_sw128_kmajor(saddr);
-}
 // kind::f8f6f4, F32 accumulate, M = 128 over the pair, N = 256; A E4M3 or E5M2
 // K-major, B E4M3.
 __host__ __device__ constexpr uint32_t idesc_f8(bool a_e5m2, bool b_mn_major) {
   return (1u << 4) | (a_e5m2 ? (1u << 7) : 0u) | (b_mn_major ? (1u << 16) : 0u) | ((256u >> 3) << 17) |
          ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Low words of the operands' descriptors (umma_desc_sw128_kmajor; the same
+// serves V, 128 contiguous bytes of MN per K row with the next 8 rows 1024 B on),
+// which alone differ between MMAs: by the offset in 16-byte units.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) {
+  return static_cast<uint32_t>(umma_desc_sw128_kmajor(saddr));
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// An MMA takes 64 clocks, so the instructions that lead to it count: an add for
+// each operand, nothing else.
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(acc), "n"(kDescHigh), "n"(kIdesc)
       : "memory");
 }
 // Arrives on `bar` of both CTAs once every MMA issued so far is complete.
@@ -561,68 +568,56 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
   }
 }
 
-// Leader, one thread: the MMAs of both CTAs.
+// Leader, one thread of warps 1 and 3: the MMAs of both CTAs.  kPv false: S = Q K^T
+// of every tile; kPv true: O += P V.  A thread of its own for each, on its own
+// scheduler: beside four softmax warps one alone issues an MMA in 94 to 128
+// clocks, where the tensor cores take 64.
+template <bool kPv>
 __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint32_t q0, uint32_t p0, uint32_t chunk0,
                                            uint32_t tmem, Walk w) {
-  uint32_t ns = 0, no = 0, nq = 0;   // S and O tiles issued, segments
+  constexpr int kFirst = kPv ? 4 : 0;
+  const uint32_t a0 = desc_low(kPv ? p0 : q0), b0 = desc_low(chunk0 + kFirst * kChunkBytes);
+  uint32_t n = 0, nq = 0;            // tiles issued, segments
   bool ok = true;
-  auto chunk = [&](int slot, uint32_t tile) {
-    ok = ok && wait_one(ctl, &ctl->full[slot], tile & 1, p);
-    tc_fence_after();
-    return chunk0 + slot * kChunkBytes;
-  };
-  auto issue_s = [&]() {
-    if (ns >= 2) ok = ok && wait_one(ctl, &ctl->sfree[ns & 1], ((ns - 2) >> 1) & 1, p);
-    const uint32_t d = tmem + kSCol + (ns & 1) * 128;
-    for (int b = 0; b < 4 && ok; ++b) {
-      const uint32_t k0 = chunk(b, ns);
-      if (!ok) return;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-          mma_pair(d, umma_desc_sw128_kmajor(q0 + (term * 4 + b) * 8192 + kk * 32),
-                   umma_desc_sw128_kmajor(k0 + kk * 32), idesc_f8(false, false), (b | kk | term) != 0 ? 1u : 0u);
-      commit_pair(&ctl->empty[b]);
-    }
-    commit_pair(&ctl->sfull[ns & 1]);
-    ++ns;
-  };
-  auto issue_o = [&](bool first) {
-    ok = ok && wait_one(ctl, &ctl->pready, no & 1, p);
-    for (int v = 0; v < 4 && ok; ++v) {
-      const uint32_t v0 = chunk(4 + v, no);
-      if (!ok) return;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            mma_pair(tmem + n * 128,
-                     umma_desc_sw128_kmajor(p0 + term * 16384 + (v >> 1) * 8192 + (v & 1) * 64 + kk * 32),
-                     desc_mnmajor(v0 + n * 8192 + kk * 4096), idesc_f8(term != 0, true),
-                     first && (v | kk | term) == 0 ? 0u : 1u);
-      commit_pair(&ctl->empty[4 + v]);
-    }
-    commit_pair(&ctl->odone);
-    ++no;
-  };
   Segment g;
   while (ok && next_segment(p, w, g)) {
-    ok = wait_one(ctl, &ctl->qready, nq & 1, p);
+    if (!kPv) ok = wait_one(ctl, &ctl->qready, nq & 1, p);
     ++nq;
-    if (ok) issue_s();
-    for (int t = g.begin; t < g.end && ok; ++t) {
-      if (t + 1 < g.end) issue_s();
-      if (ok) issue_o(t == g.begin);
+    for (int t = g.begin; t < g.end && ok; ++t, ++n) {
+      const uint32_t par = n & 1;
+      if (kPv) ok = wait_one(ctl, &ctl->pready, par, p);
+      else if (n >= 2) ok = wait_one(ctl, &ctl->sfree[par], ((n - 2) >> 1) & 1, p);
+      const uint32_t s = tmem + kSCol + par * 128;
+      const uint32_t add = t == g.begin ? 0u : 1u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ok = ok && wait_one(ctl, &ctl->full[kFirst + i], par, p);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            if constexpr (!kPv) {    // 32 dims u of block i, term v
+              mma_pair<idesc_f8(false, false)>(s, a0 + (v * 4 + i) * 512 + u * 2, b0 + i * 1024 + u * 2,
+                                               (i | u | v) != 0 ? 1u : 0u);
+            } else {                 // 32 tokens u / 2 of chunk i, term u % 2, dims v
+              const uint32_t a = a0 + (u & 1) * 1024 + (i >> 1) * 512 + (i & 1) * 4 + (u >> 1) * 2;
+              const uint32_t b = b0 + i * 1024 + v * 512 + (u >> 1) * 256;
+              if ((u & 1) == 0) mma_pair<idesc_f8(false, true)>(tmem + v * 128, a, b, (i | u) == 0 ? add : 1u);
+              else mma_pair<idesc_f8(true, true)>(tmem + v * 128, a, b, 1u);
+            }
+          }
+        commit_pair(&ctl->empty[kFirst + i]);
+      }
+      if (ok) commit_pair(kPv ? &ctl->odone : &ctl->sfull[par]);
     }
   }
   // Every MMA is complete before tensor memory is released.
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl->drain))
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl->drain[kPv]))
       : "memory");
-  mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+  mbar_wait(&ctl->drain[kPv], 0, kDrainWaitNs);
 }
 
 // Q of the segment's 64 lines of this CTA: q * 2^s = hi + lo, s a power of two a
@@ -836,9 +831,10 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
         if (rank == 0) {
           for (int v = 0; v < 4 && ok; ++v)
             ok = warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
-          if (ok && sw == 0 && lane == 0) arrive_at(vseen1);
+          if (ok && sw == 0 && lane == 0) arrive_release_at(vseen1);
         } else if (ok) {
           ok = warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
+          acquire_cluster();
         }
         ++nv;
         for (int v = from / 64; v < 4 && ok; ++v) {
@@ -926,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* pop = smem + kQBytes;
   uint8_t* chunks = smem + kChunkOff;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + kCtlOff);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cta_rank();
   const int pair = blockIdx.x >> 1;
 
@@ -945,7 +941,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->qready, 2 * kSoftmaxWarps);
     mbar_init(&ctl->odone, 1);
     mbar_init(&ctl->vseen, 1);
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain[0], 1);
+    mbar_init(&ctl->drain[1], 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&map);
@@ -974,8 +971,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     copy<false>(map, p, ctl, chunks, lane, rank, w);
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) issue_mmas(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
+  } else if (warp == 1 || warp == 3) {
+    if (rank == 0 && lane == 0) {
+      if (warp == 1) issue_mmas<false>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
+      else issue_mmas<true>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
+    }
     __syncwarp();
   } else if (warp == 2) {
     copy<true>(map, p, ctl, chunks, lane, rank, w);
