@@ -533,7 +533,17 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
-  return launched(launch_mla_chunk(p, map, workspace, static_cast<cudaStream_t>(stream)));
+  // Output [rows * heads][512] bf16, boxes of 32 dims x 32 lines.
+  CUtensorMap omap;
+  cuuint64_t odim[2] = {static_cast<cuuint64_t>(DSA_LATENT_DIM), static_cast<cuuint64_t>(rows) * heads};
+  cuuint64_t ostride[1] = {static_cast<cuuint64_t>(DSA_LATENT_DIM) * 2};
+  cuuint32_t obox[2] = {32, 32};
+  cr = encode(&omap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, odim, ostride, obox, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
+  return launched(launch_mla_chunk(p, map, omap, workspace, dev->num_sms,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_get_error(int32_t* code_out, int32_t* row_out, int32_t* count_out, int32_t reset) {

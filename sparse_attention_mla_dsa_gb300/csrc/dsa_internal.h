@@ -190,14 +190,21 @@ struct PlanRowsParams {
 // num_sms bounds the grid only; the results do not depend on it.
 cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t stream);
 
+// An item whose tiles several pairs share, as the first of them left it.
+struct ChunkRecord {
+  int64_t line0;     // its first line in q and out
+  int32_t lines;
+  int32_t parts;     // pairs that share it, this one included; 0: none
+};
 struct ChunkParams {
   dsa_seqs seqs;
   const uint16_t* q;
   int64_t nslots;
   uint16_t* out;
   float* lse;
-  float* part_o;     // workspace: [pairs][2][128][512] FP32 unnormalised output of a part
+  float* part_o;     // workspace: [pairs][2][128][128][4] FP32 unnormalised output of a part, 4 dims x lines
   float* part_ml;    // workspace: [pairs][2][128] (max, sum)
+  ChunkRecord* records;  // workspace: [pairs]
   int* err;
   uint64_t wait_ns;
   int32_t rows;
@@ -210,8 +217,9 @@ struct ChunkParams {
 int mla_chunk_box_rows(int block_size);
 size_t mla_chunk_workspace_bytes(int pairs);
 // `map` describes the latent pool [nslots][512] bytes for 128-byte x box_rows
-// copies (1-row boxes where they are gathered).
-cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, void* workspace,
-                             cudaStream_t stream);
+// copies (1-row boxes where they are gathered), `omap` the output [rows * heads]
+// [512] bf16 for 64-byte x 32-line stores.
+cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& omap,
+                             void* workspace, int num_sms, cudaStream_t stream);
 
 }  // namespace dsa

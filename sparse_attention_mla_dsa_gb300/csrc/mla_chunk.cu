@@ -58,14 +58,15 @@ constexpr int kMasks = 8;            // tiles whose token masks are kept
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
-constexpr int kMergeLines = 8;       // lines of a merge CTA, a warp each
+constexpr int kMaxPairs = 256;
 
 struct __align__(16) Ctl {
   uint64_t full[kChunks];            // leader: the copies of both CTAs have landed
   uint64_t empty[kChunks];
-  uint64_t sfull[2], sfree[2], mask_ready[kMasks];
+  uint64_t sfull[2], sfree[2];
   uint64_t pready, odone, qready, vseen, drain[2];
   uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
+  uint32_t tag[kMasks];              // 2 * (tile + 1), and 1 if every token before the item's end has one
   uint32_t fills[kChunks], peer_fills[kChunks];  // fills begun of each chunk; the other CTA's
   uint32_t tmem_base;
   int abort_flag;
@@ -287,6 +288,15 @@ __device__ __forceinline__ bool wait_one(Ctl* c, uint64_t* bar, uint32_t parity,
   if (p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
   return wait_polls(c, bar, parity, p.err, p.wait_ns);
 }
+// The same for a whole warp, every lane polling (no lane waits for another's
+// answer unless there is none yet).
+__device__ __forceinline__ bool wait_all(Ctl* c, uint64_t* bar, uint32_t parity, int lane, const ChunkParams& p) {
+  const bool done = p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
+  if (__all_sync(0xFFFFFFFFu, done)) return true;
+  int ok = 1;
+  if (lane == 0) ok = wait_polls(c, bar, parity, p.err, p.wait_ns) ? 1 : 0;
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
 __device__ __forceinline__ bool warp_wait(Ctl* c, uint64_t* bar, uint32_t parity, int lane, const ChunkParams& p) {
   int ok = 1;
   if (lane == 0) ok = wait_one(c, bar, parity, p) ? 1 : 0;
@@ -378,23 +388,41 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
-  uint16_t out;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
-  return out;
+// 32 lines x 32 dims of the output, from this warp's 2 KB of shared memory.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(src)
+      : "memory");
 }
-__device__ __forceinline__ float2 e4m3x2_decode(uint16_t codes) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(codes));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
-}
-// Two softmax weights (fp16, already times 256) as E4M3 codes and the E5M2
-// codes of their remainders, which fp16 holds exactly.
-__device__ __forceinline__ void split_weights(uint32_t h2, uint16_t& hi, uint16_t& lo) {
-  uint32_t d2, r2;
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Two fp16 values as E4M3 codes, and their remainders, which fp16 holds exactly.
+__device__ __forceinline__ uint16_t split_e4m3(uint32_t h2, uint32_t& rest) {
+  uint16_t hi;
+  uint32_t d2;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h2));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d2) : "h"(hi));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r2) : "r"(h2), "r"(d2));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h2), "r"(d2));
+  return hi;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(hi), "f"(lo));
+  return h2;
+}
+// q, already scaled: two E4M3 terms.
+__device__ __forceinline__ void split_q(uint32_t h2, uint16_t& hi, uint16_t& lo) {
+  uint32_t r2;
+  hi = split_e4m3(h2, r2);
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r2));
+}
+// Two softmax weights (already times 256): an E4M3 term and the E5M2 term of
+// the remainder.
+__device__ __forceinline__ void split_weights(uint32_t h2, uint16_t& hi, uint16_t& lo) {
+  uint32_t r2;
+  hi = split_e4m3(h2, r2);
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r2));
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -443,6 +471,7 @@ __device__ __forceinline__ void softmax_sync() {
 // block up and issues its copies.  Absent tokens are at row nslots, past the end.
 struct Rows {
   int32_t at[8];   // [0]: the box's first row; gathers: tokens 4l.. and 128 + 4l..
+  bool missing;    // this lane has a token without a latent before the item's end
 };
 // kMask: also the tile's token mask, and the error of a missing block.
 template <bool kMask>
@@ -495,7 +524,9 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
       }
     }
   }
+  if constexpr (kMask) __syncwarp();
   if (kMask && missing && rank == 0) record_error(p.err, DSA_DEVERR_BLOCK, g.seq);
+  r.missing = missing;
   return r;
 }
 
@@ -516,8 +547,11 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
     auto look = [&](int t) {
       const Rows r = lookup<!kV>(p, g, end, t, lane, rank, kV ? nullptr : ctl->mask[looked % kMasks]);
       if constexpr (!kV) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->mask_ready[looked % kMasks]);
+        const bool whole = !__any_sync(0xFFFFFFFFu, r.missing);
+        if (lane == 0) {
+          __threadfence_block();
+          *reinterpret_cast<volatile uint32_t*>(&ctl->tag[looked % kMasks]) = 2 * (looked + 1) + (whole ? 1u : 0u);
+        }
         ++looked;
         const int tok = lane * p.box_rows - static_cast<int>(rank) * 128;
         if (p.box_rows > 0 && tok >= 0 && tok < 128 && r.at[0] < p.nslots)
@@ -644,30 +678,23 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
   for (int j = 0; j < kPer; ++j) {
     const int i = sw + j * kSoftmaxWarps;
     const uint32_t w[8] = {qa[j].x, qa[j].y, qa[j].z, qa[j].w, qb[j].x, qb[j].y, qb[j].z, qb[j].w};
-    float x[16];
-    float amax = 0.0f;
-    bool finite = true;
+    auto bf2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    __nv_bfloat162 top = __habs2(bf2(w[0]));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+    for (int k = 1; k < 8; ++k) top = __hmax2_nan(top, __habs2(bf2(w[k])));
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      finite &= fabsf(x[k]) < INFINITY;
-      amax = fmaxf(amax, fabsf(x[k]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    finite = __all_sync(0xFFFFFFFFu, finite);
-    int e = 0;
-    if (finite && amax > 0.0f) frexpf(amax, &e);  // amax < 2^e
-    const int sh = max(-126, min(126, 8 - e));
-    const float scale = copysignf(ldexpf(1.0f, sh), sz);
+    for (int o = 16; o > 0; o >>= 1)
+      top = __hmax2_nan(top, bf2(__shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&top), o)));
+    const __nv_bfloat16 amax = __hmax_nan(__low2bfloat16(top), __high2bfloat16(top));
+    const uint32_t bits = static_cast<uint32_t>(__bfloat16_as_ushort(amax)) << 16;  // >= 0
+    const bool finite = bits < 0x7F800000u;
+    // amax < 2^(field - 126); 2^sh puts it in [128, 256)
+    const int sh = finite ? min(126, 134 - static_cast<int>(bits >> 23)) : 0;
+    const float scale = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), sz);
     if (lane == 0) {
       // Never 0, which times a masked -inf would be NaN.  A line with an
       // infinity or a NaN gives NaN logits, as its formula does.
-      float f = fabsf(sz) * ldexpf(1.0f, -sh);
+      float f = fabsf(sz) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       if (f < 1e-37f) f = 1e-37f;
       ctl->qexp[i] = finite ? f : NAN;
     }
@@ -677,10 +704,8 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
       uint16_t hc[2], lc[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float a0 = x[4 * k + 2 * u] * scale, a1 = x[4 * k + 2 * u + 1] * scale;
-        hc[u] = e4m3x2(a0, a1);
-        const float2 hv = e4m3x2_decode(hc[u]);
-        lc[u] = e4m3x2(a0 - hv.x, a1 - hv.y);
+        const uint32_t x = w[2 * k + u];
+        split_q(pack_f16(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale), hc[u], lc[u]);
       }
       hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
       lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
@@ -695,19 +720,24 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
 // line: lane i and lane 64 + i of tensor memory hold its logits of the tile's
 // first and second 128 tokens (its output's first and second 256 dims), and four
 // warps share a quarter of the lanes, so eight threads have a line.
-__device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t* qop, uint8_t* pop, uint8_t* chunks,
-                                        uint32_t tmem, int warp, int lane, uint32_t rank, int pair, Walk w) {
+// The warps pass the same barriers in the same order whatever happens: after a
+// wait that gave up they go on with what there is, without telling the MMAs.
+__device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkParams& p, Ctl* ctl, uint8_t* qop,
+                                        uint8_t* pop, uint8_t* chunks, uint32_t tmem, int warp, int lane,
+                                        uint32_t rank, int pair, int64_t per, Walk w) {
   const int sw = warp - kSoftmaxWarp0, quarter = warp & 3, sub = sw >> 2;
   const int half = quarter >> 1, group = quarter & 1;
   const int i = group * 32 + lane;                      // line of this CTA
   const int part = half * 4 + sub;
   const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t ocol = tmem + lane_base + sub * 64;    // this thread's 64 output columns
+  const uint32_t scol = tmem + lane_base + kSCol + sub * kTok;
   const uint32_t sfree0 = map_to(&ctl->sfree[0], 0), sfree1 = map_to(&ctl->sfree[1], 0);
   const uint32_t pready = map_to(&ctl->pready, 0), qready = map_to(&ctl->qready, 0);
-  const uint32_t vseen1 = map_to(&ctl->vseen, 1);
+  uint8_t* const prow = pop + half * 8192 + i * 128;
   uint32_t ns = 0, nv = 0;                              // tiles done, masked tiles
   bool ok = true;
+  ChunkRecord rec = {0, 0, 0};
   Segment g, next;
   bool more = next_segment(p, w, next);
   if (more) {
@@ -724,39 +754,41 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
     const int last = g.q.lines - 1;
     const int sees = g.q.ctx + min(line0 + i, last) / p.heads + 1;                 // tokens of this line
     const int all_see = g.q.ctx + min(g.item * kItem, last) / p.heads + 1;        // of every line of the item
+    const int64_t begun = per * pair + ns;              // tiles of the call before this segment
     float m = -INFINITY, l = 0.0f;
     for (int t = g.begin; t < g.end; ++t, ++ns) {
-      const int b = ns & 1;
-      const int tok0 = t * kTile + half * 128 + sub * kTok;
+      const uint32_t b = ns & 1;
       float z[kTok];
-      if (ok) ok = warp_wait(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
-      if (ok) ok = warp_wait(ctl, &ctl->mask_ready[ns % kMasks], (ns / kMasks) & 1, lane, p);
-      bool exceed = false;
-      float mx = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-        tmem_load32(tmem + lane_base + kSCol + b * 128 + sub * kTok, z);
-        const uint32_t there = ctl->mask[ns % kMasks][part];
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(b ? sfree1 : sfree0);
-        const int visible = sees - tok0;                // of this thread's tokens
-        const uint32_t seen = there & (visible >= kTok ? ~0u : visible <= 0 ? 0u : (1u << visible) - 1u);
-        if (seen != ~0u) {
-#pragma unroll
-          for (int k = 0; k < kTok; ++k) z[k] = (seen >> k) & 1u ? z[k] : -INFINITY;
-        }
-        float mk[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-        for (int k = 4; k < kTok; k += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mk[u] = fmaxf(fmaxf(mk[u], z[k + u]), k + 4 + u < kTok ? z[k + 4 + u] : -INFINITY);
-        mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * scale;
-        if (seen == 0) mx = -INFINITY;                  // (NaN where the scale is)
-        exceed = mx > m + kPMaxLog2;
+      ok &= wait_all(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
+      tc_fence_after();
+      tmem_load32(scol + b * 128, z);
+      tc_fence_before();
+      if (lane == 0 && ok) arrive_at(b ? sfree1 : sfree0);
+      // Left before the tile's copies began, which S waited for.
+      const uint32_t tag = *reinterpret_cast<volatile uint32_t*>(&ctl->tag[ns % kMasks]);
+      const int visible = sees - (t * kTile + half * 128 + sub * kTok);   // of this thread's tokens
+      uint32_t seen = visible >= kTok ? ~0u : visible <= 0 ? 0u : (1u << visible) - 1u;
+      if (tag != 2 * (ns + 1) + 1) {
+        __threadfence_block();
+        seen &= ctl->mask[ns % kMasks][part];
       }
-      bool o_idle = ns == 0;                            // the MMAs that read P and add to O are done
-      if (line_sync_or(group, exceed)) {
+      const int from = max(0, all_see - t * kTile);     // the tile's tokens from here on are hidden from some line
+      bool nan = false;                                 // one of them has a NaN logit
+      if (from < kTile || seen != ~0u) {
+        const int hidden = from - (half * 128 + sub * kTok);
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+          nan |= k >= hidden && z[k] != z[k];
+          z[k] = (seen >> k) & 1u ? z[k] : -INFINITY;
+        }
+      }
+      float mk[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+      for (int k = 4; k < kTok; k += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mk[u] = fmaxf(fmaxf(mk[u], z[k + u]), k + 4 + u < kTok ? z[k + 4 + u] : -INFINITY);
+      float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * scale;
+      if (line_sync_or(group, mx > m + kPMaxLog2)) {
         ctl->red[part][i] = mx;
         line_sync(group);
         float tm = ctl->red[0][i];
@@ -768,92 +800,84 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
           m = tm;
           l *= alpha;
         }
-        if (ok && t > g.begin && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-          ok = warp_wait(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
-          o_idle = true;
-          if (ok) {
-            tc_fence_after();
+        if (t > g.begin && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+          ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
+          tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < 64; k += 32) {
-              float v[32];
-              tmem_load32(ocol + k, v);
+          for (int k = 0; k < 64; k += 32) {
+            float v[32];
+            tmem_load32(ocol + k, v);
 #pragma unroll
-              for (int d = 0; d < 32; ++d) v[d] *= alpha;
-              tmem_store16(ocol + k, v);
-              tmem_store16(ocol + k + 16, v + 16);
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            for (int d = 0; d < 32; ++d) v[d] *= alpha;
+            tmem_store16(ocol + k, v);
+            tmem_store16(ocol + k + 16, v + 16);
           }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
         line_sync(group);                               // red[] has been read
       }
-      uint32_t hw[kTok / 4], lw[kTok / 4];
-      if (ok) {
-        const float base = m == -INFINITY ? 0.0f : -m;  // nothing seen yet: every weight is 0
-        float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};   // of the tile first: a long tail of small weights
-#pragma unroll                                          // would be rounded away against a large running sum
-        for (int k = 0; k < kTok / 4; ++k) {
-          uint16_t hc[2], lc[2];
+      const float base = m == -INFINITY ? 0.0f : -m;    // nothing seen yet: every weight is 0
+      float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};     // of the tile first: a long tail of small weights
+      uint32_t hw[kTok / 4], lw[kTok / 4];              // would be rounded away against a large running sum
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float2 x = fma2(make_float2(z[4 * k + 2 * u], z[4 * k + 2 * u + 1]), make_float2(scale, scale),
-                                  make_float2(base, base));
-            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-            sum[u].x += e.x;
-            sum[u].y += e.y;
-            uint32_t h2;
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(e.y), "f"(e.x));
-            const __half2 s2 = __hmul2(*reinterpret_cast<const __half2*>(&h2), __float2half2_rn(kPScale));
-            split_weights(*reinterpret_cast<const uint32_t*>(&s2), hc[u], lc[u]);
-          }
-          hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
-          lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (!o_idle) ok = warp_wait(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
-      }
-      if (ok) {
-        uint8_t* row = pop + half * 8192 + i * 128;
+      for (int k = 0; k < kTok / 4; ++k) {
+        uint16_t hc[2], lc[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
-          *reinterpret_cast<uint4*>(row + at) = make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]);
-          *reinterpret_cast<uint4*>(row + 16384 + at) =
-              make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
+        for (int u = 0; u < 2; ++u) {
+          const float2 x = fma2(make_float2(z[4 * k + 2 * u], z[4 * k + 2 * u + 1]), make_float2(scale, scale),
+                                make_float2(base, base));
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          sum[u].x += e.x;
+          sum[u].y += e.y;
+          const uint32_t h2 = pack_f16(e.x, e.y);
+          const __half2 s2 = __hmul2(*reinterpret_cast<const __half2*>(&h2), __float2half2_rn(kPScale));
+          split_weights(*reinterpret_cast<const uint32_t*>(&s2), hc[u], lc[u]);
         }
+        hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
+        lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
       }
-      // Tokens that a line of the item does not see have weight 0 there, which a
-      // NaN latent would turn into NaN: such codes are zeroed in V (a line that
-      // sees one has a NaN weight, so its output is NaN all the same).  The
-      // leader, whose barriers say when V has landed in both CTAs, tells the other.
-      const int from = max(0, all_see - t * kTile);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (ns > 0) ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);   // P has been read
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
+        *reinterpret_cast<uint4*>(prow + at) = make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]);
+        *reinterpret_cast<uint4*>(prow + 16384 + at) =
+            make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
+      }
+      // A token that some line of the item does not see has weight 0 there, which
+      // a NaN latent would turn into NaN.  Such a latent shows as a NaN logit of
+      // every line of both CTAs; its codes are then zeroed in V (a line that sees
+      // it has a NaN weight, so its output is NaN all the same).  The leader, whose
+      // barriers say when V has landed in both CTAs, tells the other in every such
+      // tile.
       if (from < kTile) {
-        if (rank == 0) {
-          for (int v = 0; v < 4 && ok; ++v)
-            ok = warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
-          if (ok && sw == 0 && lane == 0) arrive_release_at(vseen1);
-        } else if (ok) {
-          ok = warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
+        const bool patch = line_sync_or(group, nan);
+        if (rank == 0 && (patch || sw == 0)) {
+          for (int v = 0; v < 4; ++v) ok &= warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
+          if (sw == 0 && lane == 0) arrive_release_at(map_to(&ctl->vseen, 1));
+        } else if (rank == 1 && patch) {
+          ok &= warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
           acquire_cluster();
         }
         ++nv;
-        for (int v = from / 64; v < 4 && ok; ++v) {
-          const int r0 = max(0, from - v * 64), units = (64 - r0) * 16;  // rows r0..63 x 2 blocks x 8
-          uint4* base = reinterpret_cast<uint4*>(chunks + (4 + v) * kChunkBytes);
-          for (int u = sw * 32 + lane; u < units; u += kSoftmaxThreads) {
-            uint4* q4 = base + (u & 1) * 512 + r0 * 8 + (u >> 1);
-            const uint4 x = *q4;
-            const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
-            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
+        if (patch) {
+          for (int v = from / 64; v < 4; ++v) {
+            const int r0 = max(0, from - v * 64), units = (64 - r0) * 16;  // rows r0..63 x 2 blocks x 8
+            uint4* base4 = reinterpret_cast<uint4*>(chunks + (4 + v) * kChunkBytes);
+            for (int u = part * 32 + lane; u < units; u += kSoftmaxThreads / 2) {
+              uint4* q4 = base4 + (u & 1) * 512 + r0 * 8 + (u >> 1);
+              const uint4 x = *q4;
+              const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
+              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
+            }
           }
         }
       }
-      if (ok) {
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(pready);
-      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) arrive_at(pready);
     }
 
     // Every S of the segment is complete: the next one's Q takes its place
@@ -865,57 +889,87 @@ __device__ __forceinline__ void softmax(const ChunkParams& p, Ctl* ctl, uint8_t*
       convert_q(p, ctl, qop, next, next.item * kItem + static_cast<int>(rank) * kLines, sw, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_at(qready);
+      if (lane == 0 && ok) arrive_at(qready);
     }
     // The line's sum in a fixed order, then its output.
     float lt = ctl->red[0][i];
 #pragma unroll
     for (int k = 1; k < 8; ++k) lt += ctl->red[k][i];
     softmax_sync();                                     // red[] has been read; the next qexp is there
-    if (ok) ok = warp_wait(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
-    if (!ok) continue;
+    ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
     tc_fence_after();
     const bool whole = g.begin == 0 && g.end == g.tiles;
-    const int line = line0 + i;
-    const int64_t gline = static_cast<int64_t>(g.q.row0) * p.heads + line;
+    const int64_t gline0 = static_cast<int64_t>(g.q.row0) * p.heads + line0;
     const int d0 = half * 256 + sub * 64;
-    // slot 0: the item began in an earlier range, 1: it goes on in a later one
-    const int64_t pline = (static_cast<int64_t>(pair) * 2 + (g.begin > 0 ? 0 : 1)) * kItem + rank * kLines + i;
-    const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
+    if (whole) {
+      const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
+      // Through 2 KB of this warp's share of P, 32 lines x 32 dims at a time:
+      // rows of 64 bytes, swizzled, which a copy then writes in whole sectors.
+      uint8_t* const stage = pop + (part >> 1) * 8192 + group * 4096 + (part & 1) * 2048;
+      const bool box = ok && line0 + group * 32 + 31 <= last;
 #pragma unroll 1
-    for (int k = 0; k < 64; k += 32) {
-      float v[32];
-      tmem_load32(ocol + k, v);
-      if (line <= last) {
-        if (whole) {
-          uint32_t o[16];
+      for (int k = 0; k < 64; k += 32) {
+        float v[32];
+        tmem_load32(ocol + k, v);
+        uint4 o[4];
+        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-          for (int d = 0; d < 16; ++d)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[d]) : "f"(v[2 * d + 1] * inv), "f"(v[2 * d] * inv));
-          uint4* dst = reinterpret_cast<uint4*>(p.out + gline * 512 + d0 + k);
+        for (int d = 0; d < 16; ++d)
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(ow[d]) : "f"(v[2 * d + 1] * inv), "f"(v[2 * d] * inv));
+        if (box) {
+          if (k > 0) {
+            if (lane == 0) tma_store_read();
+            __syncwarp();
+          }
 #pragma unroll
-          for (int d = 0; d < 4; ++d) dst[d] = make_uint4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + pline * 512 + d0 + k);
+          for (int d = 0; d < 4; ++d)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((d ^ ((lane >> 1) & 3)) * 16)) = o[d];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store(&omap, smem_u32(stage), d0 + k, static_cast<int32_t>(gline0 + group * 32));
+        } else if (ok && line0 + i <= last) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (gline0 + i) * 512 + d0 + k);
 #pragma unroll
-          for (int d = 0; d < 8; ++d) dst[d] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+          for (int d = 0; d < 4; ++d) dst[d] = o[d];
         }
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    if (part == 0 && line <= last) {
-      if (whole) {
-        if (p.lse != nullptr) p.lse[gline] = lt != 0.0f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        reinterpret_cast<float2*>(p.part_ml)[pline] = make_float2(m, lt);
+      if (lane == 0) tma_store_read();
+      if (ok && part == 0 && line0 + i <= last && p.lse != nullptr)
+        p.lse[gline0 + i] = lt != 0.0f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    } else {
+      // Slot 0: the item began in an earlier range, 1: it goes on in a later one.
+      // [128 groups of 4 dims][128 lines][4]: a warp's lines side by side.
+      const int slot = g.begin > 0 ? 0 : 1, pline = static_cast<int>(rank) * kLines + i;
+      float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                    ((static_cast<int64_t>(pair) * 2 + slot) * 128 + d0 / 4) * kItem + pline;
+#pragma unroll 1
+      for (int k = 0; k < 64; k += 32) {
+        float v[32];
+        tmem_load32(ocol + k, v);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          dst[(k / 4 + d) * kItem] = make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+      }
+      if (part == 0)
+        reinterpret_cast<float2*>(p.part_ml)[(static_cast<int64_t>(pair) * 2 + slot) * kItem + pline] = make_float2(m, lt);
+      if (slot == 1) {
+        rec.line0 = static_cast<int64_t>(g.q.row0) * p.heads + g.item * kItem;
+        rec.lines = min(kItem, g.q.lines - g.item * kItem);
+        // the last range that has a tile of the item, from this one on
+        rec.parts = static_cast<int>((begun + g.tiles - 1) / per - pair) + 1;
       }
     }
     tc_fence_before();
+    __syncwarp();
   }
+  if (lane == 0) tma_store_done();
+  if (rank == 0 && sw == 0 && lane == 0) p.records[pair] = rec;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    mla_chunk_kernel(const __grid_constant__ CUtensorMap map, const ChunkParams p) {
+    mla_chunk_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap omap,
+                     const ChunkParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;           // (no static shared memory: it begins on a 1024-byte boundary)
   uint8_t* qop = smem;
@@ -936,7 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->sfull[k], 1);
       mbar_init(&ctl->sfree[k], 2 * kSoftmaxWarps);
     }
-    for (int k = 0; k < kMasks; ++k) mbar_init(&ctl->mask_ready[k], 1);
+    for (int k = 0; k < kMasks; ++k) ctl->tag[k] = 0;
     mbar_init(&ctl->pready, 2 * kSoftmaxWarps);
     mbar_init(&ctl->qready, 2 * kSoftmaxWarps);
     mbar_init(&ctl->odone, 1);
@@ -946,6 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ctl->abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&map);
+    tma_prefetch_map(&omap);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
@@ -953,10 +1008,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  grid_dep_wait();    // lengths, tables, latents and q come from kernels before
-  // The merge kernel reads the lengths before its own wait: released only now,
-  // when the kernels that write them are complete.
   grid_dep_launch();
+  grid_dep_wait();    // lengths, tables, latents and q come from kernels before
   const Place at = find_place<kThreads>(p, p.pairs, [&](int64_t per) { return per * pair; },
                                         reinterpret_cast<int64_t*>(smem), blockIdx.x == 0);
   Walk w;
@@ -980,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     copy<true>(map, p, ctl, chunks, lane, rank, w);
   } else if (warp >= kSoftmaxWarp0) {
-    softmax(p, ctl, qop, pop, chunks, tmem, warp, lane, rank, pair, w);
+    softmax(omap, p, ctl, qop, pop, chunks, tmem, warp, lane, rank, pair, at.per, w);
   }
 
   tc_fence_before();
@@ -1007,81 +1060,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds up the parts of the items that several ranges share.  Block x: the item
-// that the boundary between ranges x and x + 1 falls into, if that is the
-// item's first; block y: eight of its lines, a warp each.
-__global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
-  __shared__ int64_t scratch[kMergeThreads + sizeof(Place) / 8];
-  const int boundary = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_launch();
-  const Place at = find_place<kMergeThreads>(p, p.pairs, [&](int64_t per) { return per * boundary; }, scratch, false);
-  if (at.seq < 0 || at.tile == 0 || at.tile > at.per) return;  // (more than a range ago: not the first)
-  const SeqInfo q = seq_info(p, at.seq);
-  const int tiles = item_tiles(p, q, at.item);
-  const int64_t start = at.per * boundary - at.tile;
-  const int parts = static_cast<int>((start + tiles - 1) / at.per) - (boundary - 1) + 1;
-  const int i = blockIdx.y * kMergeLines + warp, line = at.item * kItem + i;
-  grid_dep_wait();
-  if (line >= q.lines) return;
+// Adds up the parts of the items that several ranges share.  A unit is 64 lines
+// x kDims groups of 4 dims of one item; four threads have a line and take every
+// fourth part, then are added up in order.  CTAs take units in turn.
+template <int kDims>
+__device__ __forceinline__ void merge_unit(const ChunkParams& p, const ChunkRecord& r, int first, int half, int d4,
+                                           float4 (&x_acc)[3][kDims][64], float2 (&x_ml)[3][64]) {
+  const int i = threadIdx.x & 63, set = threadIdx.x >> 6, line = half * 64 + i;
   // part 0 in slot 1 of its pair, the others in slot 0 of theirs
-  auto pline = [&](int u) {
-    return (static_cast<int64_t>(boundary - 1 + u) * 2 + (u == 0 ? 1 : 0)) * kItem + i;
-  };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float m = -INFINITY;
-  bool nan = false;
-  for (int u = lane; u < parts; u += 32) {
-    const float2 x = ld_dep_f2(ml + pline(u));
-    m = fmaxf(m, x.x);
-    nan |= x.y != x.y;
-  }
+  auto slot = [&](int u) { return static_cast<int64_t>(first + u) * 2 + (u == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + line;
+  const float4* o = reinterpret_cast<const float4*>(p.part_o) + static_cast<int64_t>(d4) * kItem + line;
+  float m = -INFINITY, l = 0.0f;
+  float4 acc[kDims];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  nan = __any_sync(0xFFFFFFFFu, nan);
-  float l = 0.0f, acc[16];
+  for (int d = 0; d < kDims; ++d) acc[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kBatch = kDims > 2 ? 2 : 8;             // parts in flight
+  for (int u0 = set; u0 < r.parts; u0 += 4 * kBatch) {
+    float2 x[kBatch];
+    float4 v[kBatch][kDims];
 #pragma unroll
-  for (int d = 0; d < 16; ++d) acc[d] = 0.0f;
-  if (m != -INFINITY) {
-#pragma unroll 2
-    for (int u = 0; u < parts; ++u) {
-      const float2 x = ld_dep_f2(ml + pline(u));
-      const float wgt = ex2(x.x - m);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + pline(u) * 512) + lane;
-      l += wgt * x.y;
+    for (int k = 0; k < kBatch; ++k) {
+      const int u = u0 + 4 * k;
+      if (u < r.parts) {
+        x[k] = ld_dep_f2(ml + slot(u) * kItem);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = ld_dep_f4(src + k * 32);
-        // (0 of a part without weight: it may hold anything)
-        if (wgt != 0.0f) {
-          acc[4 * k] += wgt * v.x;
-          acc[4 * k + 1] += wgt * v.y;
-          acc[4 * k + 2] += wgt * v.z;
-          acc[4 * k + 3] += wgt * v.w;
-        }
+        for (int d = 0; d < kDims; ++d) v[k][d] = ld_dep_f4(o + (slot(u) * 128 + d) * kItem);
+      } else {
+        x[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) v[k][d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, x[k].x);
+    const float base = top == -INFINITY ? 0.0f : top;   // (no weight yet: 0 times a sum that may be NaN)
+    const float a = ex2(m - base);
+    m = top;
+    l *= a;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      acc[d].x *= a; acc[d].y *= a; acc[d].z *= a; acc[d].w *= a;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float wgt = ex2(x[k].x - base);
+      l += wgt * x[k].y;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) {
+        acc[d].x += wgt * v[k][d].x; acc[d].y += wgt * v[k][d].y;
+        acc[d].z += wgt * v[k][d].z; acc[d].w += wgt * v[k][d].w;
       }
     }
   }
-  const float inv = nan ? NAN : (m != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
-  const int64_t gline = static_cast<int64_t>(q.row0) * p.heads + line;
+  __syncthreads();                                      // the unit before has been read
+  if (set > 0) {
+    x_ml[set - 1][i] = make_float2(m, l);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t o[2];
-#pragma unroll
-    for (int d = 0; d < 2; ++d)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[d]) : "f"(acc[4 * k + 2 * d + 1] * inv), "f"(acc[4 * k + 2 * d] * inv));
-    *reinterpret_cast<uint2*>(p.out + gline * 512 + k * 128 + lane * 4) = make_uint2(o[0], o[1]);
+    for (int d = 0; d < kDims; ++d) x_acc[set - 1][d][i] = acc[d];
   }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[gline] = nan ? NAN : (m != -INFINITY ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY);
+  __syncthreads();
+  if (set > 0 || line >= r.lines) return;
+  float top = m;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) top = fmaxf(top, x_ml[k][i].x);
+  const float base = top == -INFINITY ? 0.0f : top;
+  const float a = ex2(m - base);
+  l *= a;
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) {
+    acc[d].x *= a; acc[d].y *= a; acc[d].z *= a; acc[d].w *= a;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const float wgt = ex2(x_ml[k][i].x - base);
+    l += wgt * x_ml[k][i].y;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      const float4 v = x_acc[k][d][i];
+      acc[d].x += wgt * v.x; acc[d].y += wgt * v.y; acc[d].z += wgt * v.z; acc[d].w += wgt * v.w;
+    }
+  }
+  const float inv = l != l ? l : (top != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
+  const int64_t gline = r.line0 + line;
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) {
+    uint32_t o2[2];
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2[0]) : "f"(acc[d].y * inv), "f"(acc[d].x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2[1]) : "f"(acc[d].w * inv), "f"(acc[d].z * inv));
+    *reinterpret_cast<uint2*>(p.out + gline * 512 + (d4 + d) * 4) = make_uint2(o2[0], o2[1]);
+  }
+  if (d4 == 0 && p.lse != nullptr)
+    p.lse[gline] = l != 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+__global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
+  __shared__ ChunkRecord rec[kMaxPairs];
+  __shared__ float4 x_acc[3][8][64];
+  __shared__ float2 x_ml[3][64];
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int k = threadIdx.x; k < p.pairs; k += kMergeThreads) rec[k] = p.records[k];
+  __syncthreads();
+  // Many parts (few items, long): narrow units, so that they reach every SM.
+  int unit = blockIdx.x;
+  for (int k = 0; k < p.pairs; ++k) {
+    const ChunkRecord r = rec[k];
+    if (r.parts < 2) continue;
+    const int halves = r.lines > 64 ? 2 : 1, n = halves * (r.parts > 8 ? 64 : 16);
+    for (; unit < n; unit += gridDim.x) {
+      const int half = halves == 2 ? unit & 1 : 0, at = halves == 2 ? unit >> 1 : unit;
+      if (r.parts > 8) merge_unit<2>(p, r, k, half, at * 2, reinterpret_cast<float4(&)[3][2][64]>(x_acc), x_ml);
+      else merge_unit<8>(p, r, k, half, at * 8, x_acc, x_ml);
+    }
+    unit -= n;
+  }
 }
 
 }  // namespace
 
 // Two slots a pair: the part of an item that began before its range, and of one
-// that goes on after it.
+// that goes on after it; their (max, sum); a record of the latter.
 size_t mla_chunk_workspace_bytes(int pairs) {
   const size_t lines = static_cast<size_t>(pairs) * 2 * kItem;
-  return lines * 512 * sizeof(float) + lines * 2 * sizeof(float);
+  return lines * 512 * sizeof(float) + lines * 2 * sizeof(float) + pairs * sizeof(ChunkRecord);
 }
 
 // Token rows of one copy: the largest power of two, 64 at most, that divides
@@ -1092,9 +1195,13 @@ int mla_chunk_box_rows(int block_size) {
   return h >= 8 ? h : 0;
 }
 
-cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, void* workspace, cudaStream_t stream) {
+cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& omap, void* workspace,
+                             int num_sms, cudaStream_t stream) {
+  if (p.pairs < 1 || p.pairs > kMaxPairs) return cudaErrorInvalidValue;
+  const size_t lines = static_cast<size_t>(p.pairs) * 2 * kItem;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.part_o + static_cast<size_t>(p.pairs) * 2 * kItem * 512;
+  p.part_ml = p.part_o + lines * 512;
+  p.records = reinterpret_cast<ChunkRecord*>(p.part_ml + lines * 2);
   cudaError_t e = cudaFuncSetAttribute(mla_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemBytes));
   if (e != cudaSuccess) return e;
@@ -1106,10 +1213,10 @@ cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, void* worksp
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, mla_chunk_kernel, map, p);
+  e = cudaLaunchKernelEx(&cfg, mla_chunk_kernel, map, omap, p);
   if (e != cudaSuccess || p.pairs == 1) return e;
   cudaLaunchConfig_t mcfg = {};
-  mcfg.gridDim = dim3(p.pairs - 1, kItem / kMergeLines, 1);
+  mcfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms), 1, 1);
   mcfg.blockDim = dim3(kMergeThreads, 1, 1);
   mcfg.stream = stream;
   mcfg.attrs = attr;
