@@ -64,7 +64,9 @@ struct __align__(16) Ctl {
   uint64_t full[kChunks];            // leader: the copies of both CTAs have landed
   uint64_t empty[kChunks];
   uint64_t sfull[2], sfree[2];
-  uint64_t pready, odone, qready, vseen, drain[2];
+  uint64_t pready[2];               // P of the tile's first and second 128 tokens
+  uint64_t odone[2];                 // O of even and odd tiles: waited for every few tiles, not in each
+  uint64_t qready, vseen, drain[2];
   uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
   uint32_t tag[kMasks];              // 2 * (tile + 1), and 1 if every token before the item's end has one
   uint32_t fills[kChunks], peer_fills[kChunks];  // fills begun of each chunk; the other CTA's
@@ -619,12 +621,12 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
     ++nq;
     for (int t = g.begin; t < g.end && ok; ++t, ++n) {
       const uint32_t par = n & 1;
-      if (kPv) ok = wait_one(ctl, &ctl->pready, par, p);
-      else if (n >= 2) ok = wait_one(ctl, &ctl->sfree[par], ((n - 2) >> 1) & 1, p);
+      if (!kPv && n >= 2) ok = wait_one(ctl, &ctl->sfree[par], ((n - 2) >> 1) & 1, p);
       const uint32_t s = tmem + kSCol + par * 128;
       const uint32_t add = t == g.begin ? 0u : 1u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (kPv && i % 2 == 0) ok = ok && wait_one(ctl, &ctl->pready[i / 2], par, p);
         ok = ok && wait_one(ctl, &ctl->full[kFirst + i], par, p);
         if (!ok) break;
         tc_fence_after();
@@ -644,7 +646,7 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
           }
         commit_pair(&ctl->empty[kFirst + i]);
       }
-      if (ok) commit_pair(kPv ? &ctl->odone : &ctl->sfull[par]);
+      if (ok) commit_pair(kPv ? &ctl->odone[par] : &ctl->sfull[par]);
     }
   }
   // Every MMA is complete before tensor memory is released.
@@ -733,8 +735,11 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   const uint32_t ocol = tmem + lane_base + sub * 64;    // this thread's 64 output columns
   const uint32_t scol = tmem + lane_base + kSCol + sub * kTok;
   const uint32_t sfree0 = map_to(&ctl->sfree[0], 0), sfree1 = map_to(&ctl->sfree[1], 0);
-  const uint32_t pready = map_to(&ctl->pready, 0), qready = map_to(&ctl->qready, 0);
+  const uint32_t pready = map_to(&ctl->pready[half], 0), qready = map_to(&ctl->qready, 0);
   uint8_t* const prow = pop + half * 8192 + i * 128;
+  // Every O up to tile n is complete.  A warp that waits for tile n has seen half
+  // of n - 1 complete, so n - 2, the phase before on n's barrier, is.
+  auto wait_o = [&](uint32_t n) { return wait_all(ctl, &ctl->odone[n & 1], (n >> 1) & 1, lane, p); };
   uint32_t ns = 0, nv = 0;                              // tiles done, masked tiles
   bool ok = true;
   ChunkRecord rec = {0, 0, 0};
@@ -749,6 +754,12 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   }
   while (more) {
     g = next;
+    more = next_segment(p, w, next);
+    if (more) {                                         // its Q, brought into L2 now
+      const int i8 = next.item * kItem + static_cast<int>(rank) * kLines + sw + (lane >> 3) * kSoftmaxWarps;
+      if (i8 < next.q.lines)
+        prefetch_l2(p.q + (static_cast<int64_t>(next.q.row0) * p.heads + i8) * 512 + (lane & 7) * 64);
+    }
     const int line0 = g.item * kItem + static_cast<int>(rank) * kLines;
     const float scale = ctl->qexp[i];
     const int last = g.q.lines - 1;
@@ -801,7 +812,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
           l *= alpha;
         }
         if (t > g.begin && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-          ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
+          ok &= wait_o(ns - 1);
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < 64; k += 32) {
@@ -837,7 +848,9 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (ns > 0) ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);   // P has been read
+      // This half of P has been read: the MMAs take the tile's first 128 tokens
+      // first, so it is written again while those of the second half run.
+      if (ns > 0) ok &= wait_all(ctl, &ctl->empty[half ? 7 : 5], (ns - 1) & 1, lane, p);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
@@ -854,6 +867,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       if (from < kTile) {
         const bool patch = line_sync_or(group, nan);
         if (rank == 0 && (patch || sw == 0)) {
+          if (ns > 0) ok &= wait_o(ns - 1);             // (the V before has landed, too)
           for (int v = 0; v < 4; ++v) ok &= warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
           if (sw == 0 && lane == 0) arrive_release_at(map_to(&ctl->vseen, 1));
         } else if (rank == 1 && patch) {
@@ -872,6 +886,8 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
               if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
             }
           }
+          fence_proxy_async_smem();
+          line_sync(group);                             // before the first half of P tells that V can be used
         }
       }
       fence_proxy_async_smem();
@@ -882,7 +898,6 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 
     // Every S of the segment is complete: the next one's Q takes its place
     // while the last P V runs, and its first S runs beside the epilogue.
-    more = next_segment(p, w, next);
     ctl->red[part][i] = l;
     softmax_sync();                                     // l; qexp has been read
     if (more) {
@@ -896,7 +911,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 #pragma unroll
     for (int k = 1; k < 8; ++k) lt += ctl->red[k][i];
     softmax_sync();                                     // red[] has been read; the next qexp is there
-    ok &= wait_all(ctl, &ctl->odone, (ns - 1) & 1, lane, p);
+    ok &= wait_o(ns - 1);
     tc_fence_after();
     const bool whole = g.begin == 0 && g.end == g.tiles;
     const int64_t gline0 = static_cast<int64_t>(g.q.row0) * p.heads + line0;
@@ -991,9 +1006,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->sfree[k], 2 * kSoftmaxWarps);
     }
     for (int k = 0; k < kMasks; ++k) ctl->tag[k] = 0;
-    mbar_init(&ctl->pready, 2 * kSoftmaxWarps);
+    mbar_init(&ctl->pready[0], kSoftmaxWarps);
+    mbar_init(&ctl->pready[1], kSoftmaxWarps);
     mbar_init(&ctl->qready, 2 * kSoftmaxWarps);
-    mbar_init(&ctl->odone, 1);
+    mbar_init(&ctl->odone[0], 1);
+    mbar_init(&ctl->odone[1], 1);
     mbar_init(&ctl->vseen, 1);
     mbar_init(&ctl->drain[0], 1);
     mbar_init(&ctl->drain[1], 1);
