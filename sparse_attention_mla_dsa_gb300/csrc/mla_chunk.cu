@@ -23,6 +23,15 @@
 // its 64 lines of Q and its 128 tokens of the tile (all 512 dims), for O += P V
 // its 64 lines of P and its 256 dims of V (all 256 tokens).
 //
+// Copies.  An SM takes in 32 bytes a clock from L2 (62 GB/s measured, on every
+// SM), so K and V copied apart, 128 KB a tile, would take the 4,100 clocks of the
+// tile's MMAs.  Half of a CTA's V is half of its K: its tokens, its dims.  A
+// 16 KB block is 128 tokens x 128 dims for both uses (K-major for S, MN-major for
+// O), and both CTAs' MMAs read the same places, so a tile has four blocks: K in
+// all four, and once S has read them V of the tokens 0..127 in the first two and
+// of 128..255 in the last two, of which each CTA only has to copy the two that
+// are not its own tokens.  96 KB a tile, and two tiles in flight.
+//
 // Precision.  The latents stay E4M3.  q * 2^s = hi + lo, two E4M3 terms, holds
 // a bf16 q exactly but for elements 2^10 below the head's largest; a softmax
 // weight is an E4M3 term and the E5M2 term of its remainder (2^-7 of the weight
@@ -46,30 +55,32 @@ constexpr int kItem = 128;           // lines of an item (MMA M over the pair)
 constexpr int kLines = 64;           // lines of a CTA
 constexpr int kTile = 256;           // tokens of a tile
 constexpr int kTok = 32;             // tokens of a softmax thread
-constexpr int kChunks = 8;           // 16 KB each: 0..3 a tile's K (128 dims), 4..7 its V (64 tokens)
-constexpr uint32_t kChunkBytes = 16384;
+constexpr int kBlocks = 8;           // of 128 tokens x 128 dims; four a tile, for two tiles
+constexpr uint32_t kBlockBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [term][128-dim block][64 lines][128 B]
 constexpr uint32_t kPBytes = 32768;  // [term][128-token half][64 lines][128 B]
-constexpr uint32_t kChunkOff = kQBytes + kPBytes;
-constexpr uint32_t kCtlOff = kChunkOff + kChunks * kChunkBytes;
+constexpr uint32_t kBlockOff = kQBytes + kPBytes;
+constexpr uint32_t kCtlOff = kBlockOff + kBlocks * kBlockBytes;
 constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
 constexpr int kMasks = 8;            // tiles whose token masks are kept
+constexpr int kItemCost = 2;         // an item costs what so many tiles cost, besides its tiles
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
 constexpr int kMaxPairs = 256;
 
+// Barriers of tile t have index t & 1 (or 4 * (t & 1) + block) and phase t >> 1.
 struct __align__(16) Ctl {
-  uint64_t full[kChunks];            // leader: the copies of both CTAs have landed
-  uint64_t empty[kChunks];
+  uint64_t kfull[kBlocks], vfull[kBlocks];  // leader: copies have landed, in both CTAs
+  uint64_t kread[kBlocks];           // S has read the block
+  uint64_t vread[4];                 // O has read V and P of the tokens 0..127, 128..255 (2 * (t & 1) + half)
   uint64_t sfull[2], sfree[2];
-  uint64_t pready[2];               // P of the tile's first and second 128 tokens
-  uint64_t odone[2];                 // O of even and odd tiles: waited for every few tiles, not in each
+  uint64_t pready[2];                // P of the tile's first and second 128 tokens (index: half, phase: t)
   uint64_t qready, vseen, drain[2];
   uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
   uint32_t tag[kMasks];              // 2 * (tile + 1), and 1 if every token before the item's end has one
-  uint32_t fills[kChunks], peer_fills[kChunks];  // fills begun of each chunk; the other CTA's
+  uint32_t fills[2 * kBlocks], peer_fills[2 * kBlocks];  // copies begun of each block, K and V; the other CTA's
   uint32_t tmem_base;
   int abort_flag;
   float qexp[kLines];
@@ -112,27 +123,28 @@ __device__ __forceinline__ int item_tiles(const ChunkParams& p, const SeqInfo& q
 __device__ __forceinline__ int items_within(const ChunkParams& p, const SeqInfo& q, int x) {
   return x <= 0 ? 0 : x >= q.rows ? q.items : static_cast<int>(static_cast<int64_t>(x) * p.heads / kItem);
 }
-// All its tiles: items by their number of tiles v, those within v tiles less
-// those within v - 1.
-__device__ __forceinline__ int64_t seq_tiles(const ChunkParams& p, const SeqInfo& q) {
+// The request's cost: items by their number of tiles v, those within v tiles
+// less those within v - 1.
+__device__ __forceinline__ int64_t seq_cost(const ChunkParams& p, const SeqInfo& q) {
   if (q.items == 0) return 0;
   int64_t sum = 0;
   int below = 0;
   for (int v = (q.ctx + kTile) / kTile; below < q.items; ++v) {
     const int upto = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
-    sum += static_cast<int64_t>(upto - below) * v;
+    sum += static_cast<int64_t>(upto - below) * (v + kItemCost);
     below = upto;
   }
   return sum;
 }
 
 struct Place {
-  int64_t total;   // tiles of the call
-  int64_t per;     // tiles of a pair
-  int seq, item, tile;
+  int64_t total;   // cost of the call
+  int64_t per;     // cost of a pair's range
+  int seq, item;
+  int64_t off;     // cost of the item before the place: its own first, then its tiles
 };
 
-// Finds tile `target(total)` of the call: every thread sums a run of requests,
+// Finds the place `target(per)` of the call: every thread sums a run of requests,
 // the CTA scans the sums, and the thread whose run holds it walks to it.
 // `scratch`: kN int64 and a Place of shared memory.  Returns seq -1 past the end.
 template <int kN, typename Target>
@@ -146,7 +158,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
     int why = 0;
     const SeqInfo q = seq_info(p, s, &why);
     if (why != 0 && report) record_error(p.err, why, s);
-    sum += seq_tiles(p, q);
+    sum += seq_cost(p, q);
   }
   scratch[tid] = sum;
   if (tid == 0) found.seq = -1;
@@ -179,7 +191,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
   if (want < found.total && want >= at && want < at + sum) {
     for (int s = s0; s < s1; ++s) {
       const SeqInfo q = seq_info(p, s);
-      const int64_t t = seq_tiles(p, q);
+      const int64_t t = seq_cost(p, q);
       if (want >= at + t) {
         at += t;
         continue;
@@ -188,11 +200,11 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
       int below = 0;
       for (int v = (q.ctx + kTile) / kTile;; ++v) {
         const int upto = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
-        const int64_t here = static_cast<int64_t>(upto - below) * v;
+        const int64_t here = static_cast<int64_t>(upto - below) * (v + kItemCost);
         if (off < here) {
           found.seq = s;
-          found.item = below + static_cast<int>(off / v);
-          found.tile = static_cast<int>(off % v);
+          found.item = below + static_cast<int>(off / (v + kItemCost));
+          found.off = off % (v + kItemCost);
           break;
         }
         off -= here;
@@ -214,27 +226,29 @@ struct Segment {
   int begin, end;         // tiles of the segment
 };
 struct Walk {
-  int seq, item, begin;
-  int64_t left;           // tiles
+  int seq, item;
+  int64_t off;            // cost of the item before the range's place in it
+  int64_t left;           // cost
 };
 __device__ __forceinline__ bool next_segment(const ChunkParams& p, Walk& w, Segment& g) {
   if (w.left <= 0) return false;
   g.q = seq_info(p, w.seq);
   while (w.item >= g.q.items) {
     w.item = 0;
-    w.begin = 0;
     if (++w.seq >= p.seqs.seqs) return false;
     g.q = seq_info(p, w.seq);
   }
   g.seq = w.seq;
   g.item = w.item;
   g.tiles = item_tiles(p, g.q, w.item);
-  g.begin = w.begin;
-  g.end = static_cast<int>(min(static_cast<int64_t>(g.tiles), w.begin + w.left));
-  w.left -= g.end - g.begin;
-  w.begin = 0;
+  const int64_t end = min(w.off + w.left, static_cast<int64_t>(g.tiles + kItemCost));
+  g.begin = static_cast<int>(max(static_cast<int64_t>(0), w.off - kItemCost));
+  g.end = static_cast<int>(end - kItemCost);
+  w.left -= end - w.off;
+  w.off = 0;
   ++w.item;
-  return true;
+  // A range that ends in an item's own cost leaves it to the next.
+  return g.end > g.begin;
 }
 
 // ------------------------------------------------------------------ pair
@@ -532,16 +546,15 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
   return r;
 }
 
-// Warps 0 and 2.  kV false: this CTA's 128 tokens of every tile's K, in chunks of
-// 128 dims.  kV true: its 256 dims of every tile's V, in chunks of 64 tokens.
-// Each has its own four chunks, taken again as soon as the tile before is done
-// with them (one warp alone fills a chunk: a barrier's parity says nothing to a
-// warp that may be two fills behind).
+// Warp 0: this CTA's 128 tokens of every tile's K, a block for each 128 dims.
+// Warp 2 (kV): the two blocks of V that are not among them: the other CTA's
+// tokens, this CTA's dims.  The leader's warps expect the bytes of both CTAs.
 template <bool kV>
-__device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* chunks,
+__device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* blocks,
                                      int lane, uint32_t rank, Walk w) {
-  constexpr int kFirst = kV ? 4 : 0;
-  uint32_t looked = 0, tiles = 0;
+  // tokens that this warp copies: 0..127 or 128..255
+  const int from = (kV ? rank == 0 : rank == 1) ? 128 : 0;
+  uint32_t looked = 0, n = 0;
   Segment g;
   while (next_segment(p, w, g)) {
     const int end = item_end(p, g.q, g.item);
@@ -555,49 +568,44 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
           *reinterpret_cast<volatile uint32_t*>(&ctl->tag[looked % kMasks]) = 2 * (looked + 1) + (whole ? 1u : 0u);
         }
         ++looked;
-        const int tok = lane * p.box_rows - static_cast<int>(rank) * 128;
+        const int tok = lane * p.box_rows - from;
         if (p.box_rows > 0 && tok >= 0 && tok < 128 && r.at[0] < p.nslots)
           for (int d = 0; d < 4; ++d) tma_prefetch_l2_2d(&map, d * 128, r.at[0]);
       }
       return r;
     };
     Rows next = look(g.begin);
-    for (int t = g.begin; t < g.end; ++t, ++tiles) {
+    for (int t = g.begin; t < g.end; ++t, ++n) {
       const Rows r = next;
       if (t + 1 < g.end) next = look(t + 1);   // before the waits of this tile
+      const uint32_t b4 = 4 * (n & 1), phase = (n >> 1) & 1;
       for (int i = 0; i < 4; ++i) {
-        const int slot = kFirst + i;
-        if (tiles > 0 && !warp_wait(ctl, &ctl->empty[slot], (tiles - 1) & 1, lane, p)) return;
+        // V of the tokens 0..127 goes to the first two blocks, of the others to
+        // the last two; the leader expects what the other CTA copies.
+        const bool mine = !kV || (i >= 2) == (from != 0);
+        if (!mine && rank != 0) continue;
+        uint64_t* const full = kV ? &ctl->vfull[b4 + i] : &ctl->kfull[b4 + i];
+        if (kV) {
+          if (!warp_wait(ctl, &ctl->kread[b4 + i], phase, lane, p)) return;
+        } else if (n >= 2 && (i & 1) == 0) {
+          if (!warp_wait(ctl, &ctl->vread[2 * (n & 1) + (i >> 1)], phase ^ 1, lane, p)) return;
+        }
         if (lane == 0) {
-          ctl->fills[slot] = tiles + 1;
-          // the leader expects the bytes of both CTAs
-          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 2 * kChunkBytes);
+          ctl->fills[(kV ? kBlocks : 0) + b4 + i] = (n >> 1) + 1;
+          if (rank == 0) mbar_arrive_expect_tx(full, kV ? kBlockBytes : 2 * kBlockBytes);
         }
         __syncwarp();
-        const uint32_t dst = smem_u32(chunks + slot * kChunkBytes), bar = map_to(&ctl->full[slot], 0);
-        if constexpr (!kV) {
-          if (p.box_rows > 0) {
-            const int tok = lane * p.box_rows - static_cast<int>(rank) * 128;
-            if (tok >= 0 && tok < 128) tma_box(dst + tok * 128, &map, bar, i * 128, r.at[0]);
-          } else {
-            int32_t y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = rank ? r.at[4 + k] : r.at[k];
-            tma_gather4(dst + lane * 512, &map, bar, i * 128, y);
-          }
+        if (!mine) continue;
+        const uint32_t dst = smem_u32(blocks + (b4 + i) * kBlockBytes), bar = map_to(full, 0);
+        const int x = kV ? static_cast<int>(rank) * 256 + (i & 1) * 128 : i * 128;
+        if (p.box_rows > 0) {
+          const int tok = lane * p.box_rows - from;
+          if (tok >= 0 && tok < 128) tma_box(dst + tok * 128, &map, bar, x, r.at[0]);
         } else {
-          const int x0 = static_cast<int>(rank) * 256;
-          if (p.box_rows > 0) {
-            const int tok = lane * p.box_rows - i * 64;
-            if (tok >= 0 && tok < 64)
-              for (int b = 0; b < 2; ++b) tma_box(dst + b * 8192 + tok * 128, &map, bar, x0 + b * 128, r.at[0]);
-          } else if ((lane >> 4) == (i & 1)) {
-            int32_t y[4];
+          int32_t y[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = i >= 2 ? r.at[4 + k] : r.at[k];
-            for (int b = 0; b < 2; ++b)
-              tma_gather4(dst + b * 8192 + (lane & 15) * 512, &map, bar, x0 + b * 128, y);
-          }
+          for (int k = 0; k < 4; ++k) y[k] = from ? r.at[4 + k] : r.at[k];
+          tma_gather4(dst + lane * 512, &map, bar, x, y);
         }
       }
     }
@@ -609,10 +617,9 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
 // scheduler: beside four softmax warps one alone issues an MMA in 94 to 128
 // clocks, where the tensor cores take 64.
 template <bool kPv>
-__device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint32_t q0, uint32_t p0, uint32_t chunk0,
+__device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint32_t q0, uint32_t p0, uint32_t block0,
                                            uint32_t tmem, Walk w) {
-  constexpr int kFirst = kPv ? 4 : 0;
-  const uint32_t a0 = desc_low(kPv ? p0 : q0), b0 = desc_low(chunk0 + kFirst * kChunkBytes);
+  const uint32_t a0 = desc_low(kPv ? p0 : q0);
   uint32_t n = 0, nq = 0;            // tiles issued, segments
   bool ok = true;
   Segment g;
@@ -620,33 +627,45 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
     if (!kPv) ok = wait_one(ctl, &ctl->qready, nq & 1, p);
     ++nq;
     for (int t = g.begin; t < g.end && ok; ++t, ++n) {
-      const uint32_t par = n & 1;
-      if (!kPv && n >= 2) ok = wait_one(ctl, &ctl->sfree[par], ((n - 2) >> 1) & 1, p);
+      const uint32_t par = n & 1, phase = (n >> 1) & 1;
+      const uint32_t b0 = desc_low(block0) + par * 4096;
+      if (!kPv && n >= 2) ok = wait_one(ctl, &ctl->sfree[par], phase ^ 1, p);
       const uint32_t s = tmem + kSCol + par * 128;
       const uint32_t add = t == g.begin ? 0u : 1u;
+      if constexpr (!kPv) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kPv && i % 2 == 0) ok = ok && wait_one(ctl, &ctl->pready[i / 2], par, p);
-        ok = ok && wait_one(ctl, &ctl->full[kFirst + i], par, p);
-        if (!ok) break;
-        tc_fence_after();
+        for (int i = 0; i < 4; ++i) {              // 128 dims
+          ok = ok && wait_one(ctl, &ctl->kfull[4 * par + i], phase, p);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 4; ++u)              // 32 dims
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            if constexpr (!kPv) {    // 32 dims u of block i, term v
+            for (int v = 0; v < 2; ++v)            // term
               mma_pair<idesc_f8(false, false)>(s, a0 + (v * 4 + i) * 512 + u * 2, b0 + i * 1024 + u * 2,
                                                (i | u | v) != 0 ? 1u : 0u);
-            } else {                 // 32 tokens u / 2 of chunk i, term u % 2, dims v
-              const uint32_t a = a0 + (u & 1) * 1024 + (i >> 1) * 512 + (i & 1) * 4 + (u >> 1) * 2;
-              const uint32_t b = b0 + i * 1024 + v * 512 + (u >> 1) * 256;
-              if ((u & 1) == 0) mma_pair<idesc_f8(false, true)>(tmem + v * 128, a, b, (i | u) == 0 ? add : 1u);
-              else mma_pair<idesc_f8(true, true)>(tmem + v * 128, a, b, 1u);
+          commit_pair(&ctl->kread[4 * par + i]);
+        }
+        if (ok) commit_pair(&ctl->sfull[par]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {              // 128 tokens
+          ok = ok && wait_one(ctl, &ctl->vfull[4 * par + 2 * h], phase, p) &&
+               wait_one(ctl, &ctl->vfull[4 * par + 2 * h + 1], phase, p) && wait_one(ctl, &ctl->pready[h], par, p);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < 4; ++u)              // 32 tokens
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {          // term v / 2, 128 dims v % 2
+              const uint32_t a = a0 + (v >> 1) * 1024 + h * 512 + u * 2;
+              const uint32_t b = b0 + (2 * h + (v & 1)) * 1024 + u * 256;
+              if (v < 2) mma_pair<idesc_f8(false, true)>(tmem + (v & 1) * 128, a, b, (h | u) == 0 ? add : 1u);
+              else mma_pair<idesc_f8(true, true)>(tmem + (v & 1) * 128, a, b, 1u);
             }
-          }
-        commit_pair(&ctl->empty[kFirst + i]);
+          commit_pair(&ctl->vread[2 * par + h]);
+        }
       }
-      if (ok) commit_pair(kPv ? &ctl->odone[par] : &ctl->sfull[par]);
     }
   }
   // Every MMA is complete before tensor memory is released.
@@ -725,7 +744,7 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
 // The warps pass the same barriers in the same order whatever happens: after a
 // wait that gave up they go on with what there is, without telling the MMAs.
 __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkParams& p, Ctl* ctl, uint8_t* qop,
-                                        uint8_t* pop, uint8_t* chunks, uint32_t tmem, int warp, int lane,
+                                        uint8_t* pop, uint8_t* blocks, uint32_t tmem, int warp, int lane,
                                         uint32_t rank, int pair, int64_t per, Walk w) {
   const int sw = warp - kSoftmaxWarp0, quarter = warp & 3, sub = sw >> 2;
   const int half = quarter >> 1, group = quarter & 1;
@@ -737,10 +756,11 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   const uint32_t sfree0 = map_to(&ctl->sfree[0], 0), sfree1 = map_to(&ctl->sfree[1], 0);
   const uint32_t pready = map_to(&ctl->pready[half], 0), qready = map_to(&ctl->qready, 0);
   uint8_t* const prow = pop + half * 8192 + i * 128;
-  // Every O up to tile n is complete.  A warp that waits for tile n has seen half
+  // O of tile n is complete.  A warp that waits for tile n has seen the first half
   // of n - 1 complete, so n - 2, the phase before on n's barrier, is.
-  auto wait_o = [&](uint32_t n) { return wait_all(ctl, &ctl->odone[n & 1], (n >> 1) & 1, lane, p); };
+  auto wait_o = [&](uint32_t n) { return wait_all(ctl, &ctl->vread[2 * (n & 1) + 1], (n >> 1) & 1, lane, p); };
   uint32_t ns = 0, nv = 0;                              // tiles done, masked tiles
+  int64_t begun = per * pair - w.off;
   bool ok = true;
   ChunkRecord rec = {0, 0, 0};
   Segment g, next;
@@ -765,7 +785,8 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     const int last = g.q.lines - 1;
     const int sees = g.q.ctx + min(line0 + i, last) / p.heads + 1;                 // tokens of this line
     const int all_see = g.q.ctx + min(g.item * kItem, last) / p.heads + 1;        // of every line of the item
-    const int64_t begun = per * pair + ns;              // tiles of the call before this segment
+    const int64_t at = begun;                           // cost of the call before this item
+    begun += g.tiles + kItemCost;
     float m = -INFINITY, l = 0.0f;
     for (int t = g.begin; t < g.end; ++t, ++ns) {
       const uint32_t b = ns & 1;
@@ -850,7 +871,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       // This half of P has been read: the MMAs take the tile's first 128 tokens
       // first, so it is written again while those of the second half run.
-      if (ns > 0) ok &= wait_all(ctl, &ctl->empty[half ? 7 : 5], (ns - 1) & 1, lane, p);
+      if (ns > 0) ok &= wait_all(ctl, &ctl->vread[2 * ((ns - 1) & 1) + half], ((ns - 1) >> 1) & 1, lane, p);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
@@ -867,8 +888,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       if (from < kTile) {
         const bool patch = line_sync_or(group, nan);
         if (rank == 0 && (patch || sw == 0)) {
-          if (ns > 0) ok &= wait_o(ns - 1);             // (the V before has landed, too)
-          for (int v = 0; v < 4; ++v) ok &= warp_wait(ctl, &ctl->full[4 + v], ns & 1, lane, p);
+          for (int v = 0; v < 4; ++v) ok &= warp_wait(ctl, &ctl->vfull[4 * b + v], (ns >> 1) & 1, lane, p);
           if (sw == 0 && lane == 0) arrive_release_at(map_to(&ctl->vseen, 1));
         } else if (rank == 1 && patch) {
           ok &= warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
@@ -876,14 +896,13 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         }
         ++nv;
         if (patch) {
-          for (int v = from / 64; v < 4; ++v) {
-            const int r0 = max(0, from - v * 64), units = (64 - r0) * 16;  // rows r0..63 x 2 blocks x 8
-            uint4* base4 = reinterpret_cast<uint4*>(chunks + (4 + v) * kChunkBytes);
+          for (int v = from / 128 * 2; v < 4; ++v) {    // block: 128 tokens x 128 dims
+            const int r0 = max(0, from - (v >> 1) * 128), units = (128 - r0) * 8;
+            uint4* rows = reinterpret_cast<uint4*>(blocks + (4 * b + v) * kBlockBytes) + r0 * 8;
             for (int u = part * 32 + lane; u < units; u += kSoftmaxThreads / 2) {
-              uint4* q4 = base4 + (u & 1) * 512 + r0 * 8 + (u >> 1);
-              const uint4 x = *q4;
+              const uint4 x = rows[u];
               const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
-              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) *q4 = y;
+              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) rows[u] = y;
             }
           }
           fence_proxy_async_smem();
@@ -972,7 +991,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         rec.line0 = static_cast<int64_t>(g.q.row0) * p.heads + g.item * kItem;
         rec.lines = min(kItem, g.q.lines - g.item * kItem);
         // the last range that has a tile of the item, from this one on
-        rec.parts = static_cast<int>((begun + g.tiles - 1) / per - pair) + 1;
+        rec.parts = static_cast<int>((at + kItemCost + g.tiles - 1) / per - pair) + 1;
       }
     }
     tc_fence_before();
@@ -989,31 +1008,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw;           // (no static shared memory: it begins on a 1024-byte boundary)
   uint8_t* qop = smem;
   uint8_t* pop = smem + kQBytes;
-  uint8_t* chunks = smem + kChunkOff;
+  uint8_t* blocks = smem + kBlockOff;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + kCtlOff);
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cta_rank();
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int k = 0; k < kChunks; ++k) {
-      mbar_init(&ctl->full[k], 1);
-      mbar_init(&ctl->empty[k], 1);
-      ctl->fills[k] = 0;
+    for (int k = 0; k < kBlocks; ++k) {
+      mbar_init(&ctl->kfull[k], 1);
+      mbar_init(&ctl->vfull[k], 1);
+      mbar_init(&ctl->kread[k], 1);
     }
+    for (int k = 0; k < 2 * kBlocks; ++k) ctl->fills[k] = 0;
+    for (int k = 0; k < 4; ++k) mbar_init(&ctl->vread[k], 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&ctl->sfull[k], 1);
       mbar_init(&ctl->sfree[k], 2 * kSoftmaxWarps);
+      mbar_init(&ctl->pready[k], kSoftmaxWarps);
+      mbar_init(&ctl->drain[k], 1);
     }
-    for (int k = 0; k < kMasks; ++k) ctl->tag[k] = 0;
-    mbar_init(&ctl->pready[0], kSoftmaxWarps);
-    mbar_init(&ctl->pready[1], kSoftmaxWarps);
     mbar_init(&ctl->qready, 2 * kSoftmaxWarps);
-    mbar_init(&ctl->odone[0], 1);
-    mbar_init(&ctl->odone[1], 1);
     mbar_init(&ctl->vseen, 1);
-    mbar_init(&ctl->drain[0], 1);
-    mbar_init(&ctl->drain[1], 1);
+    for (int k = 0; k < kMasks; ++k) ctl->tag[k] = 0;
     ctl->abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&map);
@@ -1032,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Walk w;
   w.seq = at.seq;
   w.item = at.item;
-  w.begin = at.tile;
+  w.off = at.off;
   w.left = at.seq < 0 ? 0 : min(at.per, at.total - at.per * pair);
   tc_fence_before();
   cluster_sync();     // barriers, tensor memory address; the scratch is free
@@ -1040,34 +1057,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    copy<false>(map, p, ctl, chunks, lane, rank, w);
+    copy<false>(map, p, ctl, blocks, lane, rank, w);
   } else if (warp == 1 || warp == 3) {
     if (rank == 0 && lane == 0) {
-      if (warp == 1) issue_mmas<false>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
-      else issue_mmas<true>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(chunks), tmem, w);
+      if (warp == 1) issue_mmas<false>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(blocks), tmem, w);
+      else issue_mmas<true>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(blocks), tmem, w);
     }
     __syncwarp();
   } else if (warp == 2) {
-    copy<true>(map, p, ctl, chunks, lane, rank, w);
+    copy<true>(map, p, ctl, blocks, lane, rank, w);
   } else if (warp >= kSoftmaxWarp0) {
-    softmax(omap, p, ctl, qop, pop, chunks, tmem, warp, lane, rank, pair, at.per, w);
+    softmax(omap, p, ctl, qop, pop, blocks, tmem, warp, lane, rank, pair, at.per, w);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (rank == 1 && tid < kChunks)
+  if (rank == 1 && tid < 2 * kBlocks)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "r"(ctl->fills[tid]) : "memory");
   cluster_sync();
   // No CTA leaves with a copy of either in flight.  All are complete unless a
-  // wait gave up; then one CTA may have begun a slot's copies that the other
-  // has not, and the bytes that will not come are made up for.
-  if (rank == 0 && tid < kChunks) {
-    const uint32_t mine = ctl->fills[tid], other = ctl->peer_fills[tid], n = max(mine, other);
+  // wait gave up; then one CTA may have begun a block's copies that the other
+  // has not, and the bytes that will not come are made up for.  (V of the tokens
+  // 128..255 is copied by the leader alone.)
+  if (rank == 0 && tid < 2 * kBlocks) {
+    uint64_t* const full = tid < kBlocks ? &ctl->kfull[tid] : &ctl->vfull[tid - kBlocks];
+    const uint32_t mine = ctl->fills[tid];
+    const uint32_t other = tid >= kBlocks && (tid & 2) != 0 ? mine : ctl->peer_fills[tid], n = max(mine, other);
     if (mine > other)
-      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&ctl->full[tid])), "r"(kChunkBytes) : "memory");
+      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full)), "r"(kBlockBytes) : "memory");
     else if (other > mine)
-      mbar_arrive_expect_tx(&ctl->full[tid], kChunkBytes);
-    if (n > 0) mbar_wait(&ctl->full[tid], (n - 1) & 1, kDrainWaitNs);
+      mbar_arrive_expect_tx(full, kBlockBytes);
+    if (n > 0) mbar_wait(full, (n - 1) & 1, kDrainWaitNs);
   }
   __syncthreads();
   cluster_sync();     // neither CTA leaves while the other may still signal it
