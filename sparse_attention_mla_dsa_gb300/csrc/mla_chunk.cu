@@ -633,7 +633,7 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
       const uint32_t s = tmem + kSCol + par * 128;
       const uint32_t add = t == g.begin ? 0u : 1u;
       if constexpr (!kPv) {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {              // 128 dims
           ok = ok && wait_one(ctl, &ctl->kfull[4 * par + i], phase, p);
           if (!ok) break;
@@ -648,13 +648,13 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
         }
         if (ok) commit_pair(&ctl->sfull[par]);
       } else {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {              // 128 tokens
           ok = ok && wait_one(ctl, &ctl->vfull[4 * par + 2 * h], phase, p) &&
                wait_one(ctl, &ctl->vfull[4 * par + 2 * h + 1], phase, p) && wait_one(ctl, &ctl->pready[h], par, p);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int u = 0; u < 4; ++u)              // 32 tokens
 #pragma unroll
             for (int v = 0; v < 4; ++v) {          // term v / 2, 128 dims v % 2
