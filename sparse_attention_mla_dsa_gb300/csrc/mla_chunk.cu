@@ -63,12 +63,25 @@ constexpr uint32_t kBlockOff = kQBytes + kPBytes;
 constexpr uint32_t kCtlOff = kBlockOff + kBlocks * kBlockBytes;
 constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
-constexpr int kMasks = 8;            // tiles whose token masks are kept
+constexpr int kMasks = 4;            // tiles whose token masks are kept (the copies are at most three ahead)
 constexpr int kItemCost = 2;         // an item costs what so many tiles cost, besides its tiles
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
 constexpr int kMaxPairs = 256;
+
+// What the softmax warps need of a segment, as the warp that copies K leaves it.
+struct SegRecord {
+  int64_t gline;                     // the item's first line in q and out
+  int32_t lines;                     // of the request, from the item's first on
+  int32_t ctx;                       // tokens that its new ones come after
+  int32_t first;                     // the item's first line in the request
+  int32_t begin, end;                // tiles; begin = end: the range is done
+  int32_t whole;                     // the item is in this range alone
+  int32_t parts;                     // else, where it begins here: ranges that share it
+  int32_t pad;
+};
+constexpr int kSegs = 4;
 
 // Barriers of tile t have index t & 1 (or 4 * (t & 1) + block) and phase t >> 1.
 struct __align__(16) Ctl {
@@ -80,7 +93,10 @@ struct __align__(16) Ctl {
   uint64_t qready, vseen, drain[2];
   uint32_t mask[kMasks][8];          // a bit for each token of a tile: there is a latent
   uint32_t tag[kMasks];              // 2 * (tile + 1), and 1 if every token before the item's end has one
-  uint32_t fills[2 * kBlocks], peer_fills[2 * kBlocks];  // copies begun of each block, K and V; the other CTA's
+  SegRecord seg[kSegs];
+  uint32_t segs;                     // segments left in seg[], over all
+  int more;                          // whether there is a next one: the softmax warps' common view
+  uint16_t fills[2 * kBlocks], peer_fills[2 * kBlocks];  // copies begun of each block, K and V; the other CTA's
   uint32_t tmem_base;
   int abort_flag;
   float qexp[kLines];
@@ -319,6 +335,24 @@ __device__ __forceinline__ bool warp_wait(Ctl* c, uint64_t* bar, uint32_t parity
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
+// Bounded wait of a warp until more than `seg` segments have been left.
+__device__ __forceinline__ bool wait_segment(Ctl* c, uint32_t seg, int lane, const ChunkParams& p) {
+  int ok = 1;
+  if (lane == 0) {
+    const uint64_t t0 = global_ns();
+    while (*reinterpret_cast<volatile uint32_t*>(&c->segs) <= seg) {
+      if (aborted(c) || global_ns() - t0 > p.wait_ns) {
+        if (!aborted(c)) record_error(p.err, DSA_DEVERR_TIMEOUT, -1);
+        set_abort(c);
+        ok = 0;
+        break;
+      }
+    }
+    __threadfence_block();
+  }
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
 // ------------------------------------------------------------------ tensor core
 // kind::f8f6f4, F32 accumulate, M = 128 over the pair, N = 256; A E4M3 or E5M2
 // K-major, B E4M3.
@@ -551,13 +585,44 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
 // tokens, this CTA's dims.  The leader's warps expect the bytes of both CTAs.
 template <bool kV>
 __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* blocks,
-                                     int lane, uint32_t rank, Walk w) {
+                                     int lane, uint32_t rank, int pair, int64_t per, Walk w) {
   // tokens that this warp copies: 0..127 or 128..255
   const int from = (kV ? rank == 0 : rank == 1) ? 128 : 0;
-  uint32_t looked = 0, n = 0;
+  uint32_t looked = 0, n = 0, segs = 0;
+  int64_t at = kV ? 0 : per * pair - w.off;    // cost of the call before the item
+  // K: leaves the segment for the softmax warps (at most three ahead of them: a
+  // tile's blocks are free once the O of the tile two before is complete).
+  auto publish = [&](const SegRecord& r) {
+    if (lane == 0) {
+      ctl->seg[segs % kSegs] = r;
+      __threadfence_block();
+      *reinterpret_cast<volatile uint32_t*>(&ctl->segs) = segs + 1;
+    }
+    ++segs;
+  };
   Segment g;
   while (next_segment(p, w, g)) {
     const int end = item_end(p, g.q, g.item);
+    if constexpr (!kV) {
+      SegRecord r;
+      r.first = g.item * kItem;
+      r.gline = static_cast<int64_t>(g.q.row0) * p.heads + r.first;
+      r.lines = g.q.lines - r.first;
+      r.ctx = g.q.ctx;
+      r.begin = g.begin;
+      r.end = g.end;
+      r.whole = g.begin == 0 && g.end == g.tiles ? 1 : 0;
+      // the last range that has a tile of the item, from this one on
+      r.parts = static_cast<int>((at + kItemCost + g.tiles - 1) / per - pair) + 1;
+      r.pad = 0;
+      at += g.tiles + kItemCost;
+      publish(r);
+      // its Q into L2
+      for (int k = lane; k < kLines * 8; k += 32) {
+        const int i = static_cast<int>(rank) * kLines + (k >> 3);
+        if (i < r.lines) prefetch_l2(p.q + (r.gline + i) * 512 + (k & 7) * 64);
+      }
+    }
     // K: also leaves the tile's mask and brings its latents into L2.
     auto look = [&](int t) {
       const Rows r = lookup<!kV>(p, g, end, t, lane, rank, kV ? nullptr : ctl->mask[looked % kMasks]);
@@ -591,7 +656,7 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
           if (!warp_wait(ctl, &ctl->vread[2 * (n & 1) + (i >> 1)], phase ^ 1, lane, p)) return;
         }
         if (lane == 0) {
-          ctl->fills[(kV ? kBlocks : 0) + b4 + i] = (n >> 1) + 1;
+          ctl->fills[(kV ? kBlocks : 0) + b4 + i] = static_cast<uint16_t>((n >> 1) + 1);
           if (rank == 0) mbar_arrive_expect_tx(full, kV ? kBlockBytes : 2 * kBlockBytes);
         }
         __syncwarp();
@@ -610,6 +675,7 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
       }
     }
   }
+  if constexpr (!kV) publish(SegRecord{});
 }
 
 // Leader, one thread of warps 1 and 3: the MMAs of both CTAs.  kPv false: S = Q K^T
@@ -679,17 +745,16 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
 // line that puts its largest |q| in [128, 256), negated where the logits' scale
 // is negative (so that it never is in the softmax).  Warp w converts lines w, w +
 // 16, ...; lane l dims 16l..16l+15.  Lines past the request's last are zero.
-__device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_t* qop, const Segment& g, int line0,
-                                          int sw, int lane) {
+__device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_t* qop, int64_t gline, int lines, int sw,
+                                          int lane) {
   constexpr int kPer = kLines / kSoftmaxWarps;
   uint4 qa[kPer], qb[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = sw + j * kSoftmaxWarps;
     qa[j] = qb[j] = make_uint4(0, 0, 0, 0);
-    if (line0 + i < g.q.lines) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(g.q.row0) * p.heads + line0 + i) * 512 + lane * 16);
+    if (i < lines) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (gline + i) * 512 + lane * 16);
       qa[j] = ld_dep_u4(src);
       qb[j] = ld_dep_u4(src + 1);
     }
@@ -745,7 +810,7 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
 // wait that gave up they go on with what there is, without telling the MMAs.
 __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkParams& p, Ctl* ctl, uint8_t* qop,
                                         uint8_t* pop, uint8_t* blocks, uint32_t tmem, int warp, int lane,
-                                        uint32_t rank, int pair, int64_t per, Walk w) {
+                                        uint32_t rank, int pair) {
   const int sw = warp - kSoftmaxWarp0, quarter = warp & 3, sub = sw >> 2;
   const int half = quarter >> 1, group = quarter & 1;
   const int i = group * 32 + lane;                      // line of this CTA
@@ -759,36 +824,37 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   // O of tile n is complete.  A warp that waits for tile n has seen the first half
   // of n - 1 complete, so n - 2, the phase before on n's barrier, is.
   auto wait_o = [&](uint32_t n) { return wait_all(ctl, &ctl->vread[2 * (n & 1) + 1], (n >> 1) & 1, lane, p); };
-  uint32_t ns = 0, nv = 0;                              // tiles done, masked tiles
-  int64_t begun = per * pair - w.off;
+  uint32_t ns = 0, nv = 0, seg = 0;                     // tiles, masked tiles, segments done
   bool ok = true;
-  ChunkRecord rec = {0, 0, 0};
-  Segment g, next;
-  bool more = next_segment(p, w, next);
-  if (more) {
-    convert_q(p, ctl, qop, next, next.item * kItem + static_cast<int>(rank) * kLines, sw, lane);
+  // One warp looks whether there is another segment, all go by its answer.
+  auto find_next = [&]() {
+    if (sw == 0) {
+      const bool there = wait_segment(ctl, seg, lane, p);
+      if (lane == 0) ctl->more = there && ctl->seg[seg % kSegs].end > ctl->seg[seg % kSegs].begin ? 1 : 0;
+    }
+    softmax_sync();
+    return *reinterpret_cast<volatile int*>(&ctl->more) != 0;
+  };
+  auto next_q = [&]() {
+    const SegRecord& r = ctl->seg[seg % kSegs];
+    convert_q(p, ctl, qop, r.gline + rank * kLines, r.lines - static_cast<int>(rank) * kLines, sw, lane);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive_at(qready);
-    softmax_sync();                                     // qexp
-  }
+    if (lane == 0 && ok) arrive_at(qready);
+  };
+  bool more = find_next();
+  if (more) next_q();
+  softmax_sync();                                       // qexp
   while (more) {
-    g = next;
-    more = next_segment(p, w, next);
-    if (more) {                                         // its Q, brought into L2 now
-      const int i8 = next.item * kItem + static_cast<int>(rank) * kLines + sw + (lane >> 3) * kSoftmaxWarps;
-      if (i8 < next.q.lines)
-        prefetch_l2(p.q + (static_cast<int64_t>(next.q.row0) * p.heads + i8) * 512 + (lane & 7) * 64);
-    }
-    const int line0 = g.item * kItem + static_cast<int>(rank) * kLines;
+    const SegRecord& g = ctl->seg[seg % kSegs];
     const float scale = ctl->qexp[i];
-    const int last = g.q.lines - 1;
-    const int sees = g.q.ctx + min(line0 + i, last) / p.heads + 1;                 // tokens of this line
-    const int all_see = g.q.ctx + min(g.item * kItem, last) / p.heads + 1;        // of every line of the item
-    const int64_t at = begun;                           // cost of the call before this item
-    begun += g.tiles + kItemCost;
+    const int first_tile = g.begin, tiles = g.end - g.begin;
+    const int in = min(static_cast<int>(rank) * kLines + i, g.lines - 1);
+    // tokens that this line sees of this thread's, and that every line of the item sees, from the tile on
+    int visible = g.ctx + (g.first + in) / p.heads + 1 - (first_tile * kTile + half * 128 + sub * kTok);
+    int all_see = g.ctx + g.first / p.heads + 1 - first_tile * kTile;
     float m = -INFINITY, l = 0.0f;
-    for (int t = g.begin; t < g.end; ++t, ++ns) {
+    for (int t = 0; t < tiles; ++t, ++ns, visible -= kTile, all_see -= kTile) {
       const uint32_t b = ns & 1;
       float z[kTok];
       ok &= wait_all(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
@@ -798,13 +864,12 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       if (lane == 0 && ok) arrive_at(b ? sfree1 : sfree0);
       // Left before the tile's copies began, which S waited for.
       const uint32_t tag = *reinterpret_cast<volatile uint32_t*>(&ctl->tag[ns % kMasks]);
-      const int visible = sees - (t * kTile + half * 128 + sub * kTok);   // of this thread's tokens
       uint32_t seen = visible >= kTok ? ~0u : visible <= 0 ? 0u : (1u << visible) - 1u;
       if (tag != 2 * (ns + 1) + 1) {
         __threadfence_block();
         seen &= ctl->mask[ns % kMasks][part];
       }
-      const int from = max(0, all_see - t * kTile);     // the tile's tokens from here on are hidden from some line
+      const int from = max(0, all_see);                 // the tile's tokens from here on are hidden from some line
       bool nan = false;                                 // one of them has a NaN logit
       if (from < kTile || seen != ~0u) {
         const int hidden = from - (half * 128 + sub * kTok);
@@ -832,7 +897,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
           m = tm;
           l *= alpha;
         }
-        if (t > g.begin && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+        if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
           ok &= wait_o(ns - 1);
           tc_fence_after();
 #pragma unroll 1
@@ -917,14 +982,14 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 
     // Every S of the segment is complete: the next one's Q takes its place
     // while the last P V runs, and its first S runs beside the epilogue.
+    const bool whole = g.whole != 0;
+    const int64_t gline0 = g.gline + rank * kLines;
+    const int lines = g.lines - static_cast<int>(rank) * kLines;   // of this CTA, if under 64
+    const int parts = g.parts, item_lines = min(kItem, g.lines);
     ctl->red[part][i] = l;
-    softmax_sync();                                     // l; qexp has been read
-    if (more) {
-      convert_q(p, ctl, qop, next, next.item * kItem + static_cast<int>(rank) * kLines, sw, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && ok) arrive_at(qready);
-    }
+    ++seg;
+    more = find_next();                                 // (and: l; qexp has been read)
+    if (more) next_q();
     // The line's sum in a fixed order, then its output.
     float lt = ctl->red[0][i];
 #pragma unroll
@@ -932,15 +997,13 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     softmax_sync();                                     // red[] has been read; the next qexp is there
     ok &= wait_o(ns - 1);
     tc_fence_after();
-    const bool whole = g.begin == 0 && g.end == g.tiles;
-    const int64_t gline0 = static_cast<int64_t>(g.q.row0) * p.heads + line0;
     const int d0 = half * 256 + sub * 64;
     if (whole) {
       const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
       // Through 2 KB of this warp's share of P, 32 lines x 32 dims at a time:
       // rows of 64 bytes, swizzled, which a copy then writes in whole sectors.
       uint8_t* const stage = pop + (part >> 1) * 8192 + group * 4096 + (part & 1) * 2048;
-      const bool box = ok && line0 + group * 32 + 31 <= last;
+      const bool box = ok && group * 32 + 31 < lines;
 #pragma unroll 1
       for (int k = 0; k < 64; k += 32) {
         float v[32];
@@ -961,7 +1024,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tma_store(&omap, smem_u32(stage), d0 + k, static_cast<int32_t>(gline0 + group * 32));
-        } else if (ok && line0 + i <= last) {
+        } else if (ok && i < lines) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + (gline0 + i) * 512 + d0 + k);
 #pragma unroll
           for (int d = 0; d < 4; ++d) dst[d] = o[d];
@@ -969,12 +1032,12 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         __syncwarp();
       }
       if (lane == 0) tma_store_read();
-      if (ok && part == 0 && line0 + i <= last && p.lse != nullptr)
+      if (ok && part == 0 && i < lines && p.lse != nullptr)
         p.lse[gline0 + i] = lt != 0.0f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
     } else {
       // Slot 0: the item began in an earlier range, 1: it goes on in a later one.
       // [128 groups of 4 dims][128 lines][4]: a warp's lines side by side.
-      const int slot = g.begin > 0 ? 0 : 1, pline = static_cast<int>(rank) * kLines + i;
+      const int slot = first_tile > 0 ? 0 : 1, pline = static_cast<int>(rank) * kLines + i;
       float4* dst = reinterpret_cast<float4*>(p.part_o) +
                     ((static_cast<int64_t>(pair) * 2 + slot) * 128 + d0 / 4) * kItem + pline;
 #pragma unroll 1
@@ -987,18 +1050,12 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       }
       if (part == 0)
         reinterpret_cast<float2*>(p.part_ml)[(static_cast<int64_t>(pair) * 2 + slot) * kItem + pline] = make_float2(m, lt);
-      if (slot == 1) {
-        rec.line0 = static_cast<int64_t>(g.q.row0) * p.heads + g.item * kItem;
-        rec.lines = min(kItem, g.q.lines - g.item * kItem);
-        // the last range that has a tile of the item, from this one on
-        rec.parts = static_cast<int>((at + kItemCost + g.tiles - 1) / per - pair) + 1;
-      }
+      if (slot == 1 && rank == 0 && sw == 0 && lane == 0) p.records[pair] = ChunkRecord{gline0, item_lines, parts};
     }
     tc_fence_before();
     __syncwarp();
   }
   if (lane == 0) tma_store_done();
-  if (rank == 0 && sw == 0 && lane == 0) p.records[pair] = rec;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -1032,6 +1089,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->vseen, 1);
     for (int k = 0; k < kMasks; ++k) ctl->tag[k] = 0;
     ctl->abort_flag = 0;
+    ctl->segs = 0;
     fence_mbar_init();
     tma_prefetch_map(&map);
     tma_prefetch_map(&omap);
@@ -1047,6 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const Place at = find_place<kThreads>(p, p.pairs, [&](int64_t per) { return per * pair; },
                                         reinterpret_cast<int64_t*>(smem), blockIdx.x == 0);
   Walk w;
+  if (rank == 0 && tid == 0) p.records[pair].parts = 0;  // until an item begins in this range and goes on
   w.seq = at.seq;
   w.item = at.item;
   w.off = at.off;
@@ -1057,7 +1116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    copy<false>(map, p, ctl, blocks, lane, rank, w);
+    copy<false>(map, p, ctl, blocks, lane, rank, pair, at.per, w);
   } else if (warp == 1 || warp == 3) {
     if (rank == 0 && lane == 0) {
       if (warp == 1) issue_mmas<false>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(blocks), tmem, w);
@@ -1065,15 +1124,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    copy<true>(map, p, ctl, blocks, lane, rank, w);
+    copy<true>(map, p, ctl, blocks, lane, rank, pair, at.per, w);
   } else if (warp >= kSoftmaxWarp0) {
-    softmax(omap, p, ctl, qop, pop, blocks, tmem, warp, lane, rank, pair, at.per, w);
+    softmax(omap, p, ctl, qop, pop, blocks, tmem, warp, lane, rank, pair);
   }
 
   tc_fence_before();
   __syncthreads();
   if (rank == 1 && tid < 2 * kBlocks)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "r"(ctl->fills[tid]) : "memory");
+    asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "h"(ctl->fills[tid]) : "memory");
   cluster_sync();
   // No CTA leaves with a copy of either in flight.  All are complete unless a
   // wait gave up; then one CTA may have begun a block's copies that the other
@@ -1081,11 +1140,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // 128..255 is copied by the leader alone.)
   if (rank == 0 && tid < 2 * kBlocks) {
     uint64_t* const full = tid < kBlocks ? &ctl->kfull[tid] : &ctl->vfull[tid - kBlocks];
-    const uint32_t mine = ctl->fills[tid];
-    const uint32_t other = tid >= kBlocks && (tid & 2) != 0 ? mine : ctl->peer_fills[tid], n = max(mine, other);
-    if (mine > other)
+    const uint16_t mine = ctl->fills[tid];
+    const uint16_t other = tid >= kBlocks && (tid & 2) != 0 ? mine : ctl->peer_fills[tid];
+    const int ahead = static_cast<int16_t>(mine - other);   // -1, 0 or 1
+    const uint32_t n = ahead >= 0 ? mine : other;
+    if (ahead > 0)
       asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full)), "r"(kBlockBytes) : "memory");
-    else if (other > mine)
+    else if (ahead < 0)
       mbar_arrive_expect_tx(full, kBlockBytes);
     if (n > 0) mbar_wait(full, (n - 1) & 1, kDrainWaitNs);
   }
