@@ -519,7 +519,7 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   p.heads = heads;
   p.kv_scale = kv_scale;
   p.sm_scale = sm_scale;
-  p.pairs = dev->num_sms / 2;
+  p.pairs = mla_chunk_pairs(seqs, rows, heads, dev->num_sms);
   p.box_rows = mla_chunk_box_rows(seqs->block_size);
   // Latent pool [nslots][512] bytes; boxes of 128 bytes (the swizzle span) by
   // box_rows rows, or one for gathers; rows outside the pool read as zero.

@@ -215,6 +215,8 @@ struct ChunkParams {
   float sm_scale;
 };
 int mla_chunk_box_rows(int block_size);
+// Pairs of a call: one for every two SMs, or for every tile that it can have.
+int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms);
 size_t mla_chunk_workspace_bytes(int pairs);
 // `map` describes the latent pool [nslots][512] bytes for 128-byte x box_rows
 // copies (1-row boxes where they are gathered), `omap` the output [rows * heads]

@@ -69,6 +69,7 @@ constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ..
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
 constexpr int kMaxPairs = 256;
+static_assert(kMaxPairs == kMergeThreads, "a merge thread for every pair");
 
 // What the softmax warps need of a segment, as the warp that copies K leaves it.
 struct SegRecord {
@@ -1158,13 +1159,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds up the parts of the items that several ranges share.  A unit is 64 lines
-// x kDims groups of 4 dims of one item; four threads have a line and take every
-// fourth part, then are added up in order.  CTAs take units in turn.
+// Adds up the parts of the items that several ranges share.  Few parts: a
+// thread has a line and kDims groups of 4 dims, and adds the parts in order.
 template <int kDims>
-__device__ __forceinline__ void merge_unit(const ChunkParams& p, const ChunkRecord& r, int first, int half, int d4,
-                                           float4 (&x_acc)[3][kDims][64], float2 (&x_ml)[3][64]) {
-  const int i = threadIdx.x & 63, set = threadIdx.x >> 6, line = half * 64 + i;
+__device__ __forceinline__ void merge_few(const ChunkParams& p, const ChunkRecord& r, int first, int line, int d4) {
+  if (line >= r.lines) return;
   // part 0 in slot 1 of its pair, the others in slot 0 of theirs
   auto slot = [&](int u) { return static_cast<int64_t>(first + u) * 2 + (u == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + line;
@@ -1173,44 +1172,100 @@ __device__ __forceinline__ void merge_unit(const ChunkParams& p, const ChunkReco
   float4 acc[kDims];
 #pragma unroll
   for (int d = 0; d < kDims; ++d) acc[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kBatch = kDims > 2 ? 2 : 8;             // parts in flight
+  for (int u0 = 0; u0 < r.parts; u0 += 2) {             // two in flight
+    float2 x[2];
+    float4 v[2][kDims];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int u = min(u0 + k, r.parts - 1);
+      x[k] = ld_dep_f2(ml + slot(u) * kItem);
+      if (u0 + k >= r.parts) x[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) v[k][d] = ld_dep_f4(o + (slot(u) * 128 + d) * kItem);
+    }
+    const float top = fmaxf(m, fmaxf(x[0].x, x[1].x));
+    const float base = top == -INFINITY ? 0.0f : top;   // (no weight yet: 0 times a sum that may be NaN)
+    const float a = ex2(m - base), w0 = ex2(x[0].x - base), w1 = ex2(x[1].x - base);
+    m = top;
+    l = l * a + w0 * x[0].y + w1 * x[1].y;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      acc[d].x = acc[d].x * a + w0 * v[0][d].x + w1 * v[1][d].x;
+      acc[d].y = acc[d].y * a + w0 * v[0][d].y + w1 * v[1][d].y;
+      acc[d].z = acc[d].z * a + w0 * v[0][d].z + w1 * v[1][d].z;
+      acc[d].w = acc[d].w * a + w0 * v[0][d].w + w1 * v[1][d].w;
+    }
+  }
+  const float inv = l != l ? l : (m != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
+  const int64_t gline = r.line0 + line;
+  uint4* out = reinterpret_cast<uint4*>(p.out + gline * 512 + d4 * 4);
+#pragma unroll
+  for (int d = 0; d < kDims; d += 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * k]) : "f"(acc[d + k].y * inv), "f"(acc[d + k].x * inv));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * k + 1]) : "f"(acc[d + k].w * inv), "f"(acc[d + k].z * inv));
+    }
+    out[d / 2] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (d4 == 0 && p.lse != nullptr)
+    p.lse[gline] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Many parts: four threads have a line and 8 dims and take every fourth part,
+// eight in flight, then are added up in order.
+__device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkRecord& r, int first, int half, int d4,
+                                           float4 (&x_acc)[3][2][64], float2 (&x_ml)[3][64]) {
+  constexpr int kDims = 2, kBatch = 8;
+  const int i = threadIdx.x & 63, set = threadIdx.x >> 6, line = half * 64 + i;
+  auto slot = [&](int u) { return static_cast<int64_t>(first + u) * 2 + (u == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + line;
+  const float4* o = reinterpret_cast<const float4*>(p.part_o) + static_cast<int64_t>(d4) * kItem + line;
+  float m = -INFINITY, l = 0.0f;
+  float4 acc[kDims];
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) acc[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float mk, float lk, const float4 (&v)[kDims], float base) {
+    const float w = ex2(mk - base);
+    l += w * lk;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      acc[d].x += w * v[d].x;
+      acc[d].y += w * v[d].y;
+      acc[d].z += w * v[d].z;
+      acc[d].w += w * v[d].w;
+    }
+  };
+  auto scale_by = [&](float a) {
+    l *= a;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) {
+      acc[d].x *= a;
+      acc[d].y *= a;
+      acc[d].z *= a;
+      acc[d].w *= a;
+    }
+  };
   for (int u0 = set; u0 < r.parts; u0 += 4 * kBatch) {
     float2 x[kBatch];
     float4 v[kBatch][kDims];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int u = u0 + 4 * k;
-      if (u < r.parts) {
-        x[k] = ld_dep_f2(ml + slot(u) * kItem);
+      const int u = min(u0 + 4 * k, r.parts - 1);
+      x[k] = ld_dep_f2(ml + slot(u) * kItem);
+      if (u0 + 4 * k >= r.parts) x[k] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int d = 0; d < kDims; ++d) v[k][d] = ld_dep_f4(o + (slot(u) * 128 + d) * kItem);
-      } else {
-        x[k] = make_float2(-INFINITY, 0.0f);
-#pragma unroll
-        for (int d = 0; d < kDims; ++d) v[k][d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+      for (int d = 0; d < kDims; ++d) v[k][d] = ld_dep_f4(o + (slot(u) * 128 + d) * kItem);
     }
     float top = m;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) top = fmaxf(top, x[k].x);
-    const float base = top == -INFINITY ? 0.0f : top;   // (no weight yet: 0 times a sum that may be NaN)
-    const float a = ex2(m - base);
+    const float base = top == -INFINITY ? 0.0f : top;
+    scale_by(ex2(m - base));
     m = top;
-    l *= a;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-      acc[d].x *= a; acc[d].y *= a; acc[d].z *= a; acc[d].w *= a;
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float wgt = ex2(x[k].x - base);
-      l += wgt * x[k].y;
-#pragma unroll
-      for (int d = 0; d < kDims; ++d) {
-        acc[d].x += wgt * v[k][d].x; acc[d].y += wgt * v[k][d].y;
-        acc[d].z += wgt * v[k][d].z; acc[d].w += wgt * v[k][d].w;
-      }
-    }
+    for (int k = 0; k < kBatch; ++k) add(x[k].x, x[k].y, v[k], base);
   }
   __syncthreads();                                      // the unit before has been read
   if (set > 0) {
@@ -1224,55 +1279,74 @@ __device__ __forceinline__ void merge_unit(const ChunkParams& p, const ChunkReco
 #pragma unroll
   for (int k = 0; k < 3; ++k) top = fmaxf(top, x_ml[k][i].x);
   const float base = top == -INFINITY ? 0.0f : top;
-  const float a = ex2(m - base);
-  l *= a;
-#pragma unroll
-  for (int d = 0; d < kDims; ++d) {
-    acc[d].x *= a; acc[d].y *= a; acc[d].z *= a; acc[d].w *= a;
-  }
+  scale_by(ex2(m - base));
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    const float wgt = ex2(x_ml[k][i].x - base);
-    l += wgt * x_ml[k][i].y;
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-      const float4 v = x_acc[k][d][i];
-      acc[d].x += wgt * v.x; acc[d].y += wgt * v.y; acc[d].z += wgt * v.z; acc[d].w += wgt * v.w;
-    }
+    const float4 v[kDims] = {x_acc[k][0][i], x_acc[k][1][i]};
+    add(x_ml[k][i].x, x_ml[k][i].y, v, base);
   }
   const float inv = l != l ? l : (top != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
   const int64_t gline = r.line0 + line;
+  uint32_t w[4];
 #pragma unroll
   for (int d = 0; d < kDims; ++d) {
-    uint32_t o2[2];
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2[0]) : "f"(acc[d].y * inv), "f"(acc[d].x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o2[1]) : "f"(acc[d].w * inv), "f"(acc[d].z * inv));
-    *reinterpret_cast<uint2*>(p.out + gline * 512 + (d4 + d) * 4) = make_uint2(o2[0], o2[1]);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * d]) : "f"(acc[d].y * inv), "f"(acc[d].x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * d + 1]) : "f"(acc[d].w * inv), "f"(acc[d].z * inv));
   }
+  *reinterpret_cast<uint4*>(p.out + gline * 512 + d4 * 4) = make_uint4(w[0], w[1], w[2], w[3]);
   if (d4 == 0 && p.lse != nullptr)
     p.lse[gline] = l != 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 8 of
+// one with many (few items then, which have to reach every SM).
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
+  constexpr int kFew = 8;
   __shared__ ChunkRecord rec[kMaxPairs];
-  __shared__ float4 x_acc[3][8][64];
+  __shared__ int begin[kMaxPairs + 1];                  // first unit of each pair's record
+  __shared__ float4 x_acc[3][2][64];
   __shared__ float2 x_ml[3][64];
+  const int tid = threadIdx.x, lane = tid & 31;
   grid_dep_launch();
   grid_dep_wait();
-  for (int k = threadIdx.x; k < p.pairs; k += kMergeThreads) rec[k] = p.records[k];
+  int units = 0;
+  if (tid < p.pairs) {
+    const ChunkRecord r = p.records[tid];
+    rec[tid] = r;
+    if (r.parts > 1) units = (r.lines > 64 ? 2 : 1) * (r.parts > kFew ? 64 : 8);
+  }
+  if (!__syncthreads_or(units)) return;
+  begin[tid] = units;
   __syncthreads();
-  // Many parts (few items, long): narrow units, so that they reach every SM.
-  int unit = blockIdx.x;
-  for (int k = 0; k < p.pairs; ++k) {
-    const ChunkRecord r = rec[k];
-    if (r.parts < 2) continue;
-    const int halves = r.lines > 64 ? 2 : 1, n = halves * (r.parts > 8 ? 64 : 16);
-    for (; unit < n; unit += gridDim.x) {
-      const int half = halves == 2 ? unit & 1 : 0, at = halves == 2 ? unit >> 1 : unit;
-      if (r.parts > 8) merge_unit<2>(p, r, k, half, at * 2, reinterpret_cast<float4(&)[3][2][64]>(x_acc), x_ml);
-      else merge_unit<8>(p, r, k, half, at * 8, x_acc, x_ml);
+  if (tid < 32) {                                       // exclusive sums
+    constexpr int kPer = kMaxPairs / 32;
+    int mine = 0;
+    for (int k = 0; k < kPer; ++k) mine += begin[lane * kPer + k];
+    int x = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
     }
-    unit -= n;
+    int at = x - mine;
+    for (int k = 0; k < kPer; ++k) {
+      const int v = begin[lane * kPer + k];
+      begin[lane * kPer + k] = at;
+      at += v;
+    }
+    if (lane == 31) begin[kMaxPairs] = at;
+  }
+  __syncthreads();
+  for (int unit = blockIdx.x; unit < begin[kMaxPairs]; unit += gridDim.x) {
+    int lo = 0, hi = kMaxPairs;                         // begin[lo] <= unit < begin[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (begin[mid] <= unit) lo = mid; else hi = mid;
+    }
+    const ChunkRecord r = rec[lo];
+    const int at = unit - begin[lo];
+    const int half = r.lines > 64 ? at & 1 : 0, d = r.lines > 64 ? at >> 1 : at;
+    if (r.parts > kFew) merge_many(p, r, lo, half, d * 2, x_acc, x_ml);
+    else merge_few<4>(p, r, lo, half * 64 + (tid & 63), d * 16 + (tid >> 6) * 4);
   }
 }
 
@@ -1291,6 +1365,15 @@ int mla_chunk_box_rows(int block_size) {
   int h = 64;
   while (block_size % h != 0) h >>= 1;
   return h >= 8 ? h : 0;
+}
+
+// What the host knows of the work: a call that can only have one tile (a first
+// token at few heads) is one pair, with nothing to merge: 20 us become 14.
+int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms) {
+  const int64_t items = static_cast<int64_t>(rows) * heads / kItem + (seqs->seqs < rows ? seqs->seqs : rows);
+  const int64_t tiles = (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq + kTile - 1) / kTile;
+  const int64_t pairs = num_sms / 2;
+  return static_cast<int>(items * tiles < pairs ? items * tiles : pairs);
 }
 
 cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& omap, void* workspace,

@@ -14,6 +14,8 @@
 // entry that another CTA appends is computed, not read.  Only the state kept in
 // place (held, the stack's count) has to change after every CTA has read it:
 // the CTA that takes the last ticket writes it.
+#include <algorithm>
+
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
 
@@ -22,8 +24,11 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-// Row-table entries per CTA that are worth another CTA's scan of the requests.
-constexpr int kEntriesPerCta = 8192;
+// Row-table entries of a warp's turn: kSpan of one row, all loads in flight
+// before the first store (a turn of one load at a time, 33 for a row of 1,025
+// entries, took 24 us for 32 rows where this takes 8).
+constexpr int kSpan = 512;
+constexpr int kPer = kSpan / 32;
 
 struct Shared {
   int warp_sum[3][kWarps];
@@ -223,11 +228,35 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     if (p.row_seq != nullptr) p.row_seq[r] = s;
   }
   if (p.row_table == nullptr) return;
-  for (int r = gwarp; r < out_rows; r += nwarps) {
-    const int s = find(sc.rows, n, r);
-    const int need = refused(s) ? 0 : max(0, sc.need[s]);
-    int32_t* row = p.row_table + static_cast<int64_t>(r) * p.row_bt_stride;
-    for (int b = lane; b < p.max_blocks_per_seq; b += 32) row[b] = b < need ? entry(s, b) : -1;
+  // A warp's turn is kSpan entries of `run` consecutive rows, whose request's
+  // entries are loaded once; single rows while there are warps to spare.
+  const int width = p.max_blocks_per_seq, spans = (width + kSpan - 1) / kSpan;
+  const int run = static_cast<int64_t>(out_rows) * spans >= 16ll * nwarps ? 4 : 1;
+  const int turns = (out_rows + run - 1) / run * spans;
+  for (int turn = gwarp; turn < turns; turn += nwarps) {
+    const int r0 = turn / spans * run, b0 = turn % spans * kSpan + lane;
+    const int r1 = min(r0 + run, out_rows);
+    int s = find(sc.rows, n, r0), need = 0, kept_blocks = 0;
+    int v[kPer];
+    for (int r = r0; r < r1; ++r) {
+      if (r == r0 || sc.rows[s + 1] <= r) {
+        while (sc.rows[s + 1] <= r) ++s;
+        need = refused(s) ? 0 : max(0, sc.need[s]);
+        kept_blocks = min(max(0, sc.held[s]), need);
+        const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = b0 + 32 * k < kept_blocks ? row[b0 + 32 * k] : -1;
+      }
+      int32_t* row = p.row_table + static_cast<int64_t>(r) * p.row_bt_stride;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int b = b0 + 32 * k;
+        if (b < width && (b < kept_blocks || b >= need)) row[b] = v[k];
+      }
+      // The entries taken in this call: few, and in few of the spans.
+      for (int b = max(kept_blocks, b0 - lane) + lane; b < min(need, b0 - lane + kSpan); b += 32)
+        row[b] = pop(sc.want[s] + (b - kept_blocks));
+    }
   }
 }
 
@@ -240,9 +269,10 @@ cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t 
         plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int64_t entries = static_cast<int64_t>(p.p.rows) *
-                          (p.p.row_table != nullptr ? p.p.max_blocks_per_seq : 16);
-  int64_t ctas = (entries + kEntriesPerCta - 1) / kEntriesPerCta;
+  // A CTA for every 16 warps' turns (or 512 rows), up to one a SM: each scans
+  // all requests.
+  const int64_t spans = p.p.row_table != nullptr ? (p.p.max_blocks_per_seq + kSpan - 1) / kSpan : 0;
+  int64_t ctas = std::max((p.p.rows * spans + kWarps - 1) / kWarps, static_cast<int64_t>((p.p.rows + kThreads - 1) / kThreads));
   if (ctas > num_sms) ctas = num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
