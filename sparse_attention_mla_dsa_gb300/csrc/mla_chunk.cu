@@ -1388,7 +1388,7 @@ cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtens
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.pairs, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.pairs), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;

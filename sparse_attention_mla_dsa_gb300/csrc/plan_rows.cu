@@ -22,16 +22,15 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-// Row-table entries of a warp's turn: kSpan of one row, all loads in flight
-// before the first store (a turn of one load at a time, 33 for a row of 1,025
-// entries, took 24 us for 32 rows where this takes 8).
+// Row-table entries of a warp's turn, all loads in flight before the first
+// store.
 constexpr int kSpan = 512;
 constexpr int kPer = kSpan / 32;
 
 struct Shared {
-  int warp_sum[3][kWarps];
+  int warp_sum[3][32];
   int taken;  // blocks taken from the stack by the requests that are served
   int last;
 };
@@ -110,9 +109,10 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     if (s < n) {
       const int len = p.seq_lens[s], fresh = p.new_tokens[s];
       held = p.held_in[s];
-      const int64_t blocks = (static_cast<int64_t>(len) + p.block_size - 1) / p.block_size;
       const bool rows_ok = fresh >= 0 && fresh <= p.rows;
-      if (rows_ok && fresh <= len && blocks <= p.max_blocks_per_seq && held >= 0 &&
+      // (32 bits hold the sum of a length and a block size)
+      const uint32_t blocks = (static_cast<uint32_t>(len) + (p.block_size - 1)) / static_cast<uint32_t>(p.block_size);
+      if (rows_ok && fresh <= len && blocks <= static_cast<uint32_t>(p.max_blocks_per_seq) && held >= 0 &&
           held <= p.max_blocks_per_seq) {
         need = static_cast<int>(blocks);
         v[1] = max(0, need - held);
@@ -229,33 +229,55 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
   }
   if (p.row_table == nullptr) return;
   // A warp's turn is kSpan entries of `run` consecutive rows, whose request's
-  // entries are loaded once; single rows while there are warps to spare.
+  // entries are looked up and loaded once; single rows while there are warps to
+  // spare (12,000 rows of 1,031 entries: 25.1 us by single rows, 15.4 by fours,
+  // where a fill of the tables takes 7.2).
   const int width = p.max_blocks_per_seq, spans = (width + kSpan - 1) / kSpan;
-  const int run = static_cast<int64_t>(out_rows) * spans >= 16ll * nwarps ? 4 : 1;
+  const int run = static_cast<int64_t>(out_rows) * spans >= 4ll * nwarps ? 4 : 1;
   const int turns = (out_rows + run - 1) / run * spans;
+  constexpr uint32_t kAll = (1u << kPer) - 1u;
+  // Entries base + 32 k + lane of a span that are below x.
+  auto below = [&](int base, int x) {
+    const int m = (x - base - lane + 31) >> 5;          // k < m
+    return m >= kPer ? kAll : m <= 0 ? 0u : (1u << m) - 1u;
+  };
   for (int turn = gwarp; turn < turns; turn += nwarps) {
-    const int r0 = turn / spans * run, b0 = turn % spans * kSpan + lane;
+    const int r0 = turn / spans * run, base = turn % spans * kSpan;
     const int r1 = min(r0 + run, out_rows);
-    int s = find(sc.rows, n, r0), need = 0, kept_blocks = 0;
+    const uint32_t in = below(base, width);
+    int s = find(sc.rows, n, r0), need = 0, kept_blocks = 0, fresh = -1;
     int v[kPer];
+    uint32_t put = 0;                                   // entries to be written from v
     for (int r = r0; r < r1; ++r) {
       if (r == r0 || sc.rows[s + 1] <= r) {
         while (sc.rows[s + 1] <= r) ++s;
         need = refused(s) ? 0 : max(0, sc.need[s]);
         kept_blocks = min(max(0, sc.held[s]), need);
-        const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride;
+        const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride + base + lane;
+        const uint32_t old = below(base, kept_blocks);
+        if (__all_sync(0xFFFFFFFFu, old == kAll)) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) v[k] = b0 + 32 * k < kept_blocks ? row[b0 + 32 * k] : -1;
+          for (int k = 0; k < kPer; ++k) v[k] = row[32 * k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) v[k] = (old >> k) & 1u ? row[32 * k] : -1;
+        }
+        put = in & (old | ~below(base, need));
+        if (kept_blocks + lane < need && kept_blocks < base + kSpan && base < need) fresh = pop(sc.want[s] + lane);
       }
       int32_t* row = p.row_table + static_cast<int64_t>(r) * p.row_bt_stride;
+      int32_t* to = row + base + lane;
+      if (__all_sync(0xFFFFFFFFu, put == kAll)) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int b = b0 + 32 * k;
-        if (b < width && (b < kept_blocks || b >= need)) row[b] = v[k];
+        for (int k = 0; k < kPer; ++k) to[32 * k] = v[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if ((put >> k) & 1u) to[32 * k] = v[k];
       }
       // The entries taken in this call: few, and in few of the spans.
-      for (int b = max(kept_blocks, b0 - lane) + lane; b < min(need, b0 - lane + kSpan); b += 32)
-        row[b] = pop(sc.want[s] + (b - kept_blocks));
+      for (int b = kept_blocks + lane; b < min(need, base + kSpan); b += 32)
+        if (b >= base) row[b] = b < kept_blocks + 32 ? fresh : pop(sc.want[s] + (b - kept_blocks));
     }
   }
 }
@@ -269,7 +291,7 @@ cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t 
         plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  // A CTA for every 16 warps' turns (or 512 rows), up to one a SM: each scans
+  // A CTA for every 32 warps' turns (or 1,024 rows), up to one a SM: each scans
   // all requests.
   const int64_t spans = p.p.row_table != nullptr ? (p.p.max_blocks_per_seq + kSpan - 1) / kSpan : 0;
   int64_t ctas = std::max((p.p.rows * spans + kWarps - 1) / kWarps, static_cast<int64_t>((p.p.rows + kThreads - 1) / kThreads));
