@@ -23,14 +23,15 @@
 // its 64 lines of Q and its 128 tokens of the tile (all 512 dims), for O += P V
 // its 64 lines of P and its 256 dims of V (all 256 tokens).
 //
-// Copies.  An SM takes in 32 bytes a clock from L2 (62 GB/s measured, on every
-// SM), so K and V copied apart, 128 KB a tile, would take the 4,100 clocks of the
-// tile's MMAs.  Half of a CTA's V is half of its K: its tokens, its dims.  A
-// 16 KB block is 128 tokens x 128 dims for both uses (K-major for S, MN-major for
-// O), and both CTAs' MMAs read the same places, so a tile has four blocks: K in
-// all four, and once S has read them V of the tokens 0..127 in the first two and
-// of 128..255 in the last two, of which each CTA only has to copy the two that
-// are not its own tokens.  96 KB a tile, and two tiles in flight.
+// Copies.  A block of 16 KB is 128 tokens x 128 dims, K-major for S and MN-major
+// for O; a tile has four of K and four of V a CTA, taken again as soon as the
+// MMAs have read them.  An SM takes in 32 bytes a clock from L2 (62 GB/s measured,
+// on every SM), so these 128 KB cost the 4,100 clocks that the tile's MMAs take.
+// Keeping the two K blocks that are also V (a CTA's tokens, its dims) and copying
+// 96 KB measured slower but for gathered pages (prompt of 1,024 rows 731 -> 775
+// us): a block then lives from its copy to the end of O, and two tiles' blocks
+// fill the shared memory, so that load, S, softmax and O of a tile follow each
+// other.
 //
 // Precision.  The latents stay E4M3.  q * 2^s = hi + lo, two E4M3 terms, holds
 // a bf16 q exactly but for elements 2^10 below the head's largest; a softmax
@@ -55,7 +56,7 @@ constexpr int kItem = 128;           // lines of an item (MMA M over the pair)
 constexpr int kLines = 64;           // lines of a CTA
 constexpr int kTile = 256;           // tokens of a tile
 constexpr int kTok = 32;             // tokens of a softmax thread
-constexpr int kBlocks = 8;           // of 128 tokens x 128 dims; four a tile, for two tiles
+constexpr int kBlocks = 8;           // of 128 tokens x 128 dims: four of K, four of V
 constexpr uint32_t kBlockBytes = 16384;
 constexpr uint32_t kQBytes = 65536;  // [term][128-dim block][64 lines][128 B]
 constexpr uint32_t kPBytes = 32768;  // [term][128-token half][64 lines][128 B]
@@ -63,7 +64,7 @@ constexpr uint32_t kBlockOff = kQBytes + kPBytes;
 constexpr uint32_t kCtlOff = kBlockOff + kBlocks * kBlockBytes;
 constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
-constexpr int kMasks = 4;            // tiles whose token masks are kept (the copies are at most three ahead)
+constexpr int kMasks = 8;            // tiles whose token masks are kept (the copies are up to four ahead)
 constexpr int kItemCost = 2;         // an item costs what so many tiles cost, besides its tiles
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
@@ -84,10 +85,10 @@ struct SegRecord {
 };
 constexpr int kSegs = 4;
 
-// Barriers of tile t have index t & 1 (or 4 * (t & 1) + block) and phase t >> 1.
+// Barriers of tile t; where no phase is given, index t & 1 and phase t >> 1.
 struct __align__(16) Ctl {
-  uint64_t kfull[kBlocks], vfull[kBlocks];  // leader: copies have landed, in both CTAs
-  uint64_t kread[kBlocks];           // S has read the block
+  uint64_t kfull[4], vfull[4];       // leader: copies have landed, in both CTAs (phase: t)
+  uint64_t kread[4];                 // S has read the block (phase: t)
   uint64_t vread[4];                 // O has read V and P of the tokens 0..127, 128..255 (2 * (t & 1) + half)
   uint64_t sfull[2], sfree[2];
   uint64_t pready[2];                // P of the tile's first and second 128 tokens (index: half, phase: t)
@@ -97,7 +98,7 @@ struct __align__(16) Ctl {
   SegRecord seg[kSegs];
   uint32_t segs;                     // segments left in seg[], over all
   int more;                          // whether there is a next one: the softmax warps' common view
-  uint16_t fills[2 * kBlocks], peer_fills[2 * kBlocks];  // copies begun of each block, K and V; the other CTA's
+  uint16_t fills[kBlocks], peer_fills[kBlocks];  // copies begun of each block; the other CTA's
   uint32_t tmem_base;
   int abort_flag;
   float qexp[kLines];
@@ -582,13 +583,14 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
 }
 
 // Warp 0: this CTA's 128 tokens of every tile's K, a block for each 128 dims.
-// Warp 2 (kV): the two blocks of V that are not among them: the other CTA's
-// tokens, this CTA's dims.  The leader's warps expect the bytes of both CTAs.
+// Warp 2 (kV): the tile's V, all tokens and this CTA's 256 dims, a block for each
+// 128 tokens x 128 dims.  The leader's warps expect the bytes of both CTAs.  Each
+// has its own blocks: one warp alone fills a block, as a barrier's parity says
+// nothing to a warp that may be two fills behind.
 template <bool kV>
 __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* blocks,
                                      int lane, uint32_t rank, int pair, int64_t per, Walk w) {
-  // tokens that this warp copies: 0..127 or 128..255
-  const int from = (kV ? rank == 0 : rank == 1) ? 128 : 0;
+  const int from = rank ? 128 : 0;             // K: the tokens of this CTA
   uint32_t looked = 0, n = 0, segs = 0;
   int64_t at = kV ? 0 : per * pair - w.off;    // cost of the call before the item
   // K: leaves the segment for the softmax warps (at most three ahead of them: a
@@ -644,33 +646,31 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
     for (int t = g.begin; t < g.end; ++t, ++n) {
       const Rows r = next;
       if (t + 1 < g.end) next = look(t + 1);   // before the waits of this tile
-      const uint32_t b4 = 4 * (n & 1), phase = (n >> 1) & 1;
       for (int i = 0; i < 4; ++i) {
-        // V of the tokens 0..127 goes to the first two blocks, of the others to
-        // the last two; the leader expects what the other CTA copies.
-        const bool mine = !kV || (i >= 2) == (from != 0);
-        if (!mine && rank != 0) continue;
-        uint64_t* const full = kV ? &ctl->vfull[b4 + i] : &ctl->kfull[b4 + i];
-        if (kV) {
-          if (!warp_wait(ctl, &ctl->kread[b4 + i], phase, lane, p)) return;
-        } else if (n >= 2 && (i & 1) == 0) {
-          if (!warp_wait(ctl, &ctl->vread[2 * (n & 1) + (i >> 1)], phase ^ 1, lane, p)) return;
+        uint64_t* const full = kV ? &ctl->vfull[i] : &ctl->kfull[i];
+        if (n >= 1) {
+          const uint32_t before = n - 1;
+          if (!kV) {
+            if (!warp_wait(ctl, &ctl->kread[i], before & 1, lane, p)) return;
+          } else if ((i & 1) == 0) {
+            if (!warp_wait(ctl, &ctl->vread[2 * (before & 1) + (i >> 1)], (before >> 1) & 1, lane, p)) return;
+          }
         }
         if (lane == 0) {
-          ctl->fills[(kV ? kBlocks : 0) + b4 + i] = static_cast<uint16_t>((n >> 1) + 1);
-          if (rank == 0) mbar_arrive_expect_tx(full, kV ? kBlockBytes : 2 * kBlockBytes);
+          ctl->fills[(kV ? 4 : 0) + i] = static_cast<uint16_t>(n + 1);
+          if (rank == 0) mbar_arrive_expect_tx(full, 2 * kBlockBytes);
         }
         __syncwarp();
-        if (!mine) continue;
-        const uint32_t dst = smem_u32(blocks + (b4 + i) * kBlockBytes), bar = map_to(full, 0);
+        const uint32_t dst = smem_u32(blocks + ((kV ? 4 : 0) + i) * kBlockBytes), bar = map_to(full, 0);
         const int x = kV ? static_cast<int>(rank) * 256 + (i & 1) * 128 : i * 128;
+        const int f = kV ? (i >> 1) * 128 : from;
         if (p.box_rows > 0) {
-          const int tok = lane * p.box_rows - from;
+          const int tok = lane * p.box_rows - f;
           if (tok >= 0 && tok < 128) tma_box(dst + tok * 128, &map, bar, x, r.at[0]);
         } else {
           int32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = from ? r.at[4 + k] : r.at[k];
+          for (int k = 0; k < 4; ++k) y[k] = f ? r.at[4 + k] : r.at[k];
           tma_gather4(dst + lane * 512, &map, bar, x, y);
         }
       }
@@ -695,14 +695,14 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
     ++nq;
     for (int t = g.begin; t < g.end && ok; ++t, ++n) {
       const uint32_t par = n & 1, phase = (n >> 1) & 1;
-      const uint32_t b0 = desc_low(block0) + par * 4096;
+      const uint32_t b0 = desc_low(block0) + (kPv ? 4096u : 0u);
       if (!kPv && n >= 2) ok = wait_one(ctl, &ctl->sfree[par], phase ^ 1, p);
       const uint32_t s = tmem + kSCol + par * 128;
       const uint32_t add = t == g.begin ? 0u : 1u;
       if constexpr (!kPv) {
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {              // 128 dims
-          ok = ok && wait_one(ctl, &ctl->kfull[4 * par + i], phase, p);
+          ok = ok && wait_one(ctl, &ctl->kfull[i], par, p);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -711,14 +711,14 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
             for (int v = 0; v < 2; ++v)            // term
               mma_pair<idesc_f8(false, false)>(s, a0 + (v * 4 + i) * 512 + u * 2, b0 + i * 1024 + u * 2,
                                                (i | u | v) != 0 ? 1u : 0u);
-          commit_pair(&ctl->kread[4 * par + i]);
+          commit_pair(&ctl->kread[i]);
         }
         if (ok) commit_pair(&ctl->sfull[par]);
       } else {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {              // 128 tokens
-          ok = ok && wait_one(ctl, &ctl->vfull[4 * par + 2 * h], phase, p) &&
-               wait_one(ctl, &ctl->vfull[4 * par + 2 * h + 1], phase, p) && wait_one(ctl, &ctl->pready[h], par, p);
+          ok = ok && wait_one(ctl, &ctl->vfull[2 * h], par, p) && wait_one(ctl, &ctl->vfull[2 * h + 1], par, p) &&
+               wait_one(ctl, &ctl->pready[h], par, p);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -858,7 +858,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     for (int t = 0; t < tiles; ++t, ++ns, visible -= kTile, all_see -= kTile) {
       const uint32_t b = ns & 1;
       float z[kTok];
-      ok &= wait_all(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
+      ok = ok && wait_all(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
       tc_fence_after();
       tmem_load32(scol + b * 128, z);
       tc_fence_before();
@@ -899,7 +899,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
           l *= alpha;
         }
         if (t > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-          ok &= wait_o(ns - 1);
+          ok = ok && wait_o(ns - 1);
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < 64; k += 32) {
@@ -937,7 +937,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       // This half of P has been read: the MMAs take the tile's first 128 tokens
       // first, so it is written again while those of the second half run.
-      if (ns > 0) ok &= wait_all(ctl, &ctl->vread[2 * ((ns - 1) & 1) + half], ((ns - 1) >> 1) & 1, lane, p);
+      if (ns > 0) ok = ok && wait_all(ctl, &ctl->vread[2 * ((ns - 1) & 1) + half], ((ns - 1) >> 1) & 1, lane, p);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int at = ((sub * 2 + k) ^ (i & 7)) * 16;
@@ -954,17 +954,18 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       if (from < kTile) {
         const bool patch = line_sync_or(group, nan);
         if (rank == 0 && (patch || sw == 0)) {
-          for (int v = 0; v < 4; ++v) ok &= warp_wait(ctl, &ctl->vfull[4 * b + v], (ns >> 1) & 1, lane, p);
+          if (ns > 0) ok = ok && wait_o(ns - 1);             // (the V before has landed, too)
+          for (int v = 0; v < 4; ++v) ok = ok && warp_wait(ctl, &ctl->vfull[v], ns & 1, lane, p);
           if (sw == 0 && lane == 0) arrive_release_at(map_to(&ctl->vseen, 1));
         } else if (rank == 1 && patch) {
-          ok &= warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
+          ok = ok && warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
           acquire_cluster();
         }
         ++nv;
         if (patch) {
           for (int v = from / 128 * 2; v < 4; ++v) {    // block: 128 tokens x 128 dims
             const int r0 = max(0, from - (v >> 1) * 128), units = (128 - r0) * 8;
-            uint4* rows = reinterpret_cast<uint4*>(blocks + (4 * b + v) * kBlockBytes) + r0 * 8;
+            uint4* rows = reinterpret_cast<uint4*>(blocks + (4 + v) * kBlockBytes) + r0 * 8;
             for (int u = part * 32 + lane; u < units; u += kSoftmaxThreads / 2) {
               const uint4 x = rows[u];
               const uint4 y = make_uint4(zero_nan4(x.x), zero_nan4(x.y), zero_nan4(x.z), zero_nan4(x.w));
@@ -996,7 +997,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 #pragma unroll
     for (int k = 1; k < 8; ++k) lt += ctl->red[k][i];
     softmax_sync();                                     // red[] has been read; the next qexp is there
-    ok &= wait_o(ns - 1);
+    ok = ok && wait_o(ns - 1);
     tc_fence_after();
     const int d0 = half * 256 + sub * 64;
     if (whole) {
@@ -1073,13 +1074,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int k = 0; k < kBlocks; ++k) {
+    for (int k = 0; k < 4; ++k) {
       mbar_init(&ctl->kfull[k], 1);
       mbar_init(&ctl->vfull[k], 1);
       mbar_init(&ctl->kread[k], 1);
+      mbar_init(&ctl->vread[k], 1);
     }
-    for (int k = 0; k < 2 * kBlocks; ++k) ctl->fills[k] = 0;
-    for (int k = 0; k < 4; ++k) mbar_init(&ctl->vread[k], 1);
+    for (int k = 0; k < kBlocks; ++k) ctl->fills[k] = 0;
     for (int k = 0; k < 2; ++k) {
       mbar_init(&ctl->sfull[k], 1);
       mbar_init(&ctl->sfree[k], 2 * kSoftmaxWarps);
@@ -1132,17 +1133,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (rank == 1 && tid < 2 * kBlocks)
+  if (rank == 1 && tid < kBlocks)
     asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "h"(ctl->fills[tid]) : "memory");
   cluster_sync();
   // No CTA leaves with a copy of either in flight.  All are complete unless a
   // wait gave up; then one CTA may have begun a block's copies that the other
-  // has not, and the bytes that will not come are made up for.  (V of the tokens
-  // 128..255 is copied by the leader alone.)
-  if (rank == 0 && tid < 2 * kBlocks) {
-    uint64_t* const full = tid < kBlocks ? &ctl->kfull[tid] : &ctl->vfull[tid - kBlocks];
-    const uint16_t mine = ctl->fills[tid];
-    const uint16_t other = tid >= kBlocks && (tid & 2) != 0 ? mine : ctl->peer_fills[tid];
+  // has not, and the bytes that will not come are made up for.
+  if (rank == 0 && tid < kBlocks) {
+    uint64_t* const full = tid < 4 ? &ctl->kfull[tid] : &ctl->vfull[tid - 4];
+    const uint16_t mine = ctl->fills[tid], other = ctl->peer_fills[tid];
     const int ahead = static_cast<int16_t>(mine - other);   // -1, 0 or 1
     const uint32_t n = ahead >= 0 ? mine : other;
     if (ahead > 0)

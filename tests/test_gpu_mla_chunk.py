@@ -381,3 +381,29 @@ def test_plan_write_attend_together(api):
         api.dsa_mla_decode_fp8(r, q, pool, sel, topk, 0.02, 0.0625, out2, None, w2)
         torch.cuda.synchronize()
         paged_ref.check_chunk(out2.view(torch.bfloat16).float().cpu().numpy(), None, ref, f"gather step {k}")
+
+
+def test_forced_timeouts_are_reported_and_the_next_call_is_clean(api):
+    # Every wait in the kernel gives up at once: the call returns, says so, and
+    # leaves nothing behind.
+    default = api.dsa_get_wait_limit_ns()
+    c = Case([(3000, 4), (300, 60)], 64, 64, seed=13).upload(api)
+    c.call(api)
+    c.check(api)
+    out, lse = c.out.clone(), c.lse.clone()
+    try:
+        api.dsa_set_wait_limit_ns(1)
+        for _ in range(3):
+            c.call(api)
+            torch.cuda.synchronize()
+            code, _, count = api.dsa_get_error(reset=True)
+            assert api.DEVERR[code] == "timeout" and count >= 1
+    finally:
+        api.dsa_set_wait_limit_ns(0)
+    assert api.dsa_get_wait_limit_ns() == default
+    for _ in range(2):
+        c.out.fill_(MARK)
+        c.lse.fill_(77.0)
+        c.call(api)
+        c.check(api)
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
