@@ -522,16 +522,21 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   p.pairs = mla_chunk_pairs(seqs, rows, heads, dev->num_sms);
   p.box_rows = mla_chunk_box_rows(seqs->block_size);
   // Latent pool [nslots][512] bytes; boxes of 128 bytes (the swizzle span) by
-  // box_rows rows, or one for gathers; rows outside the pool read as zero.
-  CUtensorMap map;
+  // box_rows rows, or one for gathers and sixteen beside them; rows outside the
+  // pool read as zero.
+  CUtensorMap map, map16;
   cuuint64_t gdim[2] = {static_cast<cuuint64_t>(DSA_LATENT_DIM), static_cast<cuuint64_t>(nslots)};
   cuuint64_t gstride[1] = {static_cast<cuuint64_t>(DSA_LATENT_DIM)};
-  cuuint32_t box[2] = {128, p.box_rows > 0 ? static_cast<cuuint32_t>(p.box_rows) : 1u};
   cuuint32_t estride[2] = {1, 1};
-  CUresult cr = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pool), gdim,
-                       gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto pool_map = [&](CUtensorMap* m, uint32_t box_rows) {
+    const cuuint32_t box[2] = {128, box_rows};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pool), gdim, gstride, box,
+                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult cr = pool_map(&map, p.box_rows > 0 ? static_cast<uint32_t>(p.box_rows) : 1u);
+  if (cr == CUDA_SUCCESS && p.box_rows == 0) cr = pool_map(&map16, 16u);
+  else map16 = map;
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
   // Output [rows * heads][512] bf16, boxes of 32 dims x 32 lines.
   CUtensorMap omap;
@@ -542,7 +547,7 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
-  return launched(launch_mla_chunk(p, map, omap, workspace, dev->num_sms,
+  return launched(launch_mla_chunk(p, map, map16, omap, workspace, dev->num_sms,
                                    static_cast<cudaStream_t>(stream)));
 }
 

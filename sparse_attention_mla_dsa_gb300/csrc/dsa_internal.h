@@ -219,9 +219,10 @@ int mla_chunk_box_rows(int block_size);
 int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms);
 size_t mla_chunk_workspace_bytes(int pairs);
 // `map` describes the latent pool [nslots][512] bytes for 128-byte x box_rows
-// copies (1-row boxes where they are gathered), `omap` the output [rows * heads]
-// [512] bf16 for 64-byte x 32-line stores.
-cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& omap,
-                             void* workspace, int num_sms, cudaStream_t stream);
+// copies (1-row boxes where they are gathered), `map16` for 16-row ones beside
+// gathers, `omap` the output [rows * heads][512] bf16 for 64-byte x 32-line stores.
+cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& map16,
+                             const CUtensorMap& omap, void* workspace, int num_sms,
+                             cudaStream_t stream);
 
 }  // namespace dsa

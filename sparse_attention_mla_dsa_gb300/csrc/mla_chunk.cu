@@ -523,6 +523,7 @@ __device__ __forceinline__ void softmax_sync() {
 // block up and issues its copies.  Absent tokens are at row nslots, past the end.
 struct Rows {
   int32_t at[8];   // [0]: the box's first row; gathers: tokens 4l.. and 128 + 4l..
+  int how[2];      // gathers: 0 nothing (another lane's box has them), 4 a gather, 16 a box
   bool missing;    // this lane has a token without a latent before the item's end
 };
 // kMask: also the tile's token mask, and the error of a missing block.
@@ -574,6 +575,16 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
         const uint32_t other = __shfl_down_sync(0xFFFFFFFFu, bits, 1);
         if ((lane & 1) == 0) mask[(k * 32 + lane) >> 1] = static_cast<uint8_t>(bits | (other << 4));
       }
+      // Four lanes whose sixteen rows follow each other leave them to the first
+      // of the four, counted from where their run begins: one copy for four (a
+      // warp issues one in ~35 ns; pages of 20 tokens: 13 copies for 32).
+      const int32_t* y = &r.at[k * 4];
+      const bool run = y[0] < none && y[1] == y[0] + 1 && y[2] == y[0] + 2 && y[3] == y[0] + 3;
+      const int32_t after = __shfl_down_sync(0xFFFFFFFFu, run ? y[0] : -1, 1);
+      const uint32_t link = __ballot_sync(0xFFFFFFFFu, run && lane < 31 && after == y[0] + 4);
+      const uint32_t breaks = ~link & ((1u << lane) - 1u);
+      const int pos = lane - (32 - __clz(breaks)), more = __ffs(~(link >> lane)) - 1;
+      r.how[k] = (pos & 3) + more >= 3 ? ((pos & 3) == 0 ? 16 : 0) : 4;
     }
   }
   if constexpr (kMask) __syncwarp();
@@ -588,7 +599,7 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
 // has its own blocks: one warp alone fills a block, as a barrier's parity says
 // nothing to a warp that may be two fills behind.
 template <bool kV>
-__device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& p, Ctl* ctl, uint8_t* blocks,
+__device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& map16, const ChunkParams& p, Ctl* ctl, uint8_t* blocks,
                                      int lane, uint32_t rank, int pair, int64_t per, Walk w) {
   const int from = rank ? 128 : 0;             // K: the tokens of this CTA
   uint32_t looked = 0, n = 0, segs = 0;
@@ -671,7 +682,9 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const ChunkParams& 
           int32_t y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[k] = f ? r.at[4 + k] : r.at[k];
-          tma_gather4(dst + lane * 512, &map, bar, x, y);
+          const int how = f ? r.how[1] : r.how[0];
+          if (how == 16) tma_box(dst + lane * 512, &map16, bar, x, y[0]);
+          else if (how == 4) tma_gather4(dst + lane * 512, &map, bar, x, y);
         }
       }
     }
@@ -1061,8 +1074,8 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    mla_chunk_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap omap,
-                     const ChunkParams p) {
+    mla_chunk_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map16,
+                     const __grid_constant__ CUtensorMap omap, const ChunkParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;           // (no static shared memory: it begins on a 1024-byte boundary)
   uint8_t* qop = smem;
@@ -1095,6 +1108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_map(&map);
     tma_prefetch_map(&omap);
+    if (p.box_rows == 0) tma_prefetch_map(&map16);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
@@ -1118,7 +1132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
-    copy<false>(map, p, ctl, blocks, lane, rank, pair, at.per, w);
+    copy<false>(map, map16, p, ctl, blocks, lane, rank, pair, at.per, w);
   } else if (warp == 1 || warp == 3) {
     if (rank == 0 && lane == 0) {
       if (warp == 1) issue_mmas<false>(p, ctl, smem_u32(qop), smem_u32(pop), smem_u32(blocks), tmem, w);
@@ -1126,7 +1140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    copy<true>(map, p, ctl, blocks, lane, rank, pair, at.per, w);
+    copy<true>(map, map16, p, ctl, blocks, lane, rank, pair, at.per, w);
   } else if (warp >= kSoftmaxWarp0) {
     softmax(omap, p, ctl, qop, pop, blocks, tmem, warp, lane, rank, pair);
   }
@@ -1212,55 +1226,49 @@ __device__ __forceinline__ void merge_few(const ChunkParams& p, const ChunkRecor
     p.lse[gline] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Many parts: four threads have a line and 8 dims and take every fourth part,
-// eight in flight, then are added up in order.
+// Many parts: four threads have a line and 4 dims and take every fourth part,
+// sixteen in flight, then are added up in order.
 __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkRecord& r, int first, int half, int d4,
-                                           float4 (&x_acc)[3][2][64], float2 (&x_ml)[3][64]) {
-  constexpr int kDims = 2, kBatch = 8;
+                                           float4 (&x_acc)[3][64], float2 (&x_ml)[3][64]) {
+  constexpr int kBatch = 16;
   const int i = threadIdx.x & 63, set = threadIdx.x >> 6, line = half * 64 + i;
   auto slot = [&](int u) { return static_cast<int64_t>(first + u) * 2 + (u == 0 ? 1 : 0); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + line;
   const float4* o = reinterpret_cast<const float4*>(p.part_o) + static_cast<int64_t>(d4) * kItem + line;
   float m = -INFINITY, l = 0.0f;
-  float4 acc[kDims];
-#pragma unroll
-  for (int d = 0; d < kDims; ++d) acc[d] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](float mk, float lk, const float4 (&v)[kDims], float base) {
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float mk, float lk, float4 v, float base) {
     const float w = ex2(mk - base);
     l += w * lk;
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-      acc[d].x += w * v[d].x;
-      acc[d].y += w * v[d].y;
-      acc[d].z += w * v[d].z;
-      acc[d].w += w * v[d].w;
-    }
+    acc.x += w * v.x;
+    acc.y += w * v.y;
+    acc.z += w * v.z;
+    acc.w += w * v.w;
   };
   auto scale_by = [&](float a) {
     l *= a;
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-      acc[d].x *= a;
-      acc[d].y *= a;
-      acc[d].z *= a;
-      acc[d].w *= a;
-    }
+    acc.x *= a;
+    acc.y *= a;
+    acc.z *= a;
+    acc.w *= a;
   };
   for (int u0 = set; u0 < r.parts; u0 += 4 * kBatch) {
     float2 x[kBatch];
-    float4 v[kBatch][kDims];
+    float4 v[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int u = min(u0 + 4 * k, r.parts - 1);
-      x[k] = ld_dep_f2(ml + slot(u) * kItem);
-      if (u0 + 4 * k >= r.parts) x[k] = make_float2(-INFINITY, 0.0f);
-#pragma unroll
-      for (int d = 0; d < kDims; ++d) v[k][d] = ld_dep_f4(o + (slot(u) * 128 + d) * kItem);
+      x[k] = make_float2(-INFINITY, 0.0f);
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int u = u0 + 4 * k;
+      if (u < r.parts) {
+        x[k] = ld_dep_f2(ml + slot(u) * kItem);
+        v[k] = ld_dep_f4(o + slot(u) * 128 * kItem);
+      }
     }
     float top = m;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) top = fmaxf(top, x[k].x);
-    const float base = top == -INFINITY ? 0.0f : top;
+    const float base = top == -INFINITY ? 0.0f : top;   // (no weight yet: 0 times a sum that may be NaN)
     scale_by(ex2(m - base));
     m = top;
 #pragma unroll
@@ -1269,8 +1277,7 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
   __syncthreads();                                      // the unit before has been read
   if (set > 0) {
     x_ml[set - 1][i] = make_float2(m, l);
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) x_acc[set - 1][d][i] = acc[d];
+    x_acc[set - 1][i] = acc;
   }
   __syncthreads();
   if (set > 0 || line >= r.lines) return;
@@ -1280,30 +1287,24 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
   const float base = top == -INFINITY ? 0.0f : top;
   scale_by(ex2(m - base));
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const float4 v[kDims] = {x_acc[k][0][i], x_acc[k][1][i]};
-    add(x_ml[k][i].x, x_ml[k][i].y, v, base);
-  }
+  for (int k = 0; k < 3; ++k) add(x_ml[k][i].x, x_ml[k][i].y, x_acc[k][i], base);
   const float inv = l != l ? l : (top != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
   const int64_t gline = r.line0 + line;
-  uint32_t w[4];
-#pragma unroll
-  for (int d = 0; d < kDims; ++d) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * d]) : "f"(acc[d].y * inv), "f"(acc[d].x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * d + 1]) : "f"(acc[d].w * inv), "f"(acc[d].z * inv));
-  }
-  *reinterpret_cast<uint4*>(p.out + gline * 512 + d4 * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+  uint32_t w[2];
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(acc.y * inv), "f"(acc.x * inv));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[1]) : "f"(acc.w * inv), "f"(acc.z * inv));
+  *reinterpret_cast<uint2*>(p.out + gline * 512 + d4 * 4) = make_uint2(w[0], w[1]);
   if (d4 == 0 && p.lse != nullptr)
     p.lse[gline] = l != 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 8 of
+// CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 4 of
 // one with many (few items then, which have to reach every SM).
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
   constexpr int kFew = 8;
   __shared__ ChunkRecord rec[kMaxPairs];
   __shared__ int begin[kMaxPairs + 1];                  // first unit of each pair's record
-  __shared__ float4 x_acc[3][2][64];
+  __shared__ float4 x_acc[3][64];
   __shared__ float2 x_ml[3][64];
   const int tid = threadIdx.x, lane = tid & 31;
   grid_dep_launch();
@@ -1312,7 +1313,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const Ch
   if (tid < p.pairs) {
     const ChunkRecord r = p.records[tid];
     rec[tid] = r;
-    if (r.parts > 1) units = (r.lines > 64 ? 2 : 1) * (r.parts > kFew ? 64 : 8);
+    if (r.parts > 1) units = (r.lines > 64 ? 2 : 1) * (r.parts > kFew ? 128 : 8);
   }
   if (!__syncthreads_or(units)) return;
   begin[tid] = units;
@@ -1344,7 +1345,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const Ch
     const ChunkRecord r = rec[lo];
     const int at = unit - begin[lo];
     const int half = r.lines > 64 ? at & 1 : 0, d = r.lines > 64 ? at >> 1 : at;
-    if (r.parts > kFew) merge_many(p, r, lo, half, d * 2, x_acc, x_ml);
+    if (r.parts > kFew) merge_many(p, r, lo, half, d, x_acc, x_ml);
     else merge_few<4>(p, r, lo, half * 64 + (tid & 63), d * 16 + (tid >> 6) * 4);
   }
 }
@@ -1375,8 +1376,8 @@ int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms) {
   return static_cast<int>(items * tiles < pairs ? items * tiles : pairs);
 }
 
-cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& omap, void* workspace,
-                             int num_sms, cudaStream_t stream) {
+cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtensorMap& map16,
+                             const CUtensorMap& omap, void* workspace, int num_sms, cudaStream_t stream) {
   if (p.pairs < 1 || p.pairs > kMaxPairs) return cudaErrorInvalidValue;
   const size_t lines = static_cast<size_t>(p.pairs) * 2 * kItem;
   p.part_o = static_cast<float*>(workspace);
@@ -1393,7 +1394,7 @@ cudaError_t launch_mla_chunk(ChunkParams p, const CUtensorMap& map, const CUtens
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, mla_chunk_kernel, map, omap, p);
+  e = cudaLaunchKernelEx(&cfg, mla_chunk_kernel, map, map16, omap, p);
   if (e != cudaSuccess || p.pairs == 1) return e;
   cudaLaunchConfig_t mcfg = {};
   mcfg.gridDim = dim3(static_cast<unsigned>(2 * num_sms), 1, 1);
