@@ -557,18 +557,29 @@ __device__ __forceinline__ Rows lookup(const ChunkParams& p, const Segment& g, i
   } else {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      // The four tokens' blocks first (one division, then steps), so that their
+      // loads are in flight together.
+      const int tok = t0 + (k * 32 + lane) * 4;
+      int blk[4], in[4], phys[4];
+      blk[0] = tok / bs;
+      in[0] = tok - blk[0] * bs;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        const bool over = in[i - 1] + 1 == bs;
+        blk[i] = blk[i - 1] + (over ? 1 : 0);
+        in[i] = over ? 0 : in[i - 1] + 1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) phys[i] = tok + i < end ? bt[blk[i]] : -1;
       uint32_t bits = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int tok = t0 + (k * 32 + lane) * 4 + i;
-        if (tok < end) {
-          const int64_t slot = static_cast<int64_t>(bt[tok / bs]) * bs + tok % bs;
-          if (slot >= 0 && slot < p.nslots) {
-            r.at[k * 4 + i] = static_cast<int32_t>(slot);
-            bits |= 1u << i;
-          } else {
-            missing = true;
-          }
+        const int64_t slot = static_cast<int64_t>(phys[i]) * bs + in[i];
+        if (phys[i] >= 0 && slot < p.nslots) {
+          r.at[k * 4 + i] = static_cast<int32_t>(slot);
+          bits |= 1u << i;
+        } else if (tok + i < end) {
+          missing = true;
         }
       }
       if constexpr (kMask) {
