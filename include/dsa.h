@@ -524,9 +524,18 @@ typedef struct dsa_seqs {
  * (DSA_DEVERR_ROWS), or with rows and seq_lens[s] < n or above
  * max_blocks_per_seq * block_size (DSA_DEVERR_SEQ_LEN), is skipped, its rows
  * left as they were (the recorded row is s).  Rows of no request are left as
- * they were.
+ * they were.  After a wait that gave up (DSA_DEVERR_TIMEOUT, row -1) the call's
+ * rows hold nothing to rely on.
  *   q   [rows][heads][latent_dim] bf16       pool [nslots][latent_dim] FP8
  *   out [rows][heads][latent_dim] bf16       lse  [rows][heads] fp32 or NULL
+ * Numerics: the latents enter the FP8 tensor cores as they are; q as two E4M3
+ * terms an element (as in dsa_mla_decode_fp8), a softmax weight as an E4M3 term
+ * and the E5M2 term of its remainder: within 2^-7 of the weight, about 2^-9.6
+ * rms, down to 2^-25 of the line's largest.  Logits, sums, maxima and the
+ * output are FP32, lse uses the unrounded weights.  The tokens are shared out
+ * among the SMs by the lengths of the whole call and partial results merged in
+ * order: the same call gives the same bits, but a row's last bits may differ
+ * beside other rows.
  * latent_dim must be 512; heads a multiple of 16 up to 4096; rows <= 65535;
  * seqs <= DSA_PLAN_MAX_SEQS; nslots below 2^31; block_size *
  * max_blocks_per_seq at most 2^30 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and out 16-byte aligned; out

@@ -465,6 +465,15 @@ dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
       p.bt_stride < p.max_blocks_per_seq || p.free_capacity < 1 || p.reserved != 0)
     return DSA_ERR_INVALID_ARG;
   if (p.row_table != nullptr && p.row_bt_stride < p.max_blocks_per_seq) return DSA_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(p.seq_lens), static_cast<const void*>(p.new_tokens),
+                        static_cast<const void*>(p.held_in), static_cast<const void*>(p.held_out),
+                        static_cast<const void*>(p.block_table), static_cast<const void*>(p.free_blocks),
+                        static_cast<const void*>(p.free_in), static_cast<const void*>(p.free_out),
+                        static_cast<const void*>(p.row_start), static_cast<const void*>(p.positions),
+                        static_cast<const void*>(p.row_lens), static_cast<const void*>(p.row_table),
+                        static_cast<const void*>(p.row_seq)})
+    if (!aligned(q, 4)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(p.slots, 8)) return DSA_ERR_INVALID_ARG;
   if (p.seqs > DSA_PLAN_MAX_SEQS || p.rows > 65535) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p.seqs) * p.max_blocks_per_seq > INT32_MAX ||
       static_cast<int64_t>(p.block_size) * p.max_blocks_per_seq > INT32_MAX)
@@ -499,7 +508,9 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   if (rows > 65535 || seqs->seqs > DSA_PLAN_MAX_SEQS) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq > (1LL << 30))
     return DSA_ERR_UNSUPPORTED;
-  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(lse_or_null, 4) ||
+      !aligned(seqs->seq_lens, 4) || !aligned(seqs->row_start, 4) || !aligned(seqs->block_table, 4))
+    return DSA_ERR_INVALID_ARG;
   const DeviceInfo* dev = device_info();
   if (dev == nullptr) return DSA_ERR_CUDA;
   if (workspace == nullptr || workspace_bytes < dsa_chunk_workspace_bytes(rows, heads) ||

@@ -120,6 +120,20 @@ def test_ragged_batches(api, seed):
                   spare_rows=int(rng.integers(0, 4)), stride=int(rng.integers(0, 3))))
 
 
+@pytest.mark.parametrize("kind", ["runs", "reversed", "strided"])
+@pytest.mark.parametrize("block", [1, 4, 20])
+def test_orders_of_pages(api, kind, block):
+    # Gathered pages that follow each other in the pool, backwards, with gaps.
+    c = Case([(777, 9)], 64, block, seed=3, spare_blocks=1)
+    n = -(-786 // block)
+    ids = {"runs": np.arange(n), "reversed": np.arange(n)[::-1], "strided": np.arange(n) * 2}[kind]
+    pool = np.full(((int(ids.max()) + 1) * block, 512), NAN8, np.uint8)
+    for b in range(n):
+        pool[int(ids[b]) * block:][:block] = c.pool[int(c.table[0, b]) * block:][:block]
+    c.table[0, :n], c.pool = ids, pool
+    run(api, c)
+
+
 def test_many_requests(api):
     run(api, Case([(s % 37, s % 3) for s in range(1100)], 16, 16, seed=3, spare_rows=2))
 
@@ -241,6 +255,15 @@ def test_huge_and_tiny_queries(api):
     rng = np.random.default_rng(1)
     c.q = bf16_bits(rng.standard_normal((2, 64, 512)) * np.logspace(-30, 1, 64)[None, :, None])
     c.q[0, 5] = 0
+    run(api, c)
+
+
+@pytest.mark.parametrize("sm_scale, kv_scale", [(-0.0625, 0.02), (0.0, 0.02), (0.0625, -0.02), (0.0625, 0.0),
+                                                (1e-30, 0.02), (0.0625, 1e-6)])
+def test_other_scales(api, sm_scale, kv_scale):
+    c = Case([(300, 3), (0, 2)], 64, 64, seed=7, q_scale=0.5)
+    c.sm_scale, c.kv_scale = sm_scale, kv_scale
+    c.q[1, 5] = 0
     run(api, c)
 
 

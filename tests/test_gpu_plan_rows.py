@@ -142,6 +142,15 @@ def test_full_prompt_and_long_tables(api):
     st.check(api, st.expect())
 
 
+def test_as_many_requests_as_allowed(api):
+    rng = np.random.default_rng(2)
+    st = State(8192, 3, 4, 8192 * 3, 9000, 11)
+    new = rng.integers(0, 2, 8192)
+    st.lengths(rng.integers(1, 13, 8192), new)
+    api.dsa_plan_rows(st.plan(api))
+    st.check(api, st.expect())
+
+
 @pytest.mark.parametrize("row_table, row_seq", [(False, True), (True, False), (False, False)])
 def test_optional_outputs_and_strided_tables(api, row_table, row_seq):
     st = State(5, 6, 16, 30, 40, 3, stride=11, row_table=row_table, row_seq=row_seq)

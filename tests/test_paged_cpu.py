@@ -41,6 +41,8 @@ def _plan(**changes):
     ({"seqs": 8193}, 2), ({"rows": 65536}, 2),
     ({"seqs": 8192, "max_blocks_per_seq": 1 << 18, "bt_stride": 1 << 18, "row_bt_stride": 1 << 18}, 2),
     ({"block_size": 1 << 28}, 2),
+    *[({n: X + 2}, 1) for n in ("seq_lens", "held_out", "block_table", "free_out", "row_start", "row_table")],
+    ({"slots": X + 4}, 1),
 ])
 def test_plan_refusals(lib, changes, status):
     assert lib.dsa_plan_rows(_plan(**changes), None) == status
@@ -66,7 +68,8 @@ def _chunk(lib, *, q=X, pool=X, nslots=64, rows=4, heads=64, dim=512, out=X, lse
     ({"row_start": None}, 1), ({"block_table": None}, 1),
     ({"rows": 0}, 1), ({"nslots": 0}, 1), ({"seqs": 0}, 1), ({"block_size": 0}, 1),
     ({"max_blocks_per_seq": 0}, 1), ({"bt_stride": 3}, 1),
-    ({"q": X + 8}, 1), ({"pool": X + 8}, 1), ({"out": X + 8}, 1),
+    ({"q": X + 8}, 1), ({"pool": X + 8}, 1), ({"out": X + 8}, 1), ({"lse": X + 2}, 1),
+    ({"seq_lens": X + 2}, 1), ({"row_start": X + 1}, 1), ({"block_table": X + 3}, 1),
     ({"dim": 576}, 2), ({"heads": 8}, 2), ({"heads": 24}, 2), ({"heads": 4112}, 2),
     ({"rows": 65536}, 2), ({"seqs": 8193}, 2), ({"nslots": 1 << 31}, 2), ({"block_size": 1 << 30}, 2),
 ])
