@@ -23,6 +23,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 1024;
+static_assert((kThreads & (kThreads - 1)) == 0, "the rows' threads are counted from the middle");
 constexpr int kWarps = kThreads / 32;
 // Row-table entries of a warp's turn, all loads in flight before the first
 // store.
@@ -157,11 +158,10 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     }
   }
   // Every thread of this CTA has read held_in and free_in; the last CTA to get
-  // here writes their successors.
-  if (tid == 0) {
-    __threadfence();
-    sh.last = atomicAdd(&p.free_out[1], 1) == static_cast<int>(gridDim.x) - 1;
-  }
+  // here writes their successors, at its end (the ticket's way to L2 and back is
+  // nobody's wait until then).
+  int ticket = 0;
+  if (tid == 0) ticket = atomicAdd(&p.free_out[1], 1);
   __syncthreads();
   const int taken = sh.taken;
   const int kept = max(0, nback - taken);  // given-back blocks that stay on the stack
@@ -180,19 +180,6 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     return pop(sc.want[s] + (b - sc.held[s]));
   };
 
-  if (sh.last) {
-    for (int s = tid; s < n; s += kThreads)
-      p.held_out[s] = sc.need[s] < 0 || refused(s) ? sc.held[s] : sc.need[s];
-    if (tid == 0) {
-      int64_t left = avail - taken;
-      if (left > p.free_capacity) {
-        record_error(kp.err, DSA_DEVERR_FREE, -1);
-        left = p.free_capacity;
-      }
-      p.free_out[0] = static_cast<int>(left);
-      p.free_out[1] = 0;
-    }
-  }
   if (first) {
     for (int s = tid; s <= n; s += kThreads) p.row_start[s] = sc.rows[s];
     if (tid == 0 && nrows > p.rows) record_error(kp.err, DSA_DEVERR_ROWS, find(sc.rows, n, p.rows));
@@ -205,15 +192,33 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride;
     if (need < 0) continue;  // an invalid request's `held` bounds nothing
     const bool no = refused(s);
-    for (int b = held + lane; b < need; b += 32) row[b] = no ? -1 : pop(sc.want[s] + (b - held));
-    for (int b = need + lane; b < held; b += 32) {
-      const int i = sc.back[s] + (b - need);
-      if (i < kept && static_cast<int64_t>(stack) + i < p.free_capacity) p.free_blocks[stack + i] = row[b];
+    // (Loads of eight turns before their stores: a prompt takes, a request that
+    // ends gives back, its blocks by the hundred.)
+    constexpr int kTurns = 8;
+    for (int b0 = held + lane; b0 < need; b0 += 32 * kTurns) {
+      int v[kTurns];
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) v[k] = !no && b0 + 32 * k < need ? pop(sc.want[s] + (b0 + 32 * k - held)) : -1;
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k)
+        if (b0 + 32 * k < need) row[b0 + 32 * k] = v[k];
+    }
+    const int fits = static_cast<int>(min(static_cast<int64_t>(kept), static_cast<int64_t>(p.free_capacity) - stack));
+    const int up = need + min(held - need, max(0, fits - sc.back[s]));  // entries below it go onto the stack
+    for (int b0 = need + lane; b0 < up; b0 += 32 * kTurns) {
+      int v[kTurns];
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k)
+        if (b0 + 32 * k < up) v[k] = row[b0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k)
+        if (b0 + 32 * k < up) p.free_blocks[stack + sc.back[s] + (b0 + 32 * k - need)] = v[k];
     }
   }
   // The rows.
   const int out_rows = min(nrows, p.rows);
-  for (int r = blockIdx.x * kThreads + tid; r < out_rows; r += gridDim.x * kThreads) {
+  // (Other warps begin with the requests' tables, and others with the rows'.)
+  for (int r = blockIdx.x * kThreads + ((tid + kThreads / 2) & (kThreads - 1)); r < out_rows; r += gridDim.x * kThreads) {
     const int s = find(sc.rows, n, r);
     const bool live = sc.need[s] >= 0 && !refused(s);
     int pos = 0;
@@ -227,21 +232,20 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     p.row_lens[r] = live ? pos + 1 : 0;
     if (p.row_seq != nullptr) p.row_seq[r] = s;
   }
-  if (p.row_table == nullptr) return;
   // A warp's turn is kSpan entries of `run` consecutive rows, whose request's
   // entries are looked up and loaded once; single rows while there are warps to
   // spare (12,000 rows of 1,031 entries: 25.1 us by single rows, 15.4 by fours,
   // where a fill of the tables takes 7.2).
   const int width = p.max_blocks_per_seq, spans = (width + kSpan - 1) / kSpan;
   const int run = static_cast<int64_t>(out_rows) * spans >= 4ll * nwarps ? 4 : 1;
-  const int turns = (out_rows + run - 1) / run * spans;
+  const int turns = p.row_table != nullptr ? (out_rows + run - 1) / run * spans : 0;
   constexpr uint32_t kAll = (1u << kPer) - 1u;
   // Entries base + 32 k + lane of a span that are below x.
   auto below = [&](int base, int x) {
     const int m = (x - base - lane + 31) >> 5;          // k < m
     return m >= kPer ? kAll : m <= 0 ? 0u : (1u << m) - 1u;
   };
-  for (int turn = gwarp; turn < turns; turn += nwarps) {
+  for (int turn = nwarps - 1 - gwarp; turn < turns; turn += nwarps) {
     const int r0 = turn / spans * run, base = turn % spans * kSpan;
     const int r1 = min(r0 + run, out_rows);
     const uint32_t in = below(base, width);
@@ -280,6 +284,22 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
         if (b >= base) row[b] = b < kept_blocks + 32 ? fresh : pop(sc.want[s] + (b - kept_blocks));
     }
   }
+
+  if (tid == 0) sh.last = ticket == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (sh.last) {
+    for (int s = tid; s < n; s += kThreads)
+      p.held_out[s] = sc.need[s] < 0 || refused(s) ? sc.held[s] : sc.need[s];
+    if (tid == 0) {
+      int64_t left = avail - taken;
+      if (left > p.free_capacity) {
+        record_error(kp.err, DSA_DEVERR_FREE, -1);
+        left = p.free_capacity;
+      }
+      p.free_out[0] = static_cast<int>(left);
+      p.free_out[1] = 0;
+    }
+  }
 }
 
 }  // namespace
@@ -291,10 +311,11 @@ cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t 
         plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  // A CTA for every 32 warps' turns (or 1,024 rows), up to one a SM: each scans
+  // A CTA for every 32 warps' turns, 1,024 rows or 64 requests, up to one a SM: each scans
   // all requests.
   const int64_t spans = p.p.row_table != nullptr ? (p.p.max_blocks_per_seq + kSpan - 1) / kSpan : 0;
-  int64_t ctas = std::max((p.p.rows * spans + kWarps - 1) / kWarps, static_cast<int64_t>((p.p.rows + kThreads - 1) / kThreads));
+  int64_t ctas = std::max((p.p.rows * spans + kWarps - 1) / kWarps,
+                          static_cast<int64_t>(std::max((p.p.rows + kThreads - 1) / kThreads, p.p.seqs / (2 * kWarps))));
   if (ctas > num_sms) ctas = num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
