@@ -139,7 +139,7 @@ __device__ __forceinline__ int item_tiles(const ChunkParams& p, const SeqInfo& q
 }
 // How many of the request's items see at most x new tokens.
 __device__ __forceinline__ int items_within(const ChunkParams& p, const SeqInfo& q, int x) {
-  return x <= 0 ? 0 : x >= q.rows ? q.items : static_cast<int>(static_cast<int64_t>(x) * p.heads / kItem);
+  return x <= 0 ? 0 : x >= q.rows ? q.items : x * p.heads / kItem;  // (65,535 x 4,096 lines at most)
 }
 // The request's cost: items by their number of tiles v, those within v tiles
 // less those within v - 1.
@@ -153,6 +153,16 @@ __device__ __forceinline__ int64_t seq_cost(const ChunkParams& p, const SeqInfo&
     below = upto;
   }
   return sum;
+}
+
+// a / b and a % b, in 32 bits where they fit (a 64-bit division is a routine of
+// its own, and every CTA of a call waits for these).
+__device__ __forceinline__ int64_t div_small(int64_t a, uint32_t b, int64_t* rest = nullptr) {
+  int64_t q;
+  if ((a >> 32) == 0) q = static_cast<uint32_t>(a) / b;
+  else q = a / static_cast<int64_t>(b);
+  if (rest != nullptr) *rest = a - q * b;
+  return q;
 }
 
 struct Place {
@@ -200,7 +210,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
       }
     if (tid == 31) {
       found.total = x;
-      found.per = max(static_cast<int64_t>(1), (x + pairs - 1) / pairs);
+      found.per = max(static_cast<int64_t>(1), div_small(x + pairs - 1, static_cast<uint32_t>(pairs)));
     }
   }
   __syncthreads();
@@ -221,8 +231,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
         const int64_t here = static_cast<int64_t>(upto - below) * (v + kItemCost);
         if (off < here) {
           found.seq = s;
-          found.item = below + static_cast<int>(off / (v + kItemCost));
-          found.off = off % (v + kItemCost);
+          found.item = below + static_cast<int>(div_small(off, static_cast<uint32_t>(v + kItemCost), &found.off));
           break;
         }
         off -= here;
@@ -337,12 +346,13 @@ __device__ __forceinline__ bool warp_wait(Ctl* c, uint64_t* bar, uint32_t parity
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
-// Bounded wait of a warp until more than `seg` segments have been left.
-__device__ __forceinline__ bool wait_segment(Ctl* c, uint32_t seg, int lane, const ChunkParams& p) {
+// Bounded wait of a warp until `there()`, a test of shared memory by lane 0.
+template <typename There>
+__device__ __forceinline__ bool wait_until(Ctl* c, int lane, const ChunkParams& p, There there) {
   int ok = 1;
   if (lane == 0) {
     const uint64_t t0 = global_ns();
-    while (*reinterpret_cast<volatile uint32_t*>(&c->segs) <= seg) {
+    while (!there()) {
       if (aborted(c) || global_ns() - t0 > p.wait_ns) {
         if (!aborted(c)) record_error(p.err, DSA_DEVERR_TIMEOUT, -1);
         set_abort(c);
@@ -353,6 +363,10 @@ __device__ __forceinline__ bool wait_segment(Ctl* c, uint32_t seg, int lane, con
     __threadfence_block();
   }
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+// More than `seg` segments have been left.
+__device__ __forceinline__ bool wait_segment(Ctl* c, uint32_t seg, int lane, const ChunkParams& p) {
+  return wait_until(c, lane, p, [&] { return *reinterpret_cast<volatile uint32_t*>(&c->segs) > seg; });
 }
 
 // ------------------------------------------------------------------ tensor core
@@ -642,13 +656,9 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
       r.pad = 0;
       at += g.tiles + kItemCost;
       publish(r);
-      // its Q into L2
-      for (int k = lane; k < kLines * 8; k += 32) {
-        const int i = static_cast<int>(rank) * kLines + (k >> 3);
-        if (i < r.lines) prefetch_l2(p.q + (r.gline + i) * 512 + (k & 7) * 64);
-      }
     }
-    // K: also leaves the tile's mask and brings its latents into L2.
+    // K: also leaves the tile's mask and brings the latents of a tile to come into
+    // L2.
     auto look = [&](int t) {
       const Rows r = lookup<!kV>(p, g, end, t, lane, rank, kV ? nullptr : ctl->mask[looked % kMasks]);
       if constexpr (!kV) {
@@ -659,7 +669,7 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
         }
         ++looked;
         const int tok = lane * p.box_rows - from;
-        if (p.box_rows > 0 && tok >= 0 && tok < 128 && r.at[0] < p.nslots)
+        if (t > g.begin && p.box_rows > 0 && tok >= 0 && tok < 128 && r.at[0] < p.nslots)
           for (int d = 0; d < 4; ++d) tma_prefetch_l2_2d(&map, d * 128, r.at[0]);
       }
       return r;
@@ -667,7 +677,11 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
     Rows next = look(g.begin);
     for (int t = g.begin; t < g.end; ++t, ++n) {
       const Rows r = next;
-      if (t + 1 < g.end) next = look(t + 1);   // before the waits of this tile
+      // The call's first K before its first V: both would share the SM's way in.
+      if (kV && n == 0 &&
+          !wait_until(ctl, lane, p, [&] { return *reinterpret_cast<volatile uint16_t*>(&ctl->fills[3]) != 0; }))
+        return;
+#pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         uint64_t* const full = kV ? &ctl->vfull[i] : &ctl->kfull[i];
         if (n >= 1) {
@@ -698,6 +712,16 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
           else if (how == 4) tma_gather4(dst + lane * 512, &map, bar, x, y);
         }
       }
+      if (!kV && t == g.begin) {
+        // The segment's Q into L2 (a segment ahead of its conversion, but for the
+        // first).
+        const SegRecord& q = ctl->seg[(segs - 1) % kSegs];
+        for (int k = lane; k < kLines * 8; k += 32) {
+          const int i = static_cast<int>(rank) * kLines + (k >> 3);
+          if (i < q.lines) prefetch_l2(p.q + (q.gline + i) * 512 + (k & 7) * 64);
+        }
+      }
+      if (t + 1 < g.end) next = look(t + 1);   // while this tile's copies are on their way
     }
   }
   if constexpr (!kV) publish(SegRecord{});
