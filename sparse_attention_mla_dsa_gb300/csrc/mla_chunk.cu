@@ -763,6 +763,12 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
         }
         if (ok) commit_pair(&ctl->sfull[par]);
       } else {
+        if (g.q.ctx + g.item * kItem / p.heads + 1 < (t + 1) * kTile) {
+          // Softmax warps of either CTA may have to rewrite this V, see there.
+          for (int v = 0; v < 4; ++v) ok = ok && wait_one(ctl, &ctl->vfull[v], par, p);
+          if (!ok) break;
+          commit_pair(&ctl->vseen);
+        }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {              // 128 tokens
           ok = ok && wait_one(ctl, &ctl->vfull[2 * h], par, p) && wait_one(ctl, &ctl->vfull[2 * h + 1], par, p) &&
@@ -934,6 +940,9 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
 #pragma unroll
         for (int u = 0; u < 4; ++u) mk[u] = fmaxf(fmaxf(mk[u], z[k + u]), k + 4 + u < kTok ? z[k + 4 + u] : -INFINITY);
       float mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * scale;
+      // The output that left through this warp's share of P has been read, before
+      // any of its eight warps writes weights there.
+      if (t == 0 && lane == 0) tma_store_read();
       if (line_sync_or(group, mx > m + kPMaxLog2)) {
         ctl->red[part][i] = mx;
         line_sync(group);
@@ -996,16 +1005,12 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       // A token that some line of the item does not see has weight 0 there, which
       // a NaN latent would turn into NaN.  Such a latent shows as a NaN logit of
       // every line of both CTAs; its codes are then zeroed in V (a line that sees
-      // it has a NaN weight, so its output is NaN all the same).  The leader, whose
-      // barriers say when V has landed in both CTAs, tells the other in every such
-      // tile.
+      // it has a NaN weight, so its output is NaN all the same).  The thread that
+      // issues the O of the tile, whose barriers say when V has landed in both CTAs,
+      // tells both in every such tile.
       if (from < kTile) {
         const bool patch = line_sync_or(group, nan);
-        if (rank == 0 && (patch || sw == 0)) {
-          if (ns > 0) ok = ok && wait_o(ns - 1);             // (the V before has landed, too)
-          for (int v = 0; v < 4; ++v) ok = ok && warp_wait(ctl, &ctl->vfull[v], ns & 1, lane, p);
-          if (sw == 0 && lane == 0) arrive_release_at(map_to(&ctl->vseen, 1));
-        } else if (rank == 1 && patch) {
+        if (patch) {
           ok = ok && warp_wait(ctl, &ctl->vseen, nv & 1, lane, p);
           acquire_cluster();
         }
@@ -1081,7 +1086,6 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         }
         __syncwarp();
       }
-      if (lane == 0) tma_store_read();
       if (ok && part == 0 && i < lines && p.lse != nullptr)
         p.lse[gline0 + i] = lt != 0.0f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
     } else {
