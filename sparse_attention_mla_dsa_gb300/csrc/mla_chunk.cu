@@ -278,6 +278,13 @@ __device__ __forceinline__ bool next_segment(const ChunkParams& p, Walk& w, Segm
   return g.end > g.begin;
 }
 
+// Lines of an item in each CTA of its pair, of `lines` that the request has from
+// the item's first on: those of a half-empty item (one token at 64 heads) are
+// shared by both, which then load, convert and store half of them each (one decode
+// 26.2 -> 24.4 us, a decode batch 150 -> 147; items of 128 lines lose 1.8 % by the
+// tests: a prompt of 2,049 rows 487 -> 495).
+__device__ __forceinline__ int cta_lines(int lines) { return lines > kLines ? kLines : kLines / 2; }
+
 // ------------------------------------------------------------------ pair
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -716,9 +723,10 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
         // The segment's Q into L2 (a segment ahead of its conversion, but for the
         // first).
         const SegRecord& q = ctl->seg[(segs - 1) % kSegs];
+        const int own = cta_lines(q.lines);
         for (int k = lane; k < kLines * 8; k += 32) {
-          const int i = static_cast<int>(rank) * kLines + (k >> 3);
-          if (i < q.lines) prefetch_l2(p.q + (q.gline + i) * 512 + (k & 7) * 64);
+          const int i = static_cast<int>(rank) * own + (k >> 3);
+          if (i < q.lines && (k >> 3) < own) prefetch_l2(p.q + (q.gline + i) * 512 + (k & 7) * 64);
         }
       }
       if (t + 1 < g.end) next = look(t + 1);   // while this tile's copies are on their way
@@ -892,7 +900,8 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   };
   auto next_q = [&]() {
     const SegRecord& r = ctl->seg[seg % kSegs];
-    convert_q(p, ctl, qop, r.gline + rank * kLines, r.lines - static_cast<int>(rank) * kLines, sw, lane);
+    const int own = cta_lines(r.lines), before = static_cast<int>(rank) * own;
+    convert_q(p, ctl, qop, r.gline + before, min(own, r.lines - before), sw, lane);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && ok) arrive_at(qready);
@@ -904,7 +913,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     const SegRecord& g = ctl->seg[seg % kSegs];
     const float scale = ctl->qexp[i];
     const int first_tile = g.begin, tiles = g.end - g.begin;
-    const int in = min(static_cast<int>(rank) * kLines + i, g.lines - 1);
+    const int in = min(static_cast<int>(rank) * cta_lines(g.lines) + i, g.lines - 1);
     // tokens that this line sees of this thread's, and that every line of the item sees, from the tile on
     int visible = g.ctx + (g.first + in) / p.heads + 1 - (first_tile * kTile + half * 128 + sub * kTok);
     int all_see = g.ctx + g.first / p.heads + 1 - first_tile * kTile;
@@ -914,6 +923,15 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
       float z[kTok];
       ok = ok && wait_all(ctl, &ctl->sfull[b], (ns >> 1) & 1, lane, p);
       tc_fence_after();
+      // This warp has none of the item's lines: it only keeps step, as P of the tile
+      // before has to be complete before its part of this one is.
+      if (group == 1 && g.lines <= kLines) {
+        if (lane == 0 && ok) arrive_at(b ? sfree1 : sfree0);
+        if (all_see < kTile) ++nv;
+        if (ns > 0) ok = ok && wait_all(ctl, &ctl->vread[2 * ((ns - 1) & 1) + half], ((ns - 1) >> 1) & 1, lane, p);
+        if (lane == 0 && ok) arrive_at(pready);
+        continue;
+      }
       tmem_load32(scol + b * 128, z);
       tc_fence_before();
       if (lane == 0 && ok) arrive_at(b ? sfree1 : sfree0);
@@ -1038,8 +1056,10 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     // Every S of the segment is complete: the next one's Q takes its place
     // while the last P V runs, and its first S runs beside the epilogue.
     const bool whole = g.whole != 0;
-    const int64_t gline0 = g.gline + rank * kLines;
-    const int lines = g.lines - static_cast<int>(rank) * kLines;   // of this CTA, if under 64
+    const int own = cta_lines(g.lines), before = static_cast<int>(rank) * own;
+    const int64_t gline0 = g.gline + before;
+    const int lines = min(own, g.lines - before);       // of this CTA
+    const bool idle = group * 32 >= lines;
     const int parts = g.parts, item_lines = min(kItem, g.lines);
     ctl->red[part][i] = l;
     ++seg;
@@ -1053,7 +1073,8 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     ok = ok && wait_o(ns - 1);
     tc_fence_after();
     const int d0 = half * 256 + sub * 64;
-    if (whole) {
+    if (idle) {                                         // (nothing to leave)
+    } else if (whole) {
       const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
       // Through 2 KB of this warp's share of P, 32 lines x 32 dims at a time:
       // rows of 64 bytes, swizzled, which a copy then writes in whole sectors.
@@ -1091,7 +1112,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     } else {
       // Slot 0: the item began in an earlier range, 1: it goes on in a later one.
       // [128 groups of 4 dims][128 lines][4]: a warp's lines side by side.
-      const int slot = first_tile > 0 ? 0 : 1, pline = static_cast<int>(rank) * kLines + i;
+      const int slot = first_tile > 0 ? 0 : 1, pline = before + i;
       float4* dst = reinterpret_cast<float4*>(p.part_o) +
                     ((static_cast<int64_t>(pair) * 2 + slot) * 128 + d0 / 4) * kItem + pline;
 #pragma unroll 1
