@@ -446,7 +446,9 @@ size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
  *   slots = table[positions / block_size] * block_size + positions % block_size,
  *   block_table row = the request's need blocks, then -1 up to max_blocks_per_seq
  * An empty row has position 0, seq_len 0, slot -1 and a table row of -1.  Rows
- * from row_start[seqs] on are left as they were.
+ * from row_start[seqs] on are left as they were, slots of an earlier step
+ * among them: calls that write by row (dsa_latent_write) are given the rows before
+ * it, which whoever packs their inputs knows to be the sum of new_tokens.
  * A request with n outside [0, min(L, rows)], need > max_blocks_per_seq or h
  * outside [0, max_blocks_per_seq] is recorded (DSA_DEVERR_SEQ_LEN, with s as
  * the row) and changes nothing; its n rows, if 0 <= n <= rows, are empty.

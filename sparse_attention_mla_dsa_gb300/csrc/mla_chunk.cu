@@ -40,6 +40,16 @@
 // of the largest, so that a long tail of small weights is not lost).  Two FP8
 // terms cost what one 16-bit term would and need no conversion of the latents.
 // Products, sums, maxima and the output are FP32.
+//
+// What bounds it.  A tile's 64 MMAs take 4,100 clocks and its copies as many; the
+// two, each waiting for blocks that the other holds, take ~5,400 together, with
+// the card at its power limit (1.4 kW) in long calls.  1,024 rows of 64 heads at
+// 9,000 tokens: 715 us, 1.6 PFLOP/s counting only visible tokens.  64 tokens of 128
+// heads at up to 128k: 390 us.  32 tokens of 64 heads (half of every MMA is empty)
+// at up to 64k: 149 us, 2.9 TB/s of latents.  An item costs 11,000 clocks besides:
+// Q through the same 32 bytes a clock (2,500), its conversion (2,800), the output's
+// store (3,700), the warps' meetings; 2,049 rows of 128 heads, an item each: 499
+// us.  One token of 16 heads: 16 us a call, most of it two cold starts.
 #include <mutex>
 
 #include "dsa_device.cuh"
@@ -65,7 +75,9 @@ constexpr uint32_t kCtlOff = kBlockOff + kBlocks * kBlockBytes;
 constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
 constexpr int kMasks = 8;            // tiles whose token masks are kept (the copies are up to four ahead)
-constexpr int kItemCost = 2;         // an item costs what so many tiles cost, besides its tiles
+// An item costs what so many tiles cost, besides its tiles (2,049 rows of 128 heads:
+// 668 us with 1, 535 with 2, 521 with 3; a ragged batch of 24: 257, 223, 239).
+constexpr int kItemCost = 2;
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
 constexpr int kMergeThreads = 256;
@@ -172,7 +184,7 @@ struct Place {
   int64_t off;     // cost of the item before the place: its own first, then its tiles
 };
 
-// Finds the place `target(per)` of the call: every thread sums a run of requests,
+// Finds place `target(per)` of the call: every thread sums a run of requests,
 // the CTA scans the sums, and the thread whose run holds it walks to it.
 // `scratch`: kN int64 and a Place of shared memory.  Returns seq -1 past the end.
 template <int kN, typename Target>
@@ -636,8 +648,9 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
   const int from = rank ? 128 : 0;             // K: the tokens of this CTA
   uint32_t looked = 0, n = 0, segs = 0;
   int64_t at = kV ? 0 : per * pair - w.off;    // cost of the call before the item
-  // K: leaves the segment for the softmax warps (at most three ahead of them: a
-  // tile's blocks are free once the O of the tile two before is complete).
+  // K: leaves the segment for the softmax warps (at most two ahead of them: the
+  // copies before waited for an S of this segment's last or the one before that,
+  // whose Q the softmax warps converted when they were done with what came before).
   auto publish = [&](const SegRecord& r) {
     if (lane == 0) {
       ctl->seg[segs % kSegs] = r;
@@ -1359,7 +1372,9 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
 }
 
 // CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 4 of
-// one with many (few items then, which have to reach every SM).
+// one with many (few items then, which have to reach every SM).  All as few: one
+// decode at 32k, 65 parts, 24 -> 43 us a call; all as many: a prompt of 1,024 rows,
+// whose items have two parts or three, 715 -> 772, a ragged batch 223 -> 279.
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
   constexpr int kFew = 8;
   __shared__ ChunkRecord rec[kMaxPairs];
@@ -1420,7 +1435,9 @@ size_t mla_chunk_workspace_bytes(int pairs) {
 }
 
 // Token rows of one copy: the largest power of two, 64 at most, that divides
-// the block; under 8 the rows are gathered four at a time.
+// the block.  A warp has a copy for each lane, so 8 rows at least for the tile's
+// 256 tokens; below that the rows are gathered four at a time, or sixteen where
+// they run on (a ragged batch in pages of 20: 362 us by fours alone, 274 so).
 int mla_chunk_box_rows(int block_size) {
   int h = 64;
   while (block_size % h != 0) h >>= 1;
@@ -1428,7 +1445,7 @@ int mla_chunk_box_rows(int block_size) {
 }
 
 // What the host knows of the work: a call that can only have one tile (a first
-// token at few heads) is one pair, with nothing to merge: 20 us become 14.
+// token at few heads) is one pair, with nothing to merge: 17.3 us become 16.0.
 int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms) {
   const int64_t items = static_cast<int64_t>(rows) * heads / kItem + (seqs->seqs < rows ? seqs->seqs : rows);
   const int64_t tiles = (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq + kTile - 1) / kTile;

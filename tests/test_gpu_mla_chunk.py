@@ -138,6 +138,16 @@ def test_many_requests(api):
     run(api, Case([(s % 37, s % 3) for s in range(1100)], 16, 16, seed=3, spare_rows=2))
 
 
+@pytest.mark.parametrize("heads, block", [(48, 16), (64, 5), (80, 64)])
+def test_full_and_partly_filled_items_in_turn(api, heads, block):
+    # Every range has several items, of few lines and of many, of one tile and of
+    # more; the tokens after each one's last are NaN.
+    rng = np.random.default_rng(heads)
+    reqs = [(int(rng.integers(0, 600)) if s % 5 == 0 else int(rng.integers(0, 40)), int(rng.choice([1, 1, 1, 2, 3, 5])))
+            for s in range(400)]
+    run(api, Case(reqs, heads, block, seed=heads, spare_rows=1))
+
+
 def test_no_new_tokens_at_all(api):
     run(api, Case([(50, 0), (0, 0)], 64, 64, spare_rows=3))
 
