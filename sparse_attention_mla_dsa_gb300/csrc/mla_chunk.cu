@@ -1222,23 +1222,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (rank == 1 && tid < kBlocks)
     asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(map_to(&ctl->peer_fills[tid], 0)), "h"(ctl->fills[tid]) : "memory");
-  cluster_sync();
-  // No CTA leaves with a copy of either in flight.  All are complete unless a
-  // wait gave up; then one CTA may have begun a block's copies that the other
-  // has not, and the bytes that will not come are made up for.
-  if (rank == 0 && tid < kBlocks) {
-    uint64_t* const full = tid < 4 ? &ctl->kfull[tid] : &ctl->vfull[tid - 4];
-    const uint16_t mine = ctl->fills[tid], other = ctl->peer_fills[tid];
-    const int ahead = static_cast<int16_t>(mine - other);   // -1, 0 or 1
-    const uint32_t n = ahead >= 0 ? mine : other;
-    if (ahead > 0)
-      asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full)), "r"(kBlockBytes) : "memory");
-    else if (ahead < 0)
-      mbar_arrive_expect_tx(full, kBlockBytes);
-    if (n > 0) mbar_wait(full, (n - 1) & 1, kDrainWaitNs);
-  }
-  __syncthreads();
   cluster_sync();     // neither CTA leaves while the other may still signal it
+  // Nor with a copy of either in flight.  All are complete unless a wait gave up
+  // (which both know by now); then one CTA may have begun a block's copies that the
+  // other has not, and the bytes that will not come are made up for.
+  if (aborted(ctl)) {
+    if (rank == 0 && tid < kBlocks) {
+      uint64_t* const full = tid < 4 ? &ctl->kfull[tid] : &ctl->vfull[tid - 4];
+      const uint16_t mine = ctl->fills[tid], other = ctl->peer_fills[tid];
+      const int ahead = static_cast<int16_t>(mine - other);   // -1, 0 or 1
+      const uint32_t n = ahead >= 0 ? mine : other;
+      if (ahead > 0)
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full)), "r"(kBlockBytes) : "memory");
+      else if (ahead < 0)
+        mbar_arrive_expect_tx(full, kBlockBytes);
+      if (n > 0) mbar_wait(full, (n - 1) & 1, kDrainWaitNs);
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
