@@ -836,14 +836,11 @@ __device__ __forceinline__ void issue_mmas(const ChunkParams& p, Ctl* ctl, uint3
   mbar_wait(&ctl->drain[kPv], 0, kDrainWaitNs);
 }
 
-// Q of the segment's 64 lines of this CTA: q * 2^s = hi + lo, s a power of two a
-// line that puts its largest |q| in [128, 256), negated where the logits' scale
-// is negative (so that it never is in the softmax).  Warp w converts lines w, w +
-// 16, ...; lane l dims 16l..16l+15.  Lines past the request's last are zero.
-__device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_t* qop, int64_t gline, int lines, int sw,
-                                          int lane) {
-  constexpr int kPer = kLines / kSoftmaxWarps;
-  uint4 qa[kPer], qb[kPer];
+// This warp's lines of Q in registers: lines w, w + 16, ... of warp w, dims 16l ..
+// 16l + 15 in lane l.  Lines past the request's last are zero.
+constexpr int kPer = kLines / kSoftmaxWarps;
+__device__ __forceinline__ void load_q(const ChunkParams& p, int64_t gline, int lines, int sw, int lane, uint4 (&qa)[kPer],
+                                       uint4 (&qb)[kPer]) {
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = sw + j * kSoftmaxWarps;
@@ -854,20 +851,22 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
       qb[j] = ld_dep_u4(src + 1);
     }
   }
+}
+// Q of the segment's lines of this CTA: q * 2^s = hi + lo, s a power of two a line
+// that puts its largest |q| in [128, 256), negated where the logits' scale is
+// negative (so that it never is in the softmax).
+__device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_t* qop, const uint4 (&qa)[kPer],
+                                          const uint4 (&qb)[kPer], int sw, int lane) {
   const float sz = p.sm_scale * p.kv_scale * 1.4426950408889634f;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = sw + j * kSoftmaxWarps;
     const uint32_t w[8] = {qa[j].x, qa[j].y, qa[j].z, qa[j].w, qb[j].x, qb[j].y, qb[j].z, qb[j].w};
-    auto bf2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
-    __nv_bfloat162 top = __habs2(bf2(w[0]));
+    // |q| as an integer orders as |q| does, infinities and NaN on top.
+    uint32_t top = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) top = __hmax2_nan(top, __habs2(bf2(w[k])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      top = __hmax2_nan(top, bf2(__shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&top), o)));
-    const __nv_bfloat16 amax = __hmax_nan(__low2bfloat16(top), __high2bfloat16(top));
-    const uint32_t bits = static_cast<uint32_t>(__bfloat16_as_ushort(amax)) << 16;  // >= 0
+    for (int k = 1; k < 8; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+    const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu)) << 16;
     const bool finite = bits < 0x7F800000u;
     // amax < 2^(field - 126); 2^sh puts it in [128, 256)
     const int sh = finite ? min(126, 134 - static_cast<int>(bits >> 23)) : 0;
@@ -886,7 +885,9 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t x = w[2 * k + u];
-        split_q(pack_f16(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale), hc[u], lc[u]);
+        const float2 f = fma2(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)),
+                              make_float2(scale, scale), make_float2(-0.0f, -0.0f));
+        split_q(pack_f16(f.x, f.y), hc[u], lc[u]);
       }
       hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
       lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
@@ -921,25 +922,27 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
   auto wait_o = [&](uint32_t n) { return wait_all(ctl, &ctl->vread[2 * (n & 1) + 1], (n >> 1) & 1, lane, p); };
   uint32_t ns = 0, nv = 0, seg = 0;                     // tiles, masked tiles, segments done
   bool ok = true;
-  // One warp looks whether there is another segment, all go by its answer.
-  auto find_next = [&]() {
-    if (sw == 0) {
-      const bool there = wait_segment(ctl, seg, lane, p);
-      if (lane == 0) ctl->more = there && ctl->seg[seg % kSegs].end > ctl->seg[seg % kSegs].begin ? 1 : 0;
-    }
-    softmax_sync();
-    return *reinterpret_cast<volatile int*>(&ctl->more) != 0;
-  };
+  // The next segment's Q, loaded before the warps meet.  One warp's view of whether
+  // there is one is everyone's.
   auto next_q = [&]() {
+    const bool there = wait_segment(ctl, seg, lane, p);
     const SegRecord& r = ctl->seg[seg % kSegs];
+    const bool some = there && r.end > r.begin;
     const int own = cta_lines(r.lines), before = static_cast<int>(rank) * own;
-    convert_q(p, ctl, qop, r.gline + before, min(own, r.lines - before), sw, lane);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0 && ok) arrive_at(qready);
+    uint4 qa[kPer], qb[kPer];
+    load_q(p, r.gline + before, some ? min(own, r.lines - before) : 0, sw, lane, qa, qb);
+    if (sw == 0 && lane == 0) ctl->more = some ? 1 : 0;
+    softmax_sync();
+    const bool go = *reinterpret_cast<volatile int*>(&ctl->more) != 0;
+    if (go) {
+      convert_q(p, ctl, qop, qa, qb, sw, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && ok) arrive_at(qready);
+    }
+    return go;
   };
-  bool more = find_next();
-  if (more) next_q();
+  bool more = next_q();
   softmax_sync();                                       // qexp
   while (more) {
     const SegRecord& g = ctl->seg[seg % kSegs];
@@ -1095,8 +1098,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     const int parts = g.parts, item_lines = min(kItem, g.lines);
     ctl->red[part][i] = l;
     ++seg;
-    more = find_next();                                 // (and: l; qexp has been read)
-    if (more) next_q();
+    more = next_q();                                    // (and: l; qexp has been read)
     // The line's sum in a fixed order, then its output.
     float lt = ctl->red[0][i];
 #pragma unroll
