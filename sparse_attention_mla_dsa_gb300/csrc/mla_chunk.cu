@@ -41,15 +41,16 @@
 // terms cost what one 16-bit term would and need no conversion of the latents.
 // Products, sums, maxima and the output are FP32.
 //
-// What bounds it.  A tile's 64 MMAs take 4,100 clocks and its copies as many; the
-// two, each waiting for blocks that the other holds, take ~5,400 together, with
-// the card at its power limit (1.4 kW) in long calls.  1,024 rows of 64 heads at
-// 9,000 tokens: 715 us, 1.6 PFLOP/s counting only visible tokens.  64 tokens of 128
-// heads at up to 128k: 390 us.  32 tokens of 64 heads (half of every MMA is empty)
-// at up to 64k: 149 us, 2.9 TB/s of latents.  An item costs 11,000 clocks besides:
-// Q through the same 32 bytes a clock (2,500), its conversion (2,800), the output's
-// store (3,700), the warps' meetings; 2,049 rows of 128 heads, an item each: 499
-// us.  One token of 16 heads: 16 us a call, most of it two cold starts.
+// What bounds it.  A tile's 64 MMAs take 4,100 clocks and its copies as many, each
+// waiting for blocks that the other holds: the tensor pipe is busy 89 % of the time
+// (1,024 rows of 64 heads at 9,000 tokens, one launch of 600 us) and the card at its
+// power limit in calls after each other: 685 us then, 1.66 PFLOP/s counting only
+// visible tokens.  64 tokens of 128 heads at up to 128k: 370 us.  32 tokens of 64
+// heads (half of every MMA is empty) at up to 64k: 137 us, 3.1 TB/s of latents.  An
+// item costs ~10,000 clocks besides: Q through the same 32 bytes a clock (3,800),
+// its conversion (2,400), the output's store (3,800), the warps' meetings; 2,049
+// rows of 128 heads, an item each: 470 us.  One token of 16 heads: 15 us a call,
+// most of it first times.
 #include <mutex>
 
 #include "dsa_device.cuh"
