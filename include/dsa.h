@@ -540,8 +540,8 @@ typedef struct dsa_seqs {
  * beside other rows.
  * latent_dim must be 512; heads a multiple of 16 up to 4096; rows <= 65535;
  * seqs <= DSA_PLAN_MAX_SEQS; nslots below 2^31; block_size *
- * max_blocks_per_seq at most 2^30 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and out 16-byte aligned; out
- * must not overlap q or the pool.  The workspace holds
+ * max_blocks_per_seq at most 2^30 (DSA_ERR_UNSUPPORTED otherwise).  q, pool and
+ * out 16-byte aligned; out must not overlap q or the pool.  The workspace holds
  * dsa_chunk_workspace_bytes(rows, heads) bytes, 256-byte aligned
  * (DSA_ERR_WORKSPACE otherwise), needs no initial value, and belongs to the call
  * until its work completes: calls that may overlap on the GPU (other streams,

@@ -51,8 +51,6 @@
 // its conversion (2,400), the output's store (3,800), the warps' meetings; 2,049
 // rows of 128 heads, an item each: 470 us.  One token of 16 heads: 15 us a call,
 // most of it first times.
-#include <mutex>
-
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
 
@@ -188,7 +186,10 @@ struct Place {
 
 // Finds place `target(per)` of the call: every thread sums a run of requests,
 // the CTA scans the sums, and the thread whose run holds it walks to it.
-// `scratch`: kN int64 and a Place of shared memory.  Returns seq -1 past the end.
+// `scratch`: kN int64 and a Place of shared memory, free again after the caller's
+// next barrier.  Returns seq -1 past the end.  (All threads read the answer from
+// shared memory: values that a shuffle gave are not known to be the same in all
+// lanes, and what is computed from them then costs long calls 2 to 10 %.)
 template <int kN, typename Target>
 __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Target target,
                                             int64_t* scratch, bool report) {
@@ -202,26 +203,26 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
     if (why != 0 && report) record_error(p.err, why, s);
     sum += seq_cost(p, q);
   }
-  scratch[tid] = sum;
+  // A scan over the warp, then one of the warps' sums.
+  const int lane = tid & 31, warp = tid >> 5;
+  int64_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) scratch[warp] = upto;
   if (tid == 0) found.seq = -1;
   __syncthreads();
   if (tid < 32) {
-    constexpr int kPer = (kN + 31) / 32;
-    int64_t mine = 0;
-    for (int i = 0; i < kPer; ++i)
-      if (tid * kPer + i < kN) mine += scratch[tid * kPer + i];
+    const int64_t mine = tid < kN / 32 ? scratch[tid] : 0;
     int64_t x = mine;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (tid >= o) x += y;
     }
-    int64_t at = x - mine;
-    for (int i = 0; i < kPer; ++i)
-      if (tid * kPer + i < kN) {
-        const int64_t v = scratch[tid * kPer + i];
-        scratch[tid * kPer + i] = at;
-        at += v;
-      }
+    if (tid < kN / 32) scratch[tid] = x - mine;
     if (tid == 31) {
       found.total = x;
       found.per = max(static_cast<int64_t>(1), div_small(x + pairs - 1, static_cast<uint32_t>(pairs)));
@@ -229,7 +230,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
   }
   __syncthreads();
   const int64_t want = target(found.per);
-  int64_t at = scratch[tid];
+  int64_t at = scratch[warp] + upto - sum;
   if (want < found.total && want >= at && want < at + sum) {
     for (int s = s0; s < s1; ++s) {
       const SeqInfo q = seq_info(p, s);
@@ -241,23 +242,21 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
       int64_t off = want - at;
       int below = 0;
       for (int v = (q.ctx + kTile) / kTile;; ++v) {
-        const int upto = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
-        const int64_t here = static_cast<int64_t>(upto - below) * (v + kItemCost);
+        const int within = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
+        const int64_t here = static_cast<int64_t>(within - below) * (v + kItemCost);
         if (off < here) {
           found.seq = s;
           found.item = below + static_cast<int>(div_small(off, static_cast<uint32_t>(v + kItemCost), &found.off));
           break;
         }
         off -= here;
-        below = upto;
+        below = within;
       }
       break;
     }
   }
   __syncthreads();
-  const Place out = found;
-  __syncthreads();
-  return out;
+  return found;
 }
 
 // The part of one item in a pair's range, and the walk over the range.
