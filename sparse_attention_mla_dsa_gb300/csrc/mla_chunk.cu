@@ -328,10 +328,8 @@ __device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same for data that threads of the other CTA read.
-__device__ __forceinline__ void arrive_release_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
+// Orders what the leader's MMAs thread announced (V has landed) before this
+// thread's reads of it.
 __device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ bool aborted(Ctl* c) {
   return *reinterpret_cast<volatile int*>(&c->abort_flag) != 0;
