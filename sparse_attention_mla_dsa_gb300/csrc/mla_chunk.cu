@@ -75,7 +75,7 @@ constexpr uint32_t kTmemCols = 512;  // O: 0..255, S: 256 + 128 * buffer
 constexpr uint32_t kSCol = 256;
 constexpr int kMasks = 8;            // tiles whose token masks are kept (the copies are up to four ahead)
 // An item costs what so many tiles cost, besides its tiles (2,049 rows of 128 heads:
-// 668 us with 1, 535 with 2, 521 with 3; a ragged batch of 24: 257, 223, 239).
+// 558 us with 1, 473 with 2 or 3; a ragged batch of 24: 230, 200, 213).
 constexpr int kItemCost = 2;
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
 constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
@@ -294,8 +294,7 @@ __device__ __forceinline__ bool next_segment(const ChunkParams& p, Walk& w, Segm
 // Lines of an item in each CTA of its pair, of `lines` that the request has from
 // the item's first on: those of a half-empty item (one token at 64 heads) are
 // shared by both, which then load, convert and store half of them each (one decode
-// 26.2 -> 24.4 us, a decode batch 150 -> 147; items of 128 lines lose 1.8 % by the
-// tests: a prompt of 2,049 rows 487 -> 495).
+// 23.6 -> 22.5 us, 32 decodes 137.5 -> 136.8).
 __device__ __forceinline__ int cta_lines(int lines) { return lines > kLines ? kLines : kLines / 2; }
 
 // ------------------------------------------------------------------ pair
@@ -1415,8 +1414,8 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
 
 // CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 4 of
 // one with many (few items then, which have to reach every SM).  All as few: one
-// decode at 32k, 65 parts, 24 -> 43 us a call; all as many: a prompt of 1,024 rows,
-// whose items have two parts or three, 715 -> 772, a ragged batch 223 -> 279.
+// decode at 32k, 65 parts, 22.5 -> 41 us a call; all as many: a prompt of 1,024
+// rows, whose items have two parts or three, 686 -> 724, a ragged batch 200 -> 255.
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
   constexpr int kFew = 8;
   __shared__ ChunkRecord rec[kMaxPairs];
@@ -1487,7 +1486,7 @@ int mla_chunk_box_rows(int block_size) {
 }
 
 // What the host knows of the work: a call that can only have one tile (a first
-// token at few heads) is one pair, with nothing to merge: 17.3 us become 16.0.
+// token at few heads) is one pair, with nothing to merge: 15.9 us become 14.6.
 int mla_chunk_pairs(const dsa_seqs* seqs, int rows, int heads, int num_sms) {
   const int64_t items = static_cast<int64_t>(rows) * heads / kItem + (seqs->seqs < rows ? seqs->seqs : rows);
   const int64_t tiles = (static_cast<int64_t>(seqs->block_size) * seqs->max_blocks_per_seq + kTile - 1) / kTile;

@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
   }
   // A warp's turn is kSpan entries of `run` consecutive rows, whose request's
   // entries are looked up and loaded once; single rows while there are warps to
-  // spare (12,000 rows of 1,031 entries: 25.1 us by single rows, 15.4 by fours,
-  // where a fill of the tables takes 7.2).
+  // spare (12,000 rows of 1,031 entries: 17.6 us by single rows, 12.8 by fours,
+  // where a fill of the tables takes 7.4; 28 rows of 1,025: 4.7 by single rows, 6.2
+  // by fours).
   const int width = p.max_blocks_per_seq, spans = (width + kSpan - 1) / kSpan;
   const int run = static_cast<int64_t>(out_rows) * spans >= 4ll * nwarps ? 4 : 1;
   const int turns = p.row_table != nullptr ? (out_rows + run - 1) / run * spans : 0;
