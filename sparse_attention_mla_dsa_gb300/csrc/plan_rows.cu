@@ -75,6 +75,9 @@ struct Scan {
   int* need;   // blocks needed after it; -1: invalid request
 };
 
+constexpr size_t scan_bytes(int seqs) { return 5 * (static_cast<size_t>(seqs) + 1) * sizeof(int); }
+static_assert(scan_bytes(DSA_PLAN_MAX_SEQS) + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+
 // Index of the last entry of the exclusive prefix `a` [n + 1] that is <= x,
 // among the requests (0 <= x < a[n]): the request that x falls into.
 __device__ __forceinline__ int find(const int* a, int n, int x) {
@@ -306,10 +309,14 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
 }  // namespace
 
 cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t stream) {
-  const size_t smem = 5 * (static_cast<size_t>(p.p.seqs) + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  const size_t smem = scan_bytes(p.p.seqs);
+  // Above 48 KB a block in all, its static part included, a kernel has to ask.  Every
+  // call asks for the most there can be: the setting is the process's, so that host
+  // threads which plan batches of different sizes must not lower it for each other.
+  static_assert(sizeof(Shared) <= 1008, "47 KB leave room for it");
+  if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(scan_bytes(DSA_PLAN_MAX_SEQS)));
     if (e != cudaSuccess) return e;
   }
   // A CTA for every 32 warps' turns, 1,024 rows or 64 requests, up to one a SM: each scans

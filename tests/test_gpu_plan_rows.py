@@ -1,5 +1,10 @@
 """dsa_plan_rows against a loop over the requests: every output an integer,
 compared exactly, with rows and table entries that must stay as they were."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -149,6 +154,55 @@ def test_as_many_requests_as_allowed(api):
     st.lengths(rng.integers(1, 13, 8192), new)
     api.dsa_plan_rows(st.plan(api))
     st.check(api, st.expect())
+
+
+def sizes_around_48_kb():
+    # The scan's 20 bytes a request and the kernel's fixed part pass 48 KB here.
+    from sparse_attention_mla_dsa_gb300 import api
+    for seqs in (2405, 2406, 2430, 2436, 2437, 2438, 2450, 2456, 2457):
+        rng = np.random.default_rng(seqs)
+        st = State(seqs, 2, 4, seqs * 2, 2600, 13)
+        st.lengths(rng.integers(1, 9, seqs), rng.integers(0, 2, seqs))
+        api.dsa_plan_rows(st.plan(api))
+        st.check(api, st.expect())
+
+
+def test_around_48_kb_of_shared_memory(api):
+    # In a process of its own, where no larger batch has been planned before.
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = "from tests.test_gpu_plan_rows import sizes_around_48_kb as f; f()"
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_with_batches_of_other_sizes(api):
+    # Each thread's calls ask for another amount of shared memory; neither may
+    # take away what the other has asked for.
+    rng = np.random.default_rng(7)
+    states, failures = [], []
+    for seqs in (8192, 2500):
+        st = State(seqs, 2, 4, seqs * 2, 600, 14, row_table=False)
+        new = np.zeros(seqs, np.int64)
+        new[rng.permutation(seqs)[:500]] = 1
+        st.lengths(rng.integers(1, 9, seqs), new)
+        states.append((st, st.plan(api), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(plan, stream):
+        try:
+            for _ in range(3000):
+                api.dsa_plan_rows(plan, stream=stream)
+        except Exception as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(plan, stream)) for _, plan, stream in states]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+    for st, _, _ in states:
+        st.check(api, st.expect())
 
 
 @pytest.mark.parametrize("row_table, row_seq", [(False, True), (True, False), (False, False)])
