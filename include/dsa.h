@@ -533,8 +533,11 @@ typedef struct dsa_seqs {
  * Numerics: the latents enter the FP8 tensor cores as they are; q as two E4M3
  * terms an element (as in dsa_mla_decode_fp8), a softmax weight as an E4M3 term
  * and the E5M2 term of its remainder: within 2^-7 of the weight, about 2^-9.6
- * rms, down to 2^-25 of the line's largest.  Logits, sums, maxima and the
- * output are FP32, lse uses the unrounded weights.  The tokens are shared out
+ * rms, down to 2^-14 of the line's largest.  A smaller one is within 2^-21 of the
+ * largest or a quarter of itself, whichever is less (but 2^-24 of the largest is
+ * the smallest step), rounded up or down by the token's place: the sum over many
+ * like weights is right to 2^-7 down to 2^-24 of the largest.  Logits, sums, maxima
+ * and the output are FP32, lse uses the unrounded weights.  The tokens are shared out
  * among the SMs by the lengths of the whole call and partial results merged in
  * order: the same call gives the same bits, but a row's last bits may differ
  * beside other rows.

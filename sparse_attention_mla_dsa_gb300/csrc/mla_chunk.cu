@@ -35,10 +35,12 @@
 //
 // Precision.  The latents stay E4M3.  q * 2^s = hi + lo, two E4M3 terms, holds
 // a bf16 q exactly but for elements 2^10 below the head's largest; a softmax
-// weight is an E4M3 term and the E5M2 term of its remainder (2^-7 of the weight
-// at most, about 2^-9.6 rms; the second term's range keeps weights down to 2^-25
-// of the largest, so that a long tail of small weights is not lost).  Two FP8
-// terms cost what one 16-bit term would and need no conversion of the latents.
+// weight is an E4M3 term and the E5M2 term of its remainder: within 2^-7 of the
+// weight, about 2^-9.6 rms, down to 2^-14 of the line's largest; then within 2^-21
+// of the largest or a quarter of the weight, whichever is less, rounded up or down by
+// the token's place, so that sums over a long tail of small weights are not off
+// (split_weights).  Two FP8 terms cost what one 16-bit term would and need no
+// conversion of the latents.
 // Products, sums, maxima and the output are FP32.
 //
 // What bounds it.  A tile's 64 MMAs take 4,100 clocks and its copies as many, each
@@ -78,7 +80,9 @@ constexpr int kMasks = 8;            // tiles whose token masks are kept (the co
 // 558 us with 1, 473 with 2 or 3; a ragged batch of 24: 230, 200, 213).
 constexpr int kItemCost = 2;
 constexpr float kPMaxLog2 = 0.75f;   // a weight 2^(z - m) stays below 2^0.75 ...
-constexpr float kPScale = 256.0f;    // ... and 256 times it below the E4M3 maximum 448
+constexpr float kPLog2 = 8.0f;       // ... and 2^8 times it, as it is summed too, below the E4M3 maximum 448
+constexpr float kPUnit = 1.0f / 256.0f;
+constexpr float kSmallLog2 = 10.0f;  // weights of a thread that are all below 2^-10 are dithered
 constexpr int kMergeThreads = 256;
 constexpr int kMaxPairs = 256;
 static_assert(kMaxPairs == kMergeThreads, "a merge thread for every pair");
@@ -509,13 +513,30 @@ __device__ __forceinline__ void split_q(uint32_t h2, uint16_t& hi, uint16_t& lo)
   hi = split_e4m3(h2, r2);
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r2));
 }
-// Two softmax weights (already times 256): an E4M3 term and the E5M2 term of
-// the remainder.
-__device__ __forceinline__ void split_weights(uint32_t h2, uint16_t& hi, uint16_t& lo) {
-  uint32_t r2;
-  hi = split_e4m3(h2, r2);
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r2));
+// Two softmax weights (already times 2^8): an E4M3 term, returned, and the E5M2 term
+// of the remainder, left as the upper bytes of `lo`'s halves: E5M2 is fp16's upper
+// byte, so `add` to the lower byte before it goes is the rounding (half a step: 0x80).
+// Below 2^-14 of the line's largest, where E4M3 has no full precision, the two terms
+// keep so few bits that a long tail of like weights would all be rounded the same way
+// (131,072 weights of 1.125 x 2^-19 beside one of 1 were 11 % short).  A thread none
+// of whose 32 weights reaches 2^-10 therefore adds a dither, another of 0 .. 255 for
+// each of a tile's 256 tokens, so that as many are rounded up as their sum needs; a
+// weight of 2^-14 or more is still within 2^-7.  Beside a weight of 2^-10 the small
+// ones' errors, 31 of at most 2^-22, are under 2^-7 of it.  A weight of 0 stays 0.
+__device__ __forceinline__ uint16_t split_weights(uint32_t h2, uint32_t add, uint32_t& lo) {
+  uint32_t rest;
+  const uint16_t hi = split_e4m3(h2, rest);
+  lo = rest + add;
+  return hi;
 }
+constexpr uint32_t reverse_bits(uint32_t x, int n) {
+  uint32_t y = 0;
+  for (int i = 0; i < n; ++i) y |= ((x >> i) & 1u) << (n - 1 - i);
+  return y;
+}
+// The upper five bits of the dither of tokens k and k + 1 of a thread's 32: evenly
+// spread over tokens that follow each other.
+constexpr uint32_t dither_of(int k) { return (reverse_bits(k, 5) << 3) | (reverse_bits(k + 1, 5) << 19); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1035,26 +1056,38 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         }
         line_sync(group);                               // red[] has been read
       }
-      const float base = m == -INFINITY ? 0.0f : -m;    // nothing seen yet: every weight is 0
+      const float base = m == -INFINITY ? 0.0f : kPLog2 - m;  // nothing seen yet: every weight is 0
       float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};     // of the tile first: a long tail of small weights
       uint32_t hw[kTok / 4], lw[kTok / 4];              // would be rounded away against a large running sum
+      auto weigh = [&](uint32_t vary, uint32_t same) {
 #pragma unroll
-      for (int k = 0; k < kTok / 4; ++k) {
-        uint16_t hc[2], lc[2];
+        for (int k = 0; k < kTok / 4; ++k) {
+          uint16_t hc[2];
+          uint32_t lc[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float2 x = fma2(make_float2(z[4 * k + 2 * u], z[4 * k + 2 * u + 1]), make_float2(scale, scale),
-                                make_float2(base, base));
-          const float2 e = make_float2(ex2(x.x), ex2(x.y));
-          sum[u].x += e.x;
-          sum[u].y += e.y;
-          const uint32_t h2 = pack_f16(e.x, e.y);
-          const __half2 s2 = __hmul2(*reinterpret_cast<const __half2*>(&h2), __float2half2_rn(kPScale));
-          split_weights(*reinterpret_cast<const uint32_t*>(&s2), hc[u], lc[u]);
+          for (int u = 0; u < 2; ++u) {
+            const float2 x = fma2(make_float2(z[4 * k + 2 * u], z[4 * k + 2 * u + 1]), make_float2(scale, scale),
+                                  make_float2(base, base));
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[u].x += e.x;
+            sum[u].y += e.y;
+            hc[u] = split_weights(pack_f16(e.x, e.y), (dither_of(4 * k + 2 * u) & vary) ^ same, lc[u]);
+          }
+          hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
+          lw[k] = __byte_perm(lc[0], lc[1], 0x7531);
         }
-        hw[k] = static_cast<uint32_t>(hc[0]) | (static_cast<uint32_t>(hc[1]) << 16);
-        lw[k] = static_cast<uint32_t>(lc[0]) | (static_cast<uint32_t>(lc[1]) << 16);
-      }
+      };
+      // Half a step added in the rounding; or, of the dither, what a token's tile and
+      // the eight threads of a line differ in.  (Two copies, as the dither's steps slow
+      // the warps that gather beside these: a ragged batch in pages of 20 took 203 us
+      // with them alone, 200 so, 196 without.)
+      const bool small = mx < m - kSmallLog2;
+      if (__any_sync(0xFFFFFFFFu, small))
+        weigh(small ? 0x00FF00FFu : 0u,
+              small ? ((static_cast<uint32_t>(all_see >> 8) * 0x9Du & 0xFFu) ^ static_cast<uint32_t>(part)) * 0x00010001u
+                    : 0x00800080u);
+      else
+        weigh(0u, 0x00800080u);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       // This half of P has been read: the MMAs take the tile's first 128 tokens
       // first, so it is written again while those of the second half run.
@@ -1120,7 +1153,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
     const int d0 = half * 256 + sub * 64;
     if (idle) {                                         // (nothing to leave)
     } else if (whole) {
-      const float inv = m != -INFINITY ? p.kv_scale / (kPScale * lt) : (lt != lt ? lt : 0.0f);
+      const float inv = m != -INFINITY ? p.kv_scale / lt : (lt != lt ? lt : 0.0f);
       // Through 2 KB of this warp's share of P, 32 lines x 32 dims at a time:
       // rows of 64 bytes, swizzled, which a copy then writes in whole sectors.
       uint8_t* const stage = pop + (part >> 1) * 8192 + group * 4096 + (part & 1) * 2048;
@@ -1153,7 +1186,7 @@ __device__ __forceinline__ void softmax(const CUtensorMap& omap, const ChunkPara
         __syncwarp();
       }
       if (ok && part == 0 && i < lines && p.lse != nullptr)
-        p.lse[gline0 + i] = lt != 0.0f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+        p.lse[gline0 + i] = lt != 0.0f ? (m + log2f(lt * kPUnit)) * 0.69314718055994531f : -INFINITY;
     } else {
       // Slot 0: the item began in an earlier range, 1: it goes on in a later one.
       // [128 groups of 4 dims][128 lines][4]: a warp's lines side by side.
@@ -1323,7 +1356,7 @@ __device__ __forceinline__ void merge_few(const ChunkParams& p, const ChunkRecor
       acc[d].w = acc[d].w * a + w0 * v[0][d].w + w1 * v[1][d].w;
     }
   }
-  const float inv = l != l ? l : (m != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
+  const float inv = l != l ? l : (m != -INFINITY ? p.kv_scale / l : 0.0f);
   const int64_t gline = r.line0 + line;
   uint4* out = reinterpret_cast<uint4*>(p.out + gline * 512 + d4 * 4);
 #pragma unroll
@@ -1337,7 +1370,7 @@ __device__ __forceinline__ void merge_few(const ChunkParams& p, const ChunkRecor
     out[d / 2] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (d4 == 0 && p.lse != nullptr)
-    p.lse[gline] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    p.lse[gline] = l != 0.0f ? (m + log2f(l * kPUnit)) * 0.69314718055994531f : -INFINITY;
 }
 
 // Many parts: four threads have a line and 4 dims and take every fourth part,
@@ -1402,14 +1435,14 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
   scale_by(ex2(m - base));
 #pragma unroll
   for (int k = 0; k < 3; ++k) add(x_ml[k][i].x, x_ml[k][i].y, x_acc[k][i], base);
-  const float inv = l != l ? l : (top != -INFINITY ? p.kv_scale / (kPScale * l) : 0.0f);
+  const float inv = l != l ? l : (top != -INFINITY ? p.kv_scale / l : 0.0f);
   const int64_t gline = r.line0 + line;
   uint32_t w[2];
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(acc.y * inv), "f"(acc.x * inv));
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[1]) : "f"(acc.w * inv), "f"(acc.z * inv));
   *reinterpret_cast<uint2*>(p.out + gline * 512 + d4 * 4) = make_uint2(w[0], w[1]);
   if (d4 == 0 && p.lse != nullptr)
-    p.lse[gline] = l != 0.0f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    p.lse[gline] = l != 0.0f ? (top + log2f(l * kPUnit)) * 0.69314718055994531f : -INFINITY;
 }
 
 // CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 4 of

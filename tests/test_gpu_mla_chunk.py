@@ -248,6 +248,50 @@ def test_one_token_over_a_long_flat_tail(api):
     run(api, c)
 
 
+def test_long_tails_of_like_weights(api):
+    # The same context 160 times, so that a range has it whole: one hot token,
+    # every other's weight 2^-13 to 2^-24 of it, another in each head.  What the tail
+    # gives is compared with its own size.  A weight is off by 2^-8 (two terms) and
+    # 2^-11 (fp16) down to 2^-14; the mean of a tile's like ones below by 1/256 of a step
+    # of a quarter or, in the last octaves, of up to the weight itself: 2^-8, and
+    # half of fp16's last step, 2^-9.  Then bf16's half step and the logits' error.
+    n, S = 156 * 256, 160
+    c = Case([(n - 1, 1)], 64, 64, seed=8)
+    base = torch.from_numpy(np.random.default_rng(0).uniform(0.5, 1.5, 512) / c.kv_scale).float()
+    codes = base.to(torch.float8_e4m3fn).view(torch.uint8).numpy().copy()
+    codes[0] = 0
+    c.pool[c.pool[:, 0] != NAN8] = codes
+    hot = c.slot(0, 777)
+    c.pool[hot] = 0
+    c.pool[hot, 0] = 0x78                                # 256
+    q = np.zeros((1, 64, 512))
+    q[0, :, 0] = np.linspace(13, 24, 64) * np.log(2) / (c.sm_scale * 256 * c.kv_scale)
+    c.q = bf16_bits(q)
+    out, lse, zmag = c.reference()[:3]
+    c.lens, c.start = np.repeat(c.lens, S), np.arange(S + 1, dtype=np.int32)
+    c.table, c.q, c.rows = np.repeat(c.table, S, 0), np.repeat(c.q, S, 0), S
+    c.upload(api).call(api)
+    g, e = c.result()
+    assert api.dsa_get_error(reset=True)[0] == 0
+    tol = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -8 + 16e-6 * zmag[0] + 1e-5
+    off = np.abs(g[:, :, 1:] - out[:, :, 1:]) / np.abs(out[:, :, 1:])
+    assert (off <= tol[None, :, None]).all(), f"{off.max((0, 2))}"
+    assert (np.abs(e - lse) <= 1e-5 + 8e-6 * zmag).all()
+
+
+def test_hidden_tokens_have_no_weight_at_all(api):
+    # Latents of zero where the rows see, as large as they can be where they do not.
+    c = Case([(300, 40), (0, 3), (20, 1)], 64, 64, seed=2)
+    c.pool[:] = 0
+    for s, last in ((0, 339), (1, 2)):
+        c.pool[c.slot(s, last)] = 0x7E
+    c.upload(api).call(api)
+    out, _ = c.result()
+    assert api.dsa_get_error(reset=True)[0] == 0
+    seen = np.isin(np.arange(c.rows), [39, 42])
+    assert (out[~seen] == 0).all() and (out[seen] != 0).any()
+
+
 def test_non_finite_queries_stay_in_their_head(api):
     c = Case([(200, 3)], 64, 64)
     q = c.q.copy()
