@@ -59,7 +59,7 @@
 extern "C" {
 #endif
 
-#define DSA_ABI_VERSION 5
+#define DSA_ABI_VERSION 6
 #define DSA_LATENT_DIM 512
 
 typedef enum dsa_status {
@@ -439,7 +439,10 @@ size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
  * from the top.  A request is refused when the blocks wanted up to and
  * including its own exceed F + Rtot: the blocks it wanted become -1 in its
  * table, it keeps h blocks, its rows are empty, and DSA_DEVERR_FREE is recorded.
- *   held_out[s] = need (h if refused), free_out[0] = blocks left on the stack.
+ *   held_out[s] = need (h if refused), free_out[0] = blocks left on the stack,
+ *   served_lens[s] = L (0 if refused or invalid), the seq_lens to give to
+ *   dsa_mla_chunk_fp8: the new tokens of a refused request have no latents, and those
+ *   that fall into its last block would be read as what that block held before.
  * Rows: request s owns rows row_start[s] .. row_start[s+1]-1, n of them; its
  * row i has
  *   positions = L-n+i, seq_lens = positions+1, row_seq = s,
@@ -488,14 +491,15 @@ typedef struct dsa_plan {
     int32_t block_size;
     int32_t free_capacity;
     int32_t reserved;            /* 0                                                    */
+    int32_t *served_lens;        /* [seqs] out; may be NULL                              */
 } dsa_plan;
 dsa_status dsa_plan_rows(const dsa_plan *plan, void *stream);
 
 /*
  * Per-request metadata of dsa_mla_chunk_fp8, all device pointers (as written
- * by dsa_plan_rows, or by the caller).  Request s has seq_lens[s] tokens in the
- * cache; its new ones, the last row_start[s+1] - row_start[s] of them, are the
- * rows row_start[s] .. row_start[s+1]-1 of q and out.
+ * by dsa_plan_rows, seq_lens its served_lens, or by the caller).  Request s has
+ * seq_lens[s] tokens in the cache; its new ones, the last row_start[s+1] -
+ * row_start[s] of them, are the rows row_start[s] .. row_start[s+1]-1 of q and out.
  */
 typedef struct dsa_seqs {
     const int32_t *seq_lens;     /* [seqs]                                               */
@@ -523,10 +527,11 @@ typedef struct dsa_seqs {
  * (DSA_DEVERR_BLOCK); a row that sees no token gets out = 0 and lse = -inf.  What
  * the pool holds at tokens a row does not see, NaN codes included, never
  * reaches the row.  A request whose rows lie outside [0, rows)
- * (DSA_DEVERR_ROWS), or with rows and seq_lens[s] < n or above
+ * (DSA_DEVERR_ROWS), or with rows and 0 != seq_lens[s] < n or above
  * max_blocks_per_seq * block_size (DSA_DEVERR_SEQ_LEN), is skipped, its rows
- * left as they were (the recorded row is s).  Rows of no request are left as
- * they were.  After a wait that gave up (DSA_DEVERR_TIMEOUT, row -1) the call's
+ * left as they were (the recorded row is s).  A request with rows and seq_lens[s]
+ * = 0 (one that dsa_plan_rows left empty, by its served_lens) has nothing to see:
+ * its rows get out = 0 and lse = -inf.  Rows of no request are left as they were.  After a wait that gave up (DSA_DEVERR_TIMEOUT, row -1) the call's
  * rows hold nothing to rely on.
  *   q   [rows][heads][latent_dim] bf16       pool [nslots][latent_dim] FP8
  *   out [rows][heads][latent_dim] bf16       lse  [rows][heads] fp32 or NULL

@@ -42,7 +42,8 @@ class Plan(ctypes.Structure):
         "free_out", "row_start", "positions", "slots", "row_lens", "row_table", "row_seq")]
         + [(n, ctypes.c_int32) for n in (
             "seqs", "rows", "max_blocks_per_seq", "bt_stride", "row_bt_stride", "block_size",
-            "free_capacity", "reserved")])
+            "free_capacity", "reserved")]
+        + [("served_lens", ctypes.c_void_p)])
 
 
 class Seqs(ctypes.Structure):
@@ -380,21 +381,24 @@ def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.T
               free_blocks: torch.Tensor, free_in: torch.Tensor, free_out: torch.Tensor,
               row_start: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
               row_lens: torch.Tensor, row_table: torch.Tensor | None = None,
-              row_seq: torch.Tensor | None = None) -> Plan:
+              row_seq: torch.Tensor | None = None,
+              served_lens: torch.Tensor | None = None) -> Plan:
     """Argument block of dsa_plan_rows over a server's buffers, built once and
     used every step.  int32 except slots (int64): seq_lens, new_tokens, held_in,
     held_out [S]; block_table [S, max_blocks]; free_blocks [capacity]; free_in
     [1 or 2]; free_out [2] (its second word starts at 0); row_start [S + 1];
     positions (or uint32), slots, row_lens, row_seq [R]; row_table [R,
     max_blocks].  held_out may be held_in and free_out free_in (state kept in
-    place).  The plan keeps the tensors alive."""
+    place).  served_lens [S], the lengths of the requests that have their blocks
+    and 0 for the others, is what make_seqs takes for the step's attention.  The
+    plan keeps the tensors alive."""
     S, R = seq_lens.shape[0], positions.shape[0]
     named = dict(seq_lens=seq_lens, new_tokens=new_tokens, held_in=held_in, held_out=held_out,
                  block_table=block_table, free_blocks=free_blocks, free_in=free_in,
                  free_out=free_out, row_start=row_start, positions=positions, slots=slots,
-                 row_lens=row_lens, row_table=row_table, row_seq=row_seq)
+                 row_lens=row_lens, row_table=row_table, row_seq=row_seq, served_lens=served_lens)
     device = _on_device(named)
-    for name in ("seq_lens", "new_tokens", "held_in", "held_out"):
+    for name in ("seq_lens", "new_tokens", "held_in", "held_out", "served_lens"):
         _shaped(named[name], (S,), name)
     for name in ("positions", "slots", "row_lens", "row_seq"):
         _shaped(named[name], (R,), name)

@@ -471,7 +471,7 @@ dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
                         static_cast<const void*>(p.free_in), static_cast<const void*>(p.free_out),
                         static_cast<const void*>(p.row_start), static_cast<const void*>(p.positions),
                         static_cast<const void*>(p.row_lens), static_cast<const void*>(p.row_table),
-                        static_cast<const void*>(p.row_seq)})
+                        static_cast<const void*>(p.row_seq), static_cast<const void*>(p.served_lens)})
     if (!aligned(q, 4)) return DSA_ERR_INVALID_ARG;
   if (!aligned(p.slots, 8)) return DSA_ERR_INVALID_ARG;
   if (p.seqs > DSA_PLAN_MAX_SEQS || p.rows > 65535) return DSA_ERR_UNSUPPORTED;

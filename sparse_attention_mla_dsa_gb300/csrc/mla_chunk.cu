@@ -129,7 +129,8 @@ struct SeqInfo {
 };
 
 // Rows, lines and items of request s; no items where it has no rows or is
-// refused (`why`: the error to record).
+// refused (`why`: the error to record).  One of length 0 with rows (-ctx of them, of
+// which none sees a token) has its items, of one tile with no tokens.
 __device__ __forceinline__ SeqInfo seq_info(const ChunkParams& p, int s, int* why = nullptr) {
   SeqInfo q;
   q.row0 = p.seqs.row_start[s];
@@ -137,7 +138,7 @@ __device__ __forceinline__ SeqInfo seq_info(const ChunkParams& p, int s, int* wh
   const int64_t rows = end - q.row0;
   int bad = 0;
   if (rows > 0 && (q.row0 < 0 || end > p.rows)) bad = DSA_DEVERR_ROWS;
-  else if (rows > 0 && (len < rows || len > static_cast<int64_t>(p.seqs.max_blocks_per_seq) * p.seqs.block_size))
+  else if (rows > 0 && len != 0 && (len < rows || len > static_cast<int64_t>(p.seqs.max_blocks_per_seq) * p.seqs.block_size))
     bad = DSA_DEVERR_SEQ_LEN;
   if (why != nullptr) *why = bad;
   q.rows = rows > 0 && bad == 0 ? static_cast<int>(rows) : 0;
@@ -151,8 +152,10 @@ __device__ __forceinline__ int item_end(const ChunkParams& p, const SeqInfo& q, 
   return q.ctx + (min(kItem * (j + 1), q.lines) - 1) / p.heads + 1;
 }
 __device__ __forceinline__ int item_tiles(const ChunkParams& p, const SeqInfo& q, int j) {
-  return (item_end(p, q, j) + kTile - 1) / kTile;
+  return max(1, (item_end(p, q, j) + kTile - 1) / kTile);
 }
+// The fewest tiles of an item of the request.
+__device__ __forceinline__ int least_tiles(const SeqInfo& q) { return max(1, (q.ctx + kTile) / kTile); }
 // How many of the request's items see at most x new tokens.
 __device__ __forceinline__ int items_within(const ChunkParams& p, const SeqInfo& q, int x) {
   return x <= 0 ? 0 : x >= q.rows ? q.items : x * p.heads / kItem;  // (65,535 x 4,096 lines at most)
@@ -163,7 +166,7 @@ __device__ __forceinline__ int64_t seq_cost(const ChunkParams& p, const SeqInfo&
   if (q.items == 0) return 0;
   int64_t sum = 0;
   int below = 0;
-  for (int v = (q.ctx + kTile) / kTile; below < q.items; ++v) {
+  for (int v = least_tiles(q); below < q.items; ++v) {
     const int upto = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
     sum += static_cast<int64_t>(upto - below) * (v + kItemCost);
     below = upto;
@@ -245,7 +248,7 @@ __device__ __forceinline__ Place find_place(const ChunkParams& p, int pairs, Tar
       }
       int64_t off = want - at;
       int below = 0;
-      for (int v = (q.ctx + kTile) / kTile;; ++v) {
+      for (int v = least_tiles(q);; ++v) {
         const int within = items_within(p, q, static_cast<int>(min(static_cast<int64_t>(v) * kTile - q.ctx, static_cast<int64_t>(q.rows))));
         const int64_t here = static_cast<int64_t>(within - below) * (v + kItemCost);
         if (off < here) {

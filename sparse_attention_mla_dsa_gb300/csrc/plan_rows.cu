@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
 
   if (first) {
     for (int s = tid; s <= n; s += kThreads) p.row_start[s] = sc.rows[s];
+    if (p.served_lens != nullptr)
+      for (int s = tid; s < n; s += kThreads) p.served_lens[s] = sc.need[s] < 0 || refused(s) ? 0 : p.seq_lens[s];
     if (tid == 0 && nrows > p.rows) record_error(kp.err, DSA_DEVERR_ROWS, find(sc.rows, n, p.rows));
   }
 

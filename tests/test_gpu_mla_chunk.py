@@ -202,6 +202,35 @@ def test_refused_requests_keep_their_rows(api):
     run(api, c, code=9)
 
 
+def empty_requests(c, which):
+    """Sets the requests' lengths to 0, and gives the reference for that."""
+    c.lens[which] = 0
+    ref = c.reference()
+    for s in which:
+        rows = slice(int(c.start[s]), int(c.start[s + 1]))
+        ref[1][rows], ref[5][rows] = -np.inf, True
+        for k in (0, 2, 3, 4):
+            ref[k][rows] = 0.0
+    return ref
+
+
+@pytest.mark.parametrize("reqs, which", [
+    ([(0, 1)], [0]), ([(500, 3)], [0]), ([(70, 5), (300, 2)], [0]), ([(300, 2), (70, 5)], [1]),
+    ([(10, 300), (700, 40), (0, 1), (5, 2)], [0, 3]), ([(40, 3)] * 3, [0, 1, 2])])
+@pytest.mark.parametrize("heads, block", [(16, 64), (64, 20), (128, 16)])
+def test_empty_requests_see_nothing(api, reqs, which, heads, block):
+    # A length of 0 with rows: what their tables name (latents of an earlier owner,
+    # NaN behind them) is not read.
+    c = Case(reqs, heads, block, seed=len(reqs), spare_rows=1)
+    run(api, c, ref=empty_requests(c, which))
+
+
+def test_empty_requests_among_many(api):
+    rng = np.random.default_rng(3)
+    c = Case([(int(rng.integers(0, 300)), int(rng.choice([0, 1, 1, 3, 9]))) for _ in range(300)], 48, 16, seed=9)
+    run(api, c, ref=empty_requests(c, rng.permutation(300)[:100]))
+
+
 @pytest.mark.parametrize("kind", ["sharp", "dominant", "rising", "mixed", "flat"])
 @pytest.mark.parametrize("ctx, new", [(2045, 3), (300, 40)])
 def test_peaked_rows(api, kind, ctx, new):
@@ -458,6 +487,41 @@ def test_plan_write_attend_together(api):
         api.dsa_mla_decode_fp8(r, q, pool, sel, topk, 0.02, 0.0625, out2, None, w2)
         torch.cuda.synchronize()
         paged_ref.check_chunk(out2.view(torch.bfloat16).float().cpu().numpy(), None, ref, f"gather step {k}")
+
+
+def test_a_request_out_of_blocks_reads_nothing(api):
+    # Request 1 has a last block with room, which holds what an earlier owner left
+    # there; it wants more blocks than there are.  Request 0 is served beside it.
+    rng = np.random.default_rng(5)
+    S, width, block, rows, heads = 2, 8, 16, 60, 64
+    d = lambda a, t=torch.int32: torch.tensor(a, dtype=t, device="cuda")  # noqa: E731
+    table = torch.full((S, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :1], table[1, :2] = d([3]), d([1, 4])
+    held, free, count = d([1, 2]), d([0, 2, 7, 7]), d([2, 0])
+    lens, new = np.array([20, 70]), np.array([8, 45])    # tokens 25 to 31 of request 1 would be new in what it has
+    start, pos, row_lens, served = d([0] * 3), d([0] * rows), d([0] * rows), d([9, 9])
+    slots, row_table = d([0] * rows, torch.int64), torch.zeros((rows, width), dtype=torch.int32, device="cuda")
+    pool = torch.from_numpy(rng.integers(0, 120, (5 * block, 512)).astype(np.uint8)).cuda()
+    plan = api.make_plan(d(lens), d(new), held, held, table, block, free, count, count, start, pos, slots,
+                         row_lens, row_table, served_lens=served)
+    n = int(new.sum())
+    kv_a = torch.from_numpy(bf16_bits(rng.standard_normal((n, 512))).view(np.int16)).cuda()
+    q = torch.from_numpy(bf16_bits(rng.standard_normal((n, heads, 512)) * 0.1).view(np.int16)).cuda()
+    out, lse = torch.full_like(q, MARK), torch.full((n, heads), 77.0, device="cuda")
+    ws = torch.empty(api.dsa_chunk_workspace_bytes(n, heads), dtype=torch.uint8, device="cuda")
+    api.dsa_plan_rows(plan)
+    assert api.DEVERR[api.dsa_get_error(reset=True)[0]] == "free"
+    api.dsa_latent_write(api.make_rows(row_lens[:n], row_table[:n], block, slots[:n], pos[:n]), kv_a,
+                         torch.full((512,), 0x3F80, dtype=torch.int16, device="cuda"), pool, 1e-6, 0.02)
+    api.dsa_get_error(reset=True)                        # the refused rows' slots
+    api.dsa_mla_chunk_fp8(api.make_seqs(served, start, table, block), q, pool, 0.02, 0.0625, out, lse, ws)
+    torch.cuda.synchronize()
+    assert api.dsa_get_error(reset=True)[0] == 0
+    assert served.tolist() == [20, 0] and row_lens[:n].tolist() == list(range(13, 21)) + [0] * 45
+    assert (out[8:] == 0).all() and torch.isneginf(lse[8:]).all()
+    ref = paged_ref.chunk([20], [0, 8], table[:1].cpu().numpy(), block, q[:8].cpu().numpy().view(np.uint16),
+                          pool.cpu().numpy(), 0.02, 0.0625)
+    paged_ref.check_chunk(out[:8].view(torch.bfloat16).float().cpu().numpy(), lse[:8].cpu().numpy(), ref)
 
 
 def test_forced_timeouts_are_reported_and_the_next_call_is_clean(api):

@@ -264,6 +264,47 @@ def test_more_rows_than_the_buffers_hold(api):
     st.check(api, ref)
 
 
+def served(api, st):
+    # The lengths that the attention is given; the rest of the plan as it is without.
+    out = torch.full((len(st.held) + 1,), MARK, dtype=torch.int32, device="cuda")
+    ref = st.expect()
+    api.dsa_plan_rows(api.make_plan(
+        st.d_lens, st.d_new, st.d_held, st.d_held_out, st.d_table, st.block, st.d_free, st.d_in, st.d_out,
+        st.row_start, st.positions, st.slots, st.row_lens, st.row_table, st.row_seq, served_lens=out[:-1]))
+    st.check(api, ref)
+    assert out[-1] == MARK
+    return out[:-1].tolist()
+
+
+def test_served_lengths_of_refused_requests(api):
+    st = State(6, 8, 4, 12, 20, 4, free=7)               # as in the test of refusals in order
+    st.held[3], st.held[5] = 1, 4
+    st.table[3, 0], st.table[5, :4] = 7, [8, 9, 10, 11]
+    st.d_table.copy_(dev(st.table))
+    st.d_held.copy_(dev(st.held))
+    st.lengths([12, 16, 9, 4, 1, 8], [4, 3, 2, 1, 1, 0])
+    assert served(api, st) == [12, 16, 0, 4, 0, 8]
+
+
+def test_served_lengths_of_invalid_requests(api):
+    st = State(9, 4, 8, 40, 16, 6)
+    st.held[:] = [1, 1, 1, 1, 1, -5, 9, 0, 0]
+    for s in (0, 1, 2, 3, 4):
+        st.table[s, 0] = 30 + s
+    st.d_table.copy_(dev(st.table))
+    st.d_held.copy_(dev(st.held))
+    st.lengths([9, 9, 2, 30, 33, 8, 8, 20, -3], [1, -1, 3, 17, 2, 1, 1, 4, 0])
+    assert served(api, st) == [9, 0, 0, 0, 0, 0, 0, 20, 0]
+
+
+@pytest.mark.parametrize("seqs", [1, 33, 1100, 8192])
+def test_served_lengths_of_served_requests(api, seqs):
+    st = State(seqs, 3, 4, seqs * 3, 9000, 15)
+    rng = np.random.default_rng(seqs)
+    st.lengths(rng.integers(1, 13, seqs), rng.integers(0, 2, seqs))
+    assert served(api, st) == st.lens.tolist()
+
+
 def test_bad_free_counts(api):
     for count in (-1, 41):
         st = State(2, 4, 8, 40, 16, 9)
@@ -338,3 +379,11 @@ def test_binding_checks(api):
             make(**kw)
     with pytest.raises(api.DsaError):
         api.dsa_plan_rows(make(block_size=0))
+
+
+def test_binding_checks_of_the_served_lengths(api):
+    st = State(3, 4, 8, 10, 6, 1)
+    for bad in (st.d_lens[:2], st.d_lens.long(), st.d_lens.cpu()):
+        with pytest.raises(ValueError, match="served_lens"):
+            api.make_plan(st.d_lens, st.d_new, st.d_held, st.d_held_out, st.d_table, 8, st.d_free, st.d_in,
+                          st.d_out, st.row_start, st.positions, st.slots, st.row_lens, served_lens=bad)

@@ -48,6 +48,10 @@ def test_plan_refusals(lib, changes, status):
     assert lib.dsa_plan_rows(_plan(**changes), None) == status
 
 
+def test_plan_refuses_served_lengths_off_their_alignment(lib):
+    assert lib.dsa_plan_rows(_plan(served_lens=X + 2), None) == 1
+
+
 def test_plan_without_a_plan(lib):
     assert lib.dsa_plan_rows(None, None) == 1
 
