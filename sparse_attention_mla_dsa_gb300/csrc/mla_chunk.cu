@@ -891,13 +891,14 @@ __device__ __forceinline__ void convert_q(const ChunkParams& p, Ctl* ctl, uint8_
     const bool finite = bits < 0x7F800000u;
     // amax < 2^(field - 126); 2^sh puts it in [128, 256)
     const int sh = finite ? min(126, 134 - static_cast<int>(bits >> 23)) : 0;
-    const float scale = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), sz);
+    // A line with an infinity or a NaN gives NaN logits, as its formula does: by its
+    // operand, so that one that sees no token has none.
+    const float scale = finite ? copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), sz) : NAN;
     if (lane == 0) {
-      // Never 0, which times a masked -inf would be NaN.  A line with an
-      // infinity or a NaN gives NaN logits, as its formula does.
+      // Never 0, which times a masked -inf would be NaN.
       float f = fabsf(sz) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       if (f < 1e-37f) f = 1e-37f;
-      ctl->qexp[i] = finite ? f : NAN;
+      ctl->qexp[i] = f;
     }
     uint32_t hw[4], lw[4];
 #pragma unroll

@@ -333,6 +333,22 @@ def test_non_finite_queries_stay_in_their_head(api):
     run(api, c, ref=ref)
 
 
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_non_finite_queries_that_see_nothing(api, heads):
+    # All blocks missing, or a length of 0: 0 and -inf whatever the query is; beside
+    # a row that sees the one block there is.
+    c = Case([(100, 3), (20, 2), (0, 40)], heads, 16, seed=4)
+    c.table[0, :] = -1
+    c.table[2, 1:] = -1
+    c.lens[1] = 0
+    ref = empty_requests(c, [1])
+    ref[0][20, 9], ref[1][20, 9] = np.nan, np.nan
+    for r in (0, 2, 3, 4):
+        c.q[r, :5, 7], c.q[r, 5:9, 400], c.q[r, 9:, 0] = 0x7F80, 0xFF80, 0x7FC0
+    c.q[20, 9, 3] = 0x7F80
+    run(api, c, ref=ref, code=4)
+
+
 def test_huge_and_tiny_queries(api):
     c = Case([(100, 2)], 64, 64, seed=6)
     rng = np.random.default_rng(1)
