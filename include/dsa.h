@@ -120,7 +120,8 @@ typedef struct dsa_rows {
  *   kv_a    [rows][latent_dim] bf16      norm_w [latent_dim] bf16
  *   pool    [nslots][latent_dim] FP8, written in place at the rows' slots
  * latent_dim must be 512.  A slot outside [0, nslots) (or a row inconsistent
- * with `positions`, when given) is skipped and recorded on the device.
+ * with `positions`, when given) is skipped and recorded on the device; a row of
+ * slot -1 and seq_len 0, an empty one of dsa_plan_rows, is skipped without that.
  */
 dsa_status dsa_latent_write(const dsa_rows *rows, const uint16_t *kv_a, const uint16_t *norm_w,
                             uint8_t *pool, int64_t nslots, int32_t latent_dim, float eps,
@@ -451,7 +452,10 @@ size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
  * An empty row has position 0, seq_len 0, slot -1 and a table row of -1.  Rows
  * from row_start[seqs] on are left as they were, slots of an earlier step
  * among them: calls that write by row (dsa_latent_write) are given the rows before
- * it, which whoever packs their inputs knows to be the sum of new_tokens.
+ * it, which whoever packs their inputs knows to be the sum of new_tokens.  With
+ * DSA_PLAN_EMPTY_TAIL they are made empty rows (row_seq -1) up to `rows`, so that a
+ * step captured over all rows of its buffers serves any number of new tokens:
+ * dsa_latent_write skips them and dsa_mla_chunk_fp8 leaves theirs as they were.
  * A request with n outside [0, min(L, rows)], need > max_blocks_per_seq or h
  * outside [0, max_blocks_per_seq] is recorded (DSA_DEVERR_SEQ_LEN, with s as
  * the row) and changes nothing; its n rows, if 0 <= n <= rows, are empty.
@@ -468,6 +472,7 @@ size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
  * (DSA_ERR_UNSUPPORTED).
  */
 #define DSA_PLAN_MAX_SEQS 8192
+#define DSA_PLAN_EMPTY_TAIL 1u
 typedef struct dsa_plan {
     const int32_t *seq_lens;     /* [seqs] tokens, the new ones included                */
     const int32_t *new_tokens;   /* [seqs] rows wanted                                   */
@@ -492,6 +497,8 @@ typedef struct dsa_plan {
     int32_t free_capacity;
     int32_t reserved;            /* 0                                                    */
     int32_t *served_lens;        /* [seqs] out; may be NULL                              */
+    uint32_t flags;              /* DSA_PLAN_*; unknown bits are DSA_ERR_INVALID_ARG     */
+    int32_t reserved2;           /* 0                                                    */
 } dsa_plan;
 dsa_status dsa_plan_rows(const dsa_plan *plan, void *stream);
 

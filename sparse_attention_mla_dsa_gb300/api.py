@@ -43,7 +43,7 @@ class Plan(ctypes.Structure):
         + [(n, ctypes.c_int32) for n in (
             "seqs", "rows", "max_blocks_per_seq", "bt_stride", "row_bt_stride", "block_size",
             "free_capacity", "reserved")]
-        + [("served_lens", ctypes.c_void_p)])
+        + [("served_lens", ctypes.c_void_p), ("flags", ctypes.c_uint32), ("reserved2", ctypes.c_int32)])
 
 
 class Seqs(ctypes.Structure):
@@ -374,6 +374,7 @@ def _table(t: torch.Tensor, rows: int, name: str) -> tuple[int, int, int]:
 
 
 _BITS32 = (torch.int32, torch.uint32)
+DSA_PLAN_EMPTY_TAIL = 1
 
 
 def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.Tensor,
@@ -382,7 +383,7 @@ def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.T
               row_start: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
               row_lens: torch.Tensor, row_table: torch.Tensor | None = None,
               row_seq: torch.Tensor | None = None,
-              served_lens: torch.Tensor | None = None) -> Plan:
+              served_lens: torch.Tensor | None = None, empty_tail: bool = False) -> Plan:
     """Argument block of dsa_plan_rows over a server's buffers, built once and
     used every step.  int32 except slots (int64): seq_lens, new_tokens, held_in,
     held_out [S]; block_table [S, max_blocks]; free_blocks [capacity]; free_in
@@ -390,8 +391,10 @@ def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.T
     positions (or uint32), slots, row_lens, row_seq [R]; row_table [R,
     max_blocks].  held_out may be held_in and free_out free_in (state kept in
     place).  served_lens [S], the lengths of the requests that have their blocks
-    and 0 for the others, is what make_seqs takes for the step's attention.  The
-    plan keeps the tensors alive."""
+    and 0 for the others, is what make_seqs takes for the step's attention.
+    empty_tail: the rows behind the last request's are made empty ones (row_seq -1)
+    instead of left as they were, for a step captured over all R rows.  The plan
+    keeps the tensors alive."""
     S, R = seq_lens.shape[0], positions.shape[0]
     named = dict(seq_lens=seq_lens, new_tokens=new_tokens, held_in=held_in, held_out=held_out,
                  block_table=block_table, free_blocks=free_blocks, free_in=free_in,
@@ -423,6 +426,7 @@ def make_plan(seq_lens: torch.Tensor, new_tokens: torch.Tensor, held_in: torch.T
             raise ValueError(f"row_table: expected {plan.max_blocks_per_seq} entries a row, got {width}")
     plan.seqs, plan.rows, plan.block_size = S, R, int(block_size)
     plan.free_capacity = free_blocks.shape[0]
+    plan.flags = DSA_PLAN_EMPTY_TAIL if empty_tail else 0
     plan.tensors, plan.device = named, device
     return plan
 

@@ -462,7 +462,8 @@ dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
       p.positions == nullptr || p.slots == nullptr || p.row_lens == nullptr)
     return DSA_ERR_INVALID_ARG;
   if (p.seqs < 1 || p.rows < 1 || p.max_blocks_per_seq < 1 || p.block_size < 1 ||
-      p.bt_stride < p.max_blocks_per_seq || p.free_capacity < 1 || p.reserved != 0)
+      p.bt_stride < p.max_blocks_per_seq || p.free_capacity < 1 || p.reserved != 0 ||
+      p.reserved2 != 0 || (p.flags & ~DSA_PLAN_EMPTY_TAIL) != 0)
     return DSA_ERR_INVALID_ARG;
   if (p.row_table != nullptr && p.row_bt_stride < p.max_blocks_per_seq) return DSA_ERR_INVALID_ARG;
   for (const void* q : {static_cast<const void*>(p.seq_lens), static_cast<const void*>(p.new_tokens),

@@ -53,7 +53,9 @@ __global__ void __launch_bounds__(kThreads) latent_write_kernel(LatentWriteParam
   if (tid == 0) {
     int bad = 0;
     const int64_t slot = p.rows.slots[r];
-    if (slot < 0 || slot >= p.nslots) {
+    if (slot == -1 && p.rows.seq_lens[r] == 0) {
+      bad = 1;  // an empty row: no new token
+    } else if (slot < 0 || slot >= p.nslots) {
       record_error(p.err, DSA_DEVERR_SLOT, r);
       bad = 1;
     } else if (p.rows.positions != nullptr) {

@@ -220,12 +220,12 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
         if (b0 + 32 * k < up) p.free_blocks[stack + sc.back[s] + (b0 + 32 * k - need)] = v[k];
     }
   }
-  // The rows.
-  const int out_rows = min(nrows, p.rows);
+  // The rows: the requests', and empty ones behind them where they are asked for.
+  const int out_rows = (p.flags & DSA_PLAN_EMPTY_TAIL) != 0 ? p.rows : min(nrows, p.rows);
   // (Other warps begin with the requests' tables, and others with the rows'.)
   for (int r = blockIdx.x * kThreads + ((tid + kThreads / 2) & (kThreads - 1)); r < out_rows; r += gridDim.x * kThreads) {
-    const int s = find(sc.rows, n, r);
-    const bool live = sc.need[s] >= 0 && !refused(s);
+    const int s = r < nrows ? find(sc.rows, n, r) : -1;
+    const bool live = s >= 0 && sc.need[s] >= 0 && !refused(s);
     int pos = 0;
     int64_t slot = -1;
     if (live) {
@@ -255,13 +255,16 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
     const int r0 = turn / spans * run, base = turn % spans * kSpan;
     const int r1 = min(r0 + run, out_rows);
     const uint32_t in = below(base, width);
-    int s = find(sc.rows, n, r0), need = 0, kept_blocks = 0, fresh = -1;
+    int s = find(sc.rows, n, r0), until = 0, need = 0, kept_blocks = 0, fresh = -1;
     int v[kPer];
     uint32_t put = 0;                                   // entries to be written from v
     for (int r = r0; r < r1; ++r) {
-      if (r == r0 || sc.rows[s + 1] <= r) {
-        while (sc.rows[s + 1] <= r) ++s;
-        need = refused(s) ? 0 : max(0, sc.need[s]);
+      if (r >= until) {                                 // the first row of s, or behind the requests' rows
+        if (r < nrows)
+          while ((until = sc.rows[s + 1]) <= r) ++s;
+        else
+          until = out_rows;
+        need = r >= nrows || refused(s) ? 0 : max(0, sc.need[s]);
         kept_blocks = min(max(0, sc.held[s]), need);
         const int32_t* row = p.block_table + static_cast<int64_t>(s) * p.bt_stride + base + lane;
         const uint32_t old = below(base, kept_blocks);

@@ -505,6 +505,80 @@ def test_plan_write_attend_together(api):
         paged_ref.check_chunk(out2.view(torch.bfloat16).float().cpu().numpy(), None, ref, f"gather step {k}")
 
 
+def test_plan_write_attend_captured_once(api):
+    # The three calls of a step in one graph over all rows of its buffers, replayed
+    # with the state in place: prompts, chunks, decodes, a rejected verify, an end, a
+    # request out of blocks, a step with no new tokens, one that fills the buffers.
+    rng = np.random.default_rng(22)
+    S, width, block, rows, heads, cap = 5, 12, 16, 96, 64, 15
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens_d, new_d, held, served = i32(S), i32(S), i32(S), i32(S)
+    table = torch.full((S, width), -1, dtype=torch.int32, device="cuda")
+    free = torch.from_numpy(rng.permutation(cap).astype(np.int32)).cuda()
+    count = torch.tensor([cap, 0], dtype=torch.int32, device="cuda")
+    start, pos, row_lens, row_table = i32(S + 1), i32(rows), i32(rows), i32(rows, width)
+    slots = torch.full((rows,), -1, dtype=torch.int64, device="cuda")
+    plan = api.make_plan(lens_d, new_d, held, held, table, block, free, count, count, start, pos, slots,
+                         row_lens, row_table, served_lens=served, empty_tail=True)
+    seqs = api.make_seqs(served, start, table, block)
+    r = api.make_rows(row_lens, row_table, block, slots, pos)
+    pool = torch.full((cap * block, 512), NAN8, dtype=torch.uint8, device="cuda")
+    norm_w = torch.from_numpy(bf16_bits(rng.standard_normal(512) * 0.1 + 1).view(np.int16)).cuda()
+    ws = torch.empty(api.dsa_chunk_workspace_bytes(rows, heads), dtype=torch.uint8, device="cuda")
+    kv_a = torch.zeros((rows, 512), dtype=torch.int16, device="cuda")
+    q = torch.zeros((rows, heads, 512), dtype=torch.int16, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros((rows, heads), device="cuda")
+
+    def step():
+        api.dsa_plan_rows(plan)
+        api.dsa_latent_write(r, kv_a, norm_w, pool, 1e-6, 0.02)
+        api.dsa_mla_chunk_fp8(seqs, q, pool, 0.02, 0.0625, out, lse, ws)
+
+    step()                                               # (nothing yet: no tokens, no rows)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    lens = np.zeros(S, np.int64)
+    steps = [([60, 1, 0, 17, 0], set()), ([1, 1, 33, 4, 0], set()), ([0] * 5, set()), ([1, 1, 0, 1, 90], {4}),
+             ([4, -1, 1, 1, 40], set()), ([2, 30, 1, 1, 1], set()), ([90, 0, 2, 3, 1], set())]
+    for k, (new, refused) in enumerate(steps):
+        new = np.array(new)
+        if k == 5:
+            lens[0] -= 3                                 # three of the four verified tokens rejected
+        if k == 6:
+            lens[0] = lens[1] = 0                        # ends; another takes its place at once
+        lens = np.where(new < 0, 0, lens + np.maximum(new, 0))
+        new = np.maximum(new, 0)
+        n = int(new.sum())
+        assert n <= rows and (k != 6 or n == rows)
+        lens_d.copy_(torch.from_numpy(lens))
+        new_d.copy_(torch.from_numpy(new))
+        kv_a.copy_(torch.from_numpy(bf16_bits(rng.standard_normal((rows, 512))).view(np.int16)))
+        q.copy_(torch.from_numpy(bf16_bits(rng.standard_normal((rows, heads, 512)) * 0.1).view(np.int16)))
+        out.fill_(MARK)
+        lse.fill_(77.0)
+        before = pool.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        code = api.DEVERR[api.dsa_get_error(reset=True)[0]]
+        assert code == ("free" if refused else "none"), f"step {k}: {code}"
+        live = np.where(np.isin(np.arange(S), list(refused)), 0, lens)
+        assert served.tolist() == live.tolist()
+        wrote = torch.unique((pool != before).any(1).nonzero()[:, 0])
+        mine = torch.unique(slots[:n][slots[:n] >= 0])
+        assert torch.isin(wrote, mine).all(), f"step {k}: a latent of no new token was written"
+        assert (slots[n:] == -1).all() and len(mine) == int(new[live > 0].sum())
+        case = Case([(0, 1)], heads, block)              # (only for the reference of empty requests)
+        case.lens, case.start, case.table, case.width = live.copy(), start.cpu().numpy(), table.cpu().numpy(), width
+        case.q, case.pool = q.cpu().numpy().view(np.uint16), pool.cpu().numpy()
+        ref = empty_requests(case, sorted(refused))
+        paged_ref.check_chunk(out.view(torch.bfloat16).float().cpu().numpy(), lse.cpu().numpy(), ref, f"step {k}")
+        assert ref[5].sum() == n and (out[n:] == MARK).all() and (lse[n:] == 77.0).all()
+        for s in refused:                                # its caller takes the step back
+            lens[s] -= new[s]
+
+
 def test_a_request_out_of_blocks_reads_nothing(api):
     # Request 1 has a last block with room, which holds what an earlier owner left
     # there; it wants more blocks than there are.  Request 0 is served beside it.

@@ -305,6 +305,27 @@ def test_served_lengths_of_served_requests(api, seqs):
     assert served(api, st) == st.lens.tolist()
 
 
+@pytest.mark.parametrize("seqs, width, block, rows, row_table, row_seq, new", [
+    (1, 1, 64, 1, True, True, 0), (1, 513, 64, 9, True, True, 1), (3, 40, 5, 64, True, True, 7),
+    (3, 40, 5, 64, False, True, 7), (3, 40, 5, 64, True, False, 21), (33, 17, 16, 300, True, True, 9),
+    (700, 257, 16, 20000, True, True, 20), (700, 1031, 16, 1403, True, True, 2), (4, 8, 8, 10, True, True, 5)])
+def test_rows_behind_the_last_made_empty(api, seqs, width, block, rows, row_table, row_seq, new):
+    # (the last case has more rows than the buffers hold)
+    rng = np.random.default_rng(rows)
+    st = State(seqs, width, block, seqs * width, rows, 16, stride=width + 2, row_table=row_table, row_seq=row_seq)
+    n = rng.integers(new // 2, new + 1, seqs)
+    st.lengths(np.minimum(n + rng.integers(0, width * block, seqs), width * block), n)
+    ref = st.expect()
+    tail = rows - len(ref["positions"])
+    api.dsa_plan_rows(api.make_plan(
+        st.d_lens, st.d_new, st.d_held, st.d_held_out, st.d_table, st.block, st.d_free, st.d_in, st.d_out,
+        st.row_start, st.positions, st.slots, st.row_lens, st.row_table, st.row_seq, empty_tail=True))
+    for name, empty in (("positions", 0), ("slots", -1), ("row_lens", 0), ("row_seq", -1)):
+        ref[name] = ref[name] + [empty] * tail
+    ref["row_table"] = ref["row_table"] + [[-1] * width] * tail
+    st.check(api, ref)
+
+
 def test_bad_free_counts(api):
     for count in (-1, 41):
         st = State(2, 4, 8, 40, 16, 9)

@@ -52,6 +52,11 @@ def test_plan_refuses_served_lengths_off_their_alignment(lib):
     assert lib.dsa_plan_rows(_plan(served_lens=X + 2), None) == 1
 
 
+@pytest.mark.parametrize("changes", [{"flags": 2}, {"flags": 1 << 31}, {"reserved2": 1}])
+def test_plan_refuses_unknown_flags(lib, changes):
+    assert lib.dsa_plan_rows(_plan(**changes), None) == 1
+
+
 def test_plan_without_a_plan(lib):
     assert lib.dsa_plan_rows(None, None) == 1
 
