@@ -45,7 +45,22 @@ const DeviceInfo* device_info() {
   return &d;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
+// cuTensorMapEncodeTiled.  It wants a current context, which a host thread whose first
+// call this is does not have yet: the runtime binds the device's then.
+struct TensorMapEncoder {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  explicit operator bool() const { return fn != nullptr; }
+  template <typename... Args>
+  CUresult operator()(Args... args) const {
+    const CUresult cr = fn(args...);
+    if (cr == CUDA_SUCCESS) return cr;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return cr;
+    return fn(args...);
+  }
+};
+
+TensorMapEncoder encode_tiled() {
   std::lock_guard<std::mutex> lock(g_mutex);
   if (g_encode_tiled == nullptr) {
     void* fn = nullptr;
@@ -55,7 +70,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
         q == cudaDriverEntryPointSuccess)
       g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  return g_encode_tiled;
+  return {g_encode_tiled};
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -144,8 +159,8 @@ dsa_status dsa_index_scores_ex(const dsa_rows* rows, const float* q_idx, const f
   if (max_len == 0) return DSA_OK;
   const DeviceInfo* dev = device_info();
   if (dev == nullptr) return DSA_ERR_CUDA;
-  auto encode = encode_tiled();
-  if (encode == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
 
   IndexParams p{};
   p.seq_lens = rows->seq_lens;
@@ -278,8 +293,8 @@ dsa_status dsa_mla_decode_fp8_ex(const dsa_rows* rows, const uint16_t* q, const 
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
     return DSA_ERR_WORKSPACE;
   mla_decode_tc_bind_workspace(p, workspace);
-  auto encode = encode_tiled();
-  if (encode == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
   // Latent pool [nslots][512] bytes; the gather reads 128-byte x 1-row boxes
   // (tile::gather4: four rows per copy) with the 128-byte swizzle; rows
   // outside the pool read as zero.
@@ -410,8 +425,8 @@ dsa_status dsa_dense_mm_bf16(const uint16_t* a, const uint16_t* b, void* c, int3
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 4)) return DSA_ERR_INVALID_ARG;
   const DeviceInfo* dev = device_info();
   if (dev == nullptr) return DSA_ERR_CUDA;
-  auto encode = encode_tiled();
-  if (encode == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
 
   DenseMmParams p{};
   p.a = a;
@@ -517,8 +532,8 @@ dsa_status dsa_mla_chunk_fp8(const dsa_seqs* seqs, const uint16_t* q, const uint
   if (workspace == nullptr || workspace_bytes < dsa_chunk_workspace_bytes(rows, heads) ||
       !aligned(workspace, 256))
     return DSA_ERR_WORKSPACE;
-  auto encode = encode_tiled();
-  if (encode == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
   ChunkParams p{};
   p.seqs = *seqs;
   p.q = q;
