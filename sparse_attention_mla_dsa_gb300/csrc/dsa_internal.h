@@ -20,6 +20,11 @@ inline cudaLaunchAttribute dependent_launch_attr() {
   return a;
 }
 
+// Shared memory that kernels whose need depends on the call ask for, always: the
+// setting is the process's, and a host thread that set its own call's need could
+// take away what another has set and not launched yet.
+constexpr int kMaxSmemBytes = 227 * 1024;
+
 // Device address of the sticky error word on the current device (nullptr on
 // failure); kernels receive it as an argument.
 int* device_error_word();

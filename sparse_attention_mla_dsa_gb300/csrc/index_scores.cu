@@ -857,7 +857,7 @@ cudaError_t launch_index_scores(const IndexParams& p, const CUtensorMap& kmap,
   cudaError_t e;
   auto kernel = p.direct ? (p.dim == 64 ? index_scores_kernel<64, true> : index_scores_kernel<128, true>)
                         : (p.dim == 64 ? index_scores_kernel<64, false> : index_scores_kernel<128, false>);
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem_bytes);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int64_t tiles_max = (static_cast<int64_t>(p.max_len) + kTileM - 1) / kTileM;

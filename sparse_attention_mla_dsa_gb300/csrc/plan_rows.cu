@@ -76,7 +76,7 @@ struct Scan {
 };
 
 constexpr size_t scan_bytes(int seqs) { return 5 * (static_cast<size_t>(seqs) + 1) * sizeof(int); }
-static_assert(scan_bytes(DSA_PLAN_MAX_SEQS) + sizeof(Shared) <= 227 * 1024, "shared memory budget");
+static_assert(scan_bytes(DSA_PLAN_MAX_SEQS) + sizeof(Shared) <= kMaxSmemBytes, "shared memory budget");
 
 // Index of the last entry of the exclusive prefix `a` [n + 1] that is <= x,
 // among the requests (0 <= x < a[n]): the request that x falls into.
@@ -315,9 +315,8 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
 
 cudaError_t launch_plan_rows(const PlanRowsParams& p, int num_sms, cudaStream_t stream) {
   const size_t smem = scan_bytes(p.p.seqs);
-  // Above 48 KB a block in all, its static part included, a kernel has to ask.  Every
-  // call asks for the most there can be: the setting is the process's, so that host
-  // threads which plan batches of different sizes must not lower it for each other.
+  // Above 48 KB a block in all, its static part included, a kernel has to ask; for the
+  // most there can be (see kMaxSmemBytes).
   static_assert(sizeof(Shared) <= 1008, "47 KB leave room for it");
   if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(

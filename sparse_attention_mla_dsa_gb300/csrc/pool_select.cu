@@ -111,8 +111,7 @@ size_t select_pools_smem_bytes(int32_t max_pools) {
 cudaError_t launch_select_pools(const PoolSelectParams& p, cudaStream_t stream) {
   const size_t smem = select_pools_smem_bytes(p.max_pools);
   cudaError_t e = cudaFuncSetAttribute(select_pools_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
   cudaLaunchConfig_t cfg = {};

@@ -433,8 +433,7 @@ size_t topk_smem_bytes(int32_t max_len, int cluster) {
 cudaError_t launch_select_topk(const TopkParams& p, cudaStream_t stream) {
   const size_t smem = topk_smem_bytes(p.max_len, p.cluster);
   cudaError_t e = cudaFuncSetAttribute(select_topk_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.cluster, p.rows, 1);

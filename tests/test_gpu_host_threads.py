@@ -1,4 +1,6 @@
-"""Entry points called from a host thread whose first CUDA call it is."""
+"""Entry points called from host threads: one whose first CUDA call it is, and two at
+once on streams of their own with calls of different sizes, where the shared memory
+that one call asks for must not be taken away by the other before its launch."""
 import threading
 
 import pytest
@@ -15,6 +17,27 @@ def api():
     api.load()
     api.dsa_get_error(reset=True)
     return api
+
+
+def topk(api, n):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    lens = torch.full((2,), n, dtype=torch.int32, device="cuda")
+    rows = api.make_rows(lens)
+    scores = torch.randn((2, n), generator=g, device="cuda")
+    sel = torch.full((2, 512), -7, dtype=torch.int32, device="cuda")
+    return lambda stream=None: api.dsa_select_topk(rows, scores, n, 512, sel, stream=stream), sel, (lens, scores)
+
+
+def pools(api, n):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    pos = torch.full((2,), 4 * n, dtype=torch.int32, device="cuda")
+    lens = pos + 1
+    rows = api.make_rows(lens, positions=pos)
+    scores = torch.randn((2, n), generator=g, device="cuda")
+    valid = torch.ones((2, n), dtype=torch.uint8, device="cuda")
+    sel = torch.full((2, 32), -7, dtype=torch.int32, device="cuda")
+    return (lambda stream=None: api.dsa_select_pools(rows, scores, valid, 4, 32, sel, stream=stream), sel,
+            (pos, lens, scores, valid))
 
 
 def scores(api, heads):
@@ -91,3 +114,34 @@ def test_first_call_of_a_host_thread(api, make, n):
     torch.cuda.synchronize()
     assert not failures, failures
     assert torch.equal(out, want) and api.dsa_get_error(reset=True)[0] == 0
+
+
+@pytest.mark.parametrize("make, small, large", [(topk, 30000, 300000), (pools, 100, 16384), (scores, 8, 64)],
+                         ids=["topk", "pools", "scores"])
+def test_calls_of_two_sizes_from_two_threads(api, make, small, large):
+    cases = [make(api, small), make(api, large)]
+    want = []
+    for call, out, _ in cases:
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams, failures = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+
+    def work(call, stream):
+        try:
+            for _ in range(2000):
+                call(stream)
+        except Exception as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(c[0], s)) for c, s in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, failures
+    assert api.dsa_get_error(reset=True)[0] == 0
+    for (_, out, _), ref in zip(cases, want):
+        assert torch.equal(out, ref)
