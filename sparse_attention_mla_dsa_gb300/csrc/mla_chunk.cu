@@ -113,7 +113,7 @@ struct __align__(16) Ctl {
   SegRecord seg[kSegs];
   uint32_t segs;                     // segments left in seg[], over all
   int more;                          // whether there is a next one: the softmax warps' common view
-  uint16_t fills[kBlocks], peer_fills[kBlocks];  // copies begun of each block; the other CTA's
+  uint16_t fills[kBlocks], peer_fills[kBlocks];  // copies begun of each block, see copy(); the other CTA's
   uint32_t tmem_base;
   int abort_flag;
   int begun;                         // the copies of the first tile's K are on their way
@@ -692,9 +692,11 @@ __device__ __forceinline__ void copy(const CUtensorMap& map, const CUtensorMap& 
     ++segs;
   };
   // The copies begun of each block, for the kernel's end: those of tile n's first i
-  // blocks too.
+  // blocks too.  (As many as 3, or 4 .. 7 with the count's last two bits: a range may
+  // have more tiles than 16 bits hold.)
   auto leave = [&](uint32_t n, int i) {
-    if (lane < 4) ctl->fills[(kV ? 4 : 0) + lane] = static_cast<uint16_t>(n + (lane < i ? 1 : 0));
+    const uint32_t begun = n + (lane < i ? 1 : 0);
+    if (lane < 4) ctl->fills[(kV ? 4 : 0) + lane] = static_cast<uint16_t>(begun < 4 ? begun : 4 | (begun & 3));
   };
   Segment g;
   while (next_segment(p, w, g)) {
@@ -1306,11 +1308,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0 && tid < kBlocks) {
       uint64_t* const full = tid < 4 ? &ctl->kfull[tid] : &ctl->vfull[tid - 4];
       const uint16_t mine = ctl->fills[tid], other = ctl->peer_fills[tid];
-      const int ahead = static_cast<int16_t>(mine - other);   // -1, 0 or 1
-      const uint32_t n = ahead >= 0 ? mine : other;
-      if (ahead > 0)
+      const int ahead = (mine - other) & 3;                   // 1, 0 or 3: one behind
+      const uint32_t n = ahead == 3 ? other : mine;
+      if (ahead == 1)
         asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(full)), "r"(kBlockBytes) : "memory");
-      else if (ahead < 0)
+      else if (ahead == 3)
         mbar_arrive_expect_tx(full, kBlockBytes);
       if (n > 0) mbar_wait(full, (n - 1) & 1, kDrainWaitNs);
     }
