@@ -277,6 +277,12 @@ def test_one_token_over_a_long_flat_tail(api):
     run(api, c)
 
 
+@pytest.mark.parametrize("heads, q_scale", [(64, 0.05), (16, 1.0), (128, 0.3)])
+def test_one_decode_of_more_than_64_parts(api, heads, q_scale):
+    # 391 tiles are six a pair of SMs: 66 parts, which the merge takes in two rounds.
+    run(api, Case([(99_999, 1)], heads, 64, seed=heads, q_scale=q_scale))
+
+
 def test_long_tails_of_like_weights(api):
     # The same context 160 times, so that a range has it whole: one hot token,
     # every other's weight 2^-13 to 2^-24 of it, another in each head.  What the tail
