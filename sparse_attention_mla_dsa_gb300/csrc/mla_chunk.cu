@@ -44,15 +44,16 @@
 // Products, sums, maxima and the output are FP32.
 //
 // What bounds it.  A tile's 64 MMAs take 4,100 clocks and its copies as many, each
-// waiting for blocks that the other holds: the tensor pipe is busy 89 % of the time
-// (1,024 rows of 64 heads at 9,000 tokens, one launch of 600 us) and the card at its
-// power limit in calls after each other: 685 us then, 1.66 PFLOP/s counting only
-// visible tokens.  64 tokens of 128 heads at up to 128k: 370 us.  32 tokens of 64
-// heads (half of every MMA is empty) at up to 64k: 137 us, 3.1 TB/s of latents.  An
+// waiting for blocks that the other holds: the tensor pipe is busy 87 % of the time
+// (1,024 rows of 64 heads at 9,000 tokens, one launch of 592 us) and the card at its
+// power limit in calls after each other: 687 us then, 1.66 PFLOP/s counting only
+// visible tokens.  64 tokens of 128 heads at up to 128k: 364 us.  32 tokens of 64
+// heads (half of every MMA is empty) at up to 64k: 138 us, 3.1 TB/s of latents.  An
 // item costs ~10,000 clocks besides: Q through the same 32 bytes a clock (3,800),
 // its conversion (2,400), the output's store (3,800), the warps' meetings; 2,049
-// rows of 128 heads, an item each: 470 us.  One token of 16 heads: 15 us a call,
-// most of it first times.
+// rows of 128 heads, an item each: 466 us.  One token of 16 heads: 12.5 us a call in
+// calls after each other, most of it first times.  Where the maxima move (logits of a
+// standard deviation of 1.1 instead of 0.07) long calls take 11 to 21 % more.
 #include "dsa_device.cuh"
 #include "dsa_internal.h"
 
@@ -1453,7 +1454,7 @@ __device__ __forceinline__ void merge_many(const ChunkParams& p, const ChunkReco
 
 // CTAs take units of 64 lines in turn: 64 dims of an item with few parts, 4 of
 // one with many (few items then, which have to reach every SM).  All as few: one
-// decode at 32k, 65 parts, 22.5 -> 41 us a call; all as many: a prompt of 1,024
+// decode at 32k, 64 parts, 22.5 -> 41 us a call; all as many: a prompt of 1,024
 // rows, whose items have two parts or three, 686 -> 724, a ragged batch 200 -> 255.
 __global__ void __launch_bounds__(kMergeThreads) mla_chunk_merge_kernel(const ChunkParams p) {
   constexpr int kFew = 8;

@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
       const int len = p.seq_lens[s], fresh = p.new_tokens[s];
       held = p.held_in[s];
       const bool rows_ok = fresh >= 0 && fresh <= p.rows;
-      // (32 bits hold the sum of a length and a block size)
+      // (32 bits hold the sum of a length of 0 or more and a block size; a length below
+      // has no rows and is refused with them)
       const uint32_t blocks = (static_cast<uint32_t>(len) + (p.block_size - 1)) / static_cast<uint32_t>(p.block_size);
       if (rows_ok && fresh <= len && blocks <= static_cast<uint32_t>(p.max_blocks_per_seq) && held >= 0 &&
           held <= p.max_blocks_per_seq) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) plan_rows_kernel(const PlanRowsParam
   }
   // A warp's turn is kSpan entries of `run` consecutive rows, whose request's
   // entries are looked up and loaded once; single rows while there are warps to
-  // spare (12,000 rows of 1,031 entries: 17.6 us by single rows, 12.8 by fours,
+  // spare (12,000 rows of 1,031 entries: 17.6 us by single rows, 12.9 by fours,
   // where a fill of the tables takes 7.4; 28 rows of 1,025: 4.7 by single rows, 6.2
   // by fours).
   const int width = p.max_blocks_per_seq, spans = (width + kSpan - 1) / kSpan;
