@@ -1,0 +1,398 @@
+"""The 8-bit operators of the layer as they are measured: the block quantiser
+(``dsa_quantize_fp8``), the block-scaled matrix product (``dsa_dense_mm_fp8``), the
+indexer key's write into an FP8 cache (``dsa_indexer_write_fp8``) and the index
+scores over that cache (``dsa_index_scores_fp8``).
+
+``own`` picks the side: False computes the plain forms in torch, True makes the
+framework's calls.  A case's request lengths follow from the case alone (``mix``
+seeds them); the contents follow from ``prepare``'s seed.  FP8 codes are handed out
+as float8_e4m3fn, which views the same bytes.
+"""
+from __future__ import annotations
+
+import math
+import random
+
+import torch
+
+own = False
+
+BLOCK = 128
+E4M3_MAX = 448.0
+EPS = 1e-6
+
+
+# ---------------------------------------------------------------------------- cases
+def listed():
+    return [
+        # One token's layer input before its projections: the smallest call, pure latency.
+        dict(name="quantise, one token", op="quantise", rows=1, k=4096, tile=1, fp32=False),
+        # The attention output of a prompt chunk of 1,024 rows (64 heads x 512) before its projection.
+        dict(name="quantise, prompt chunk", op="quantise", rows=1024, k=32768, tile=1, fp32=False),
+        # A weight of odd shape quantised in 128 x 128 blocks from its FP32 master, as at load time.
+        dict(name="quantise, odd weight", op="quantise", rows=5003, k=4112, tile=128, fp32=True),
+        # One decode token through the stacked query and latent projection.
+        dict(name="product, one token", op="product", m=1, n=2048, k=4096, fp32=False),
+        # A decode batch of 32 requests through the output projection of 64 heads: the largest weight.
+        dict(name="product, decode batch", op="product", m=32, n=4096, k=32768, fp32=False),
+        # A prompt chunk of 1,024 rows through the output projection.
+        dict(name="product, prompt chunk", op="product", m=1024, n=4096, k=32768, fp32=False),
+        # An odd number of rows through weights of odd shape, FP32 out.
+        dict(name="product, odd sizes", op="product", m=777, n=1003, k=4112, fp32=True),
+        # The keys of a verify's four rows.
+        dict(name="key write, verify", op="write", seqs=1, per_seq=4, dim=128, ctx=32768, mix=1),
+        # The keys of a prompt chunk of 4,001 rows.
+        dict(name="key write, prompt chunk", op="write", seqs=4001, per_seq=1, dim=128, ctx=32768, mix=2),
+        # One request decoding at 32k context.
+        dict(name="scores, one decode", op="scores", seqs=1, per_seq=1, heads=32, dim=128, ctx_lo=32768,
+             ctx_hi=32768, mix=3),
+        # Long-context decode of 64 requests at 4k to 128k, 64 index heads: the most cache read by one call.
+        dict(name="scores, long decode", op="scores", seqs=64, per_seq=1, heads=64, dim=128, ctx_lo=4096,
+             ctx_hi=131072, mix=4),
+        # The last 1,024 tokens of a 9,000-token prompt, each row with its own horizon.
+        dict(name="scores, prompt chunk", op="scores", seqs=1, per_seq=1024, heads=32, dim=128, ctx_lo=9000,
+             ctx_hi=9000, mix=5),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    while True:
+        op = rng.choice(["quantise", "product", "product", "write", "scores", "scores"])
+        if op == "quantise":
+            case = dict(op=op, rows=_log(rng, 1, 8192), k=16 * _log(rng, 1, 2048), tile=rng.choice([1, 1, 128]),
+                        fp32=rng.random() < 0.3)
+            if case["rows"] * case["k"] > 1024 * 32768:
+                continue
+        elif op == "product":
+            case = dict(op=op, m=_log(rng, 1, 4096), n=_log(rng, 16, 32768), k=16 * _log(rng, 4, 2048),
+                        fp32=rng.random() < 0.3)
+            if case["m"] * case["n"] * case["k"] > 1024 * 4096 * 32768 or case["n"] * case["k"] > 4096 * 32768:
+                continue
+        elif op == "write":
+            case = dict(op=op, seqs=_log(rng, 1, 4096), per_seq=rng.choice([1, 1, 2, 4, 7]),
+                        dim=rng.choice([64, 128, 128]), ctx=_log(rng, 64, 32768), mix=rng.randrange(1 << 30))
+            if case["seqs"] * case["per_seq"] > 4096:
+                continue
+        else:
+            top = _log(rng, 16, 131072)
+            case = dict(op=op, seqs=_log(rng, 1, 64), per_seq=rng.choice([1, 1, 2, 4, 5, _log(rng, 1, 1024)]),
+                        heads=rng.choice([8, 16, 24, 32, 32, 64, 64]), dim=rng.choice([64, 128, 128]),
+                        ctx_lo=max(1, top // rng.choice([1, 4, 16])), ctx_hi=top, mix=rng.randrange(1 << 30))
+            # no more than the largest listed case, padded (the plain form) or not
+            need = work(case)
+            if (need["bytes"] > 300_000_000 or need["flops"] > 7.0e10
+                    or case["seqs"] * max(top, case["per_seq"]) * case["per_seq"] * case["heads"] > 530_000_000):
+                continue
+        return case
+
+
+def _contexts(case):
+    """Tokens that each request of a scores case has, its new rows included: row
+    i of the ``per_seq`` new ones sees all but the last per_seq - 1 - i."""
+    rng = random.Random(case["mix"])
+    return [max(case["per_seq"], _log(rng, case["ctx_lo"], case["ctx_hi"])) for _ in range(case["seqs"])]
+
+
+# ---------------------------------------------------------------------------- inputs
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return {"quantise": _prepare_quantise, "product": _prepare_product, "write": _prepare_write,
+            "scores": _prepare_scores}[case["op"]](case, g)
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def _zeros(shape, dtype):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def _codes(x, scale):
+    return (x / scale).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+
+
+def _prepare_quantise(case, g):
+    rows, k = case["rows"], case["k"]
+    # activations: each row of its own size, a few large channels
+    x = _randn(g, rows, k) * _randn(g, rows, 1).exp() * (1 + 20 * (torch.rand(k, generator=g, device="cuda") < 0.01))
+    x = x.float() if case["fp32"] else x.to(torch.bfloat16)
+    return dict(op="quantise", x=x, tile=case["tile"], codes=_zeros((rows, k), torch.uint8),
+                scales=_zeros((-(-rows // case["tile"]), _blocks(k)), torch.float32))
+
+
+def _prepare_product(case, g):
+    m, n, k = case["m"], case["n"], case["k"]
+    kb = _blocks(k)
+    # activations as the quantiser leaves them (scales are powers of two) ...
+    a = _randn(g, m, kb * BLOCK)
+    a[:, k:] = 0
+    sa = _pow2_scale(a.view(m, kb, BLOCK).abs().amax(-1))
+    a = _codes(a.view(m, kb, BLOCK), sa[..., None]).view(torch.uint8).view(m, -1)[:, :k].contiguous()
+    # ... a weight as checkpoints hold it: FP32 scales amax / 448 of 128 x 128 blocks
+    nb = _blocks(n)
+    b = torch.zeros((nb * BLOCK, kb * BLOCK), device="cuda")
+    b[:n, :k] = _randn(g, n, k) / math.sqrt(k)
+    t = b.view(nb, BLOCK, kb, BLOCK)
+    sb = t.abs().amax((1, 3)) / E4M3_MAX
+    b = _codes(t, sb[:, None, :, None]).view(torch.uint8).view(nb * BLOCK, -1)[:n, :k].contiguous()
+    out = torch.float32 if case["fp32"] else torch.bfloat16
+    return dict(op="product", a=a, sa=sa.contiguous(), b=b, sb=sb.contiguous(), c=_zeros((m, n), out))
+
+
+def _prepare_write(case, g):
+    rng = random.Random(case["mix"])
+    seqs, per, dim, room = case["seqs"], case["per_seq"], case["dim"], case["ctx"] + case["per_seq"]
+    lens = [rng.randrange(per, room + 1) for _ in range(seqs)]           # the new rows included
+    # one sequence's keys behind the other's, in an arena of moderate size
+    room = min(room, max(per, 500_000 // seqs))
+    lens = [min(n, room) for n in lens]
+    pos = torch.tensor([n - per + i for n in lens for i in range(per)], device="cuda")
+    base = (torch.arange(seqs, device="cuda") * room).repeat_interleave(per)
+    rows, total = seqs * per, seqs * room
+    old = torch.randint(0, 127, (total, dim), generator=g, device="cuda").to(torch.uint8)
+    st = dict(op="write", per=per, k_raw=(_randn(g, rows, dim) + 0.3).to(torch.bfloat16),
+              ln_w=(1 + 0.1 * _randn(g, dim)).to(torch.bfloat16), ln_b=(0.1 * _randn(g, dim)).to(torch.bfloat16),
+              gate=torch.sigmoid(_randn(g, rows)).to(torch.bfloat16), positions=pos.int(), seq_lens=(pos + 1).int(),
+              base=base, idx_k=old, idx_scale=torch.ones(total, device="cuda"),
+              idx_gate=torch.ones(total, dtype=torch.bfloat16, device="cuda"),
+              written=torch.tensor([n - per for n in lens], dtype=torch.int32, device="cuda"))
+    if own:  # the argument block that a server keeps over its buffers
+        from sparse_attention_mla_dsa_gb300 import api
+        st["rows"] = api.make_rows(st["seq_lens"], positions=st["positions"])
+    return st
+
+
+def _prepare_scores(case, g):
+    seqs, per, heads, dim = case["seqs"], case["per_seq"], case["heads"], case["dim"]
+    ctx = _contexts(case)
+    rows, total, top = seqs * per, sum(ctx), max(ctx)
+    starts = [sum(ctx[:s]) for s in range(seqs)]
+    k8, ks = torch.empty((total, dim), dtype=torch.uint8, device="cuda"), torch.empty(total, device="cuda")
+    for lo in range(0, total, 1 << 20):                                  # keys as the key write stores them
+        x = _randn(g, min(1 << 20, total - lo), dim)
+        e = _pow2_scale(x.abs().amax(-1))
+        k8[lo:lo + x.shape[0]] = _codes(x, e[:, None]).view(torch.uint8)
+        ks[lo:lo + x.shape[0]] = e
+    q = _randn(g, rows, heads, dim)
+    qs = _pow2_scale(q.abs().amax(-1))
+    st = dict(op="scores", per=per, top=top, q=_codes(q, qs[..., None]).view(torch.uint8), q_scale=qs,
+              head_w=_randn(g, rows, heads) * heads ** -0.5, idx_k=k8, idx_scale=ks,
+              idx_gate=torch.sigmoid(_randn(g, total)).to(torch.bfloat16),
+              base=torch.tensor(starts, device="cuda").repeat_interleave(per),
+              seq_lens=torch.tensor([n - per + 1 + i for n in ctx for i in range(per)], dtype=torch.int32,
+                                    device="cuda"),
+              scores=_zeros((rows, top), torch.float32))
+    if own:  # the argument block that a server keeps over its buffers
+        from sparse_attention_mla_dsa_gb300 import api
+        st["rows"] = api.make_rows(st["seq_lens"])
+    return st
+
+
+# ---------------------------------------------------------------------------- one pass
+def run(st):
+    if own:
+        return {"quantise": _own_quantise, "product": _own_product, "write": _own_write,
+                "scores": _own_scores}[st["op"]](st)
+    return {"quantise": _plain_quantise, "product": _plain_product, "write": _plain_write,
+            "scores": _plain_scores}[st["op"]](st)
+
+
+def _own_quantise(st):
+    from sparse_attention_mla_dsa_gb300 import api
+    api.dsa_quantize_fp8(st["x"], st["codes"], st["scales"], block_rows=st["tile"])
+    return {"codes": st["codes"].view(torch.float8_e4m3fn), "scales": st["scales"]}
+
+
+def _own_product(st):
+    from sparse_attention_mla_dsa_gb300 import api
+    api.dsa_dense_mm_fp8(st["a"], st["sa"], st["b"], st["sb"], st["c"])
+    return st["c"]
+
+
+def _own_write(st):
+    from sparse_attention_mla_dsa_gb300 import api
+    api.dsa_indexer_write_fp8(st["rows"], st["k_raw"], st["ln_w"], st["ln_b"], EPS, st["base"], st["idx_k"],
+                              st["idx_scale"], st["idx_gate"], st["gate"], st["written"], st["per"])
+    return {"idx_k": st["idx_k"].view(torch.float8_e4m3fn), "idx_scale": st["idx_scale"],
+            "idx_gate": st["idx_gate"], "written": st["written"]}
+
+
+def _own_scores(st):
+    from sparse_attention_mla_dsa_gb300 import api
+    api.dsa_index_scores_fp8(st["rows"], st["q"], st["q_scale"], st["head_w"], st["idx_k"], st["idx_scale"],
+                             st["idx_gate"], st["base"], st["per"], st["top"], st["scores"])
+    return st["scores"]
+
+
+def _pow2_scale(top):
+    """Smallest power of two, 2^-126 at least, with top <= 448 times it."""
+    m, e = torch.frexp(top)                           # top = m 2^e, 0.5 <= m < 1; 448 = 0.875 2^9
+    e = torch.where(m > 0.875, e - 8, e - 9)
+    e = torch.where(top > 0, e, -126).clamp(min=-126)
+    return ((e + 127) << 23).int().view(torch.float32)
+
+
+def _plain_quantise(st):
+    x, tile = st["x"], st["tile"]
+    rows, k = x.shape
+    rb, kb = -(-rows // tile), _blocks(k)
+    padded = torch.zeros((rb * tile, kb * BLOCK), device="cuda")
+    padded[:rows, :k] = x
+    t = padded.view(rb, tile, kb, BLOCK)
+    scale = _pow2_scale(t.abs().amax((1, 3)))
+    codes = _codes(t, scale[:, None, :, None]).view(torch.uint8).view(rb * tile, -1)[:rows, :k]
+    return {"codes": codes.contiguous().view(torch.float8_e4m3fn), "scales": scale}
+
+
+def _spread(scale, k):
+    return scale.repeat_interleave(BLOCK, -1)[..., :k]
+
+
+def _plain_product(st):
+    a, b, k = st["a"], st["b"], st["a"].shape[1]
+    x = a.view(torch.float8_e4m3fn).float() * _spread(st["sa"], k)
+    w = b.view(torch.float8_e4m3fn).float() * _spread(st["sb"], k).repeat_interleave(BLOCK, 0)[:b.shape[0]]
+    return (x @ w.t()).to(st["c"].dtype)
+
+
+def _plain_write(st):
+    """The norm in 64 bits: its results are rounded next to borders."""
+    x = st["k_raw"].double()
+    mu = x.mean(-1, keepdim=True)
+    y = (x - mu) / ((x - mu).square().mean(-1, keepdim=True) + EPS).sqrt() * st["ln_w"].double() + st["ln_b"].double()
+    scale = _pow2_scale(y.abs().amax(-1))
+    q = y / scale[:, None]
+    # one rounding to three bits of mantissa (nearest, ties to even), in steps of 2^-9 at least
+    step = (q.abs().clamp(min=2.0 ** -6).view(torch.int64) & (0x7FF << 52)).view(torch.float64) / 8
+    codes = (torch.round(q / step) * step).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    # a sequence's rows are written where its keys reach up to them
+    per = st["per"]
+    first = st["positions"][::per]
+    live = st["written"] >= first
+    rows = live.repeat_interleave(per)[:, None]
+    at = st["base"] + st["positions"]
+    st["idx_k"][at] = torch.where(rows, codes, st["idx_k"][at])
+    st["idx_scale"][at] = torch.where(rows[:, 0], scale, st["idx_scale"][at])
+    st["idx_gate"][at] = torch.where(rows[:, 0], st["gate"], st["idx_gate"][at])
+    st["written"].copy_(torch.where(live, first + per, st["written"]))
+    return {"idx_k": st["idx_k"].view(torch.float8_e4m3fn), "idx_scale": st["idx_scale"],
+            "idx_gate": st["idx_gate"], "written": st["written"]}
+
+
+def _plain_scores(st):
+    """gate * key scale * sum over heads of (w * query scale) relu(q . k), on
+    sequences padded to the longest."""
+    rows, heads, dim = st["q"].shape
+    per, top = st["per"], st["top"]
+    q = st["q"].view(torch.float8_e4m3fn).float().view(rows // per, per * heads, dim)
+    t = torch.arange(top, device="cuda")
+    at = (st["base"][::per, None] + t).clamp(max=st["idx_k"].shape[0] - 1)
+    k = st["idx_k"][at].view(torch.float8_e4m3fn).float()
+    dots = (q @ k.transpose(1, 2)).clamp_(min=0).view(rows, heads, top)
+    score = (dots * (st["head_w"] * st["q_scale"])[..., None]).sum(1)
+    score = score * (st["idx_scale"][at] * st["idx_gate"][at].float()).repeat_interleave(per, 0)
+    return torch.where(t < st["seq_lens"][:, None], score, 0)
+
+
+# ---------------------------------------------------------------------------- measures
+def work(case):
+    op = case["op"]
+    if op == "quantise":
+        rows, k = case["rows"], case["k"]
+        return {"bytes": rows * k * (5 if case["fp32"] else 3) + 4 * -(-rows // case["tile"]) * _blocks(k),
+                "flops": 3 * rows * k}
+    if op == "product":
+        m, n, k = case["m"], case["n"], case["k"]
+        return {"bytes": (m + n) * k + 4 * _blocks(k) * (m + _blocks(n)) + m * n * (4 if case["fp32"] else 2),
+                "flops": 2 * m * n * k}
+    if op == "write":
+        rows, dim = case["seqs"] * case["per_seq"], case["dim"]
+        return {"bytes": rows * (2 * dim + dim + 4 + 2 * 2 + 4 + 4 + 8) + 8 * case["seqs"] + 4 * dim,
+                "flops": 9 * rows * dim}
+    ctx, per = _contexts(case), case["per_seq"]
+    rows, seen = per * case["seqs"], sum(per * n - per * (per - 1) // 2 for n in ctx)
+    return {"bytes": sum(ctx) * (case["dim"] + 4 + 2) + rows * case["heads"] * (case["dim"] + 8) + 12 * rows + 4 * seen,
+            "flops": seen * case["heads"] * (2 * case["dim"] + 3)}
+
+
+def _values():
+    """The 256 E4M3 values, from the format: sign, 4 bits of exponent (bias 7), 3 of mantissa."""
+    c = torch.arange(256, device="cuda")
+    e, f = (c >> 3) & 15, (c & 7).double()
+    powers = torch.tensor([2.0 ** (p - 10) for p in range(16)], dtype=torch.float64, device="cuda")
+    v = torch.where(e == 0, f * 2.0 ** -9, (8 + f) * powers[e])
+    v = torch.where((c & 127) == 127, math.nan, v)
+    return torch.where(c >= 128, -v, v)
+
+
+def _nearest(q):
+    """The E4M3 value nearest to each q in 64 bits, at a tie the one of even mantissa; q within +-448."""
+    table = _values()[:127]
+    a = q.abs()
+    hi = torch.searchsorted(table, a).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    up, down = table[hi] - a, a - table[lo]
+    code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return torch.where(q < 0, -1.0, 1.0) * table[code]
+
+
+def _exact_scale(top):
+    powers = torch.tensor([2.0 ** p for p in range(-126, 122)], dtype=torch.float64, device="cuda")
+    return powers[torch.searchsorted(E4M3_MAX * powers, top)]
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    if case["op"] == "quantise":
+        x, tile = st["x"].double(), st["tile"]
+        rows, k = x.shape
+        codes, scales = torch.empty_like(x), torch.empty(st["scales"].shape, dtype=torch.float64, device="cuda")
+        for j in range(scales.shape[1]):
+            part = x[:, j * BLOCK:(j + 1) * BLOCK]
+            top = part.abs().amax(1)
+            if tile > 1:
+                top = torch.stack([r.amax() for r in top.split(tile)])
+            scales[:, j] = _exact_scale(top)
+            codes[:, j * BLOCK:(j + 1) * BLOCK] = _nearest(part / scales[:, j].repeat_interleave(tile)[:rows, None])
+        return {"codes": codes, "scales": scales}
+    values = _values()
+    if case["op"] == "product":
+        m, n, k = case["m"], case["n"], case["k"]
+        c = torch.zeros((m, n), dtype=torch.float64, device="cuda")
+        for j in range(_blocks(k)):
+            cols = slice(j * BLOCK, min(k, (j + 1) * BLOCK))
+            p = torch.einsum("mk,nk->mn", values[st["a"][:, cols].long()], values[st["b"][:, cols].long()])
+            c += p * st["sa"][:, j, None].double() * st["sb"][:, j].double().repeat_interleave(BLOCK)[:n]
+        return c
+    if case["op"] == "write":
+        x = st["k_raw"].double()
+        d = x - x.sum(-1, keepdim=True) / case["dim"]
+        var = torch.einsum("rd,rd->r", d, d) / case["dim"]
+        y = torch.addcmul(st["ln_b"].double(), d / torch.sqrt(var + EPS)[:, None], st["ln_w"].double())
+        scale = _exact_scale(y.abs().amax(-1))
+        at = st["base"] + st["positions"].long()
+        k, ks, gate = values[st["idx_k"].long()], st["idx_scale"].double(), st["idx_gate"].double()
+        k[at], ks[at], gate[at] = _nearest(y / scale[:, None]), scale, st["gate"].double()
+        last = st["positions"].view(-1, case["per_seq"])[:, -1]
+        return {"idx_k": k, "idx_scale": ks, "idx_gate": gate, "written": last + 1}
+    out, per = torch.zeros(st["scores"].shape, dtype=torch.float64, device="cuda"), case["per_seq"]
+    first = 0
+    for s, n in enumerate(_contexts(case)):
+        k = values[st["idx_k"][first:first + n].long()] * st["idx_scale"][first:first + n, None].double()
+        for i in range(per):
+            r, seen = s * per + i, n - per + 1 + i
+            q = values[st["q"][r].long()] * st["q_scale"][r, :, None].double()
+            dots = torch.einsum("hd,td->ht", q, k[:seen])
+            score = torch.einsum("h,ht->t", st["head_w"][r].double(), torch.relu(dots))
+            out[r, :seen] = score * st["idx_gate"][first:first + seen].double()
+        first += n
+    return out
