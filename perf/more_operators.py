@@ -26,31 +26,31 @@ EPS = 1e-6
 def listed():
     return [
         # One token's layer input before its projections: the smallest call, pure latency.
-        dict(name="quantise, one token", op="quantise", rows=1, k=4096, tile=1, fp32=False),
+        dict(name="quantise: one token", op="quantise", rows=1, k=4096, tile=1, fp32=False),
         # The attention output of a prompt chunk of 1,024 rows (64 heads x 512) before its projection.
-        dict(name="quantise, prompt chunk", op="quantise", rows=1024, k=32768, tile=1, fp32=False),
+        dict(name="quantise: prompt chunk", op="quantise", rows=1024, k=32768, tile=1, fp32=False),
         # A weight of odd shape quantised in 128 x 128 blocks from its FP32 master, as at load time.
-        dict(name="quantise, odd weight", op="quantise", rows=5003, k=4112, tile=128, fp32=True),
+        dict(name="quantise: odd weight", op="quantise", rows=5003, k=4112, tile=128, fp32=True),
         # One decode token through the stacked query and latent projection.
-        dict(name="product, one token", op="product", m=1, n=2048, k=4096, fp32=False),
+        dict(name="product: one token", op="product", m=1, n=2048, k=4096, fp32=False),
         # A decode batch of 32 requests through the output projection of 64 heads: the largest weight.
-        dict(name="product, decode batch", op="product", m=32, n=4096, k=32768, fp32=False),
+        dict(name="product: decode batch", op="product", m=32, n=4096, k=32768, fp32=False),
         # A prompt chunk of 1,024 rows through the output projection.
-        dict(name="product, prompt chunk", op="product", m=1024, n=4096, k=32768, fp32=False),
+        dict(name="product: prompt chunk", op="product", m=1024, n=4096, k=32768, fp32=False),
         # An odd number of rows through weights of odd shape, FP32 out.
-        dict(name="product, odd sizes", op="product", m=777, n=1003, k=4112, fp32=True),
+        dict(name="product: odd sizes", op="product", m=777, n=1003, k=4112, fp32=True),
         # The keys of a verify's four rows.
-        dict(name="key write, verify", op="write", seqs=1, per_seq=4, dim=128, ctx=32768, mix=1),
+        dict(name="key write: verify", op="write", seqs=1, per_seq=4, dim=128, ctx=32768, mix=1),
         # The keys of a prompt chunk of 4,001 rows.
-        dict(name="key write, prompt chunk", op="write", seqs=4001, per_seq=1, dim=128, ctx=32768, mix=2),
+        dict(name="key write: prompt chunk", op="write", seqs=4001, per_seq=1, dim=128, ctx=32768, mix=2),
         # One request decoding at 32k context.
-        dict(name="scores, one decode", op="scores", seqs=1, per_seq=1, heads=32, dim=128, ctx_lo=32768,
+        dict(name="scores: one decode", op="scores", seqs=1, per_seq=1, heads=32, dim=128, ctx_lo=32768,
              ctx_hi=32768, mix=3),
         # Long-context decode of 64 requests at 4k to 128k, 64 index heads: the most cache read by one call.
-        dict(name="scores, long decode", op="scores", seqs=64, per_seq=1, heads=64, dim=128, ctx_lo=4096,
+        dict(name="scores: long decode", op="scores", seqs=64, per_seq=1, heads=64, dim=128, ctx_lo=4096,
              ctx_hi=131072, mix=4),
         # The last 1,024 tokens of a 9,000-token prompt, each row with its own horizon.
-        dict(name="scores, prompt chunk", op="scores", seqs=1, per_seq=1024, heads=32, dim=128, ctx_lo=9000,
+        dict(name="scores: prompt chunk", op="scores", seqs=1, per_seq=1024, heads=32, dim=128, ctx_lo=9000,
              ctx_hi=9000, mix=5),
     ]
 
