@@ -59,7 +59,7 @@
 extern "C" {
 #endif
 
-#define DSA_ABI_VERSION 6
+#define DSA_ABI_VERSION 7
 #define DSA_LATENT_DIM 512
 
 typedef enum dsa_status {
@@ -420,6 +420,58 @@ int32_t dsa_dense_mm_splits(int32_t n_out, int32_t k, int32_t num_sms);
 /* Workspace bytes dsa_dense_mm_bf16 needs on the current device for a weight
  * of n_out x k (0 when it needs none or on bad arguments). */
 size_t dsa_dense_mm_workspace_bytes(int32_t n_out, int32_t k);
+
+/*
+ * 8-bit operands with a scale for each block of 128 along k: the codes and
+ * scales that dsa_dense_mm_fp8 and dsa_index_scores_fp8 take.  No counterpart on
+ * the pages, whose projections and indexer keys are bf16: half the bytes.  For
+ * each block of k [128 j, 128 j + 128) of one row (block_rows = 1: activations,
+ * queries) or of 128 consecutive rows (block_rows = 128: weights), the last ones
+ * of a row or of the tensor shorter:
+ *   scale = the smallest power of two, 2^-126 at least, with max |x| <= 448 scale
+ *           (the maximum over the block's finite elements)
+ *   code  = E4M3_RNE(x / scale)         (x / scale is exact: one rounding)
+ * An infinity becomes +-448, a NaN the code 0x7F.  A power of two costs E4M3 no
+ * precision against max / 448.
+ *   x      [rows][k] bf16 (x_fp32 = 0) or fp32 (1), 16-byte aligned
+ *   codes  [rows][k] E4M3, 16-byte aligned, not overlapping x
+ *   scales [ceil(rows / block_rows)][ceil(k / 128)] fp32
+ * rows >= 1; k >= 16 and a multiple of 16; rows * ceil(k / 128) < 2^31, and with
+ * block_rows = 128 rows <= 65535 * 128 (DSA_ERR_UNSUPPORTED).
+ */
+dsa_status dsa_quantize_fp8(const void *x, int32_t x_fp32, int32_t rows, int32_t k,
+                            int32_t block_rows, uint8_t *codes, float *scales, void *stream);
+
+/*
+ * Matrix product of 8-bit operands with a scale for each block of 128, from one
+ * token to a prompt's chunk (the FP8 form of dsa_dense_mm_bf16; "glm5next_dsa/
+ * layer.rs", the gemm helper, C[M, N] = A[M, K] @ B[N, K]^T):
+ *   c[m][n] = sum_j a_scale[m][j] * b_scale[n / 128][j]
+ *                   * sum_{k in block j} e4m3(a[m][k]) * e4m3(b[n][k])
+ *   a [m_rows][k] E4M3, row-major, 16-byte aligned
+ *   a_scale [m_rows][ceil(k / 128)] fp32          (dsa_quantize_fp8, block_rows 1)
+ *   b [n_out][k] E4M3 weight, row-major, 16-byte aligned
+ *   b_scale [ceil(n_out / 128)][ceil(k / 128)] fp32  (block_rows 128, or a
+ *           checkpoint's: the scales may be any fp32 values)
+ *   c [m_rows][n_out] bf16 (c_fp32 = 0, round to nearest even) or fp32
+ *     (c_fp32 = 1), 16-byte aligned, not overlapping an input
+ * m_rows in [1, 65535] and n_out up to 65535 * 128 (DSA_ERR_UNSUPPORTED above);
+ * k >= 16 and a multiple of 16 (DSA_ERR_INVALID_ARG).  No workspace.  The weight
+ * and its scales are taken to be complete before the kernel issued just before
+ * this call on the stream started (dsa_dense_mm_bf16 reads its weight likewise);
+ * a and a_scale may be its output.
+ * Numerics: a block's products are exact and accumulate in FP32 on the tensor
+ * cores; each block's sum is multiplied by the product of its two scales
+ * (rounded to FP32) and added in FP32, blocks in order, within each of the
+ * ranges that k is split into when the output has few tiles; the ranges are then
+ * added in order.  A NaN code makes the results that it enters NaN.  With
+ * m_rows <= 64 a row's result is bit-identical whatever m_rows is and whatever
+ * the other rows hold.  After a wait that gave up (DSA_DEVERR_TIMEOUT) c holds
+ * nothing to rely on.
+ */
+dsa_status dsa_dense_mm_fp8(const uint8_t *a, const float *a_scale, const uint8_t *b,
+                            const float *b_scale, void *c, int32_t m_rows, int32_t n_out, int32_t k,
+                            int32_t c_fp32, void *stream);
 
 /*
  * Row plan of a batch of requests: block tables grown and shrunk from a free

@@ -86,6 +86,8 @@ def load() -> ctypes.CDLL:
         "dsa_indexer_write": [RP, P, P, P, f32, P, P, P, P, i64, i32, P, i32, P],
         "dsa_select_pools": [RP, P, i32, P, i32, i32, i32, P, P],
         "dsa_expand_selection": [RP, P, i32, i32, P, i32, P],
+        "dsa_quantize_fp8": [P, i32, i32, i32, i32, P, P, P],
+        "dsa_dense_mm_fp8": [P, P, P, P, P, i32, i32, i32, i32, P],
         "dsa_plan_rows": [ctypes.POINTER(Plan), P],
         "dsa_mla_chunk_fp8": [ctypes.POINTER(Seqs), P, P, i64, i32, i32, i32, f32, f32, P, P, P, sz, P],
     }
@@ -371,6 +373,61 @@ def _table(t: torch.Tensor, rows: int, name: str) -> tuple[int, int, int]:
     if (t.shape[1] > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name}: expected contiguous rows, got strides {t.stride()}")
     return t.data_ptr(), t.shape[1], t.stride(0) if rows > 1 else t.shape[1]
+
+
+def _here(tensors: dict) -> None:
+    """Every tensor given is on the current device."""
+    _current(_on_device(tensors))
+
+
+def _value_type(t: torch.Tensor, name: str) -> int:
+    """1 for FP32, 0 for bf16 (as bfloat16 or its bits)."""
+    if t.dtype is torch.float32:
+        return 1
+    if t.dtype not in _BITS16:
+        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    return 0
+
+
+def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                     block_rows: int = 1, stream=None) -> None:
+    """E4M3 codes (uint8, the shape of x) and power-of-two scales of x [..., k],
+    bf16 or float32.  ``block_rows`` 1: a scale for each 128 of k of a row, scales
+    [..., ceil(k / 128)] (or [...] where that is 1).  128 (x [rows, k]): for each 128
+    x 128, scales [ceil(rows / 128), ceil(k / 128)]."""
+    _here(dict(x=x, codes=codes, scales=scales))
+    fp32 = _value_type(x, "x")
+    if x.dim() < 1 or (block_rows != 1 and x.dim() != 2):
+        raise ValueError(f"x: unexpected shape {tuple(x.shape)}")
+    k, kb = x.shape[-1], (x.shape[-1] + 127) // 128
+    _shaped(codes, tuple(x.shape), "codes")
+    if block_rows != 1:
+        _shaped(scales, ((x.shape[0] + block_rows - 1) // block_rows, kb), "scales")
+    elif kb != 1 or tuple(scales.shape) != tuple(x.shape[:-1]):
+        _shaped(scales, tuple(x.shape[:-1]) + (kb,), "scales")
+    st = load().dsa_quantize_fp8(_ptr(x, None, "x"), fp32, x.numel() // max(k, 1), k, int(block_rows),
+                                 _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.float32, "scales"),
+                                 _stream(stream))
+    _check("dsa_quantize_fp8", st)
+
+
+def dsa_dense_mm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                     c: torch.Tensor, stream=None) -> None:
+    """c[m][n] = sum_k (a[m][k] a_scale[m][k / 128]) (b[n][k] b_scale[n / 128][k / 128]):
+    E4M3 codes (uint8) a [M, K] and weight b [N, K], float32 scales [M, ceil(K / 128)]
+    and [ceil(N / 128), ceil(K / 128)], c [M, N] bf16 or float32."""
+    _here(dict(a=a, a_scale=a_scale, b=b, b_scale=b_scale, c=c))
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"shapes a {tuple(a.shape)}, b {tuple(b.shape)}")
+    (m, k), n = a.shape, b.shape[0]
+    kb = (k + 127) // 128
+    _shaped(a_scale, (m, kb), "a_scale")
+    _shaped(b_scale, ((n + 127) // 128, kb), "b_scale")
+    _shaped(c, (m, n), "c")
+    st = load().dsa_dense_mm_fp8(_ptr(a, torch.uint8, "a"), _ptr(a_scale, torch.float32, "a_scale"),
+                                 _ptr(b, torch.uint8, "b"), _ptr(b_scale, torch.float32, "b_scale"),
+                                 _ptr(c, None, "c"), m, n, k, _value_type(c, "c"), _stream(stream))
+    _check("dsa_dense_mm_fp8", st)
 
 
 _BITS32 = (torch.int32, torch.uint32)

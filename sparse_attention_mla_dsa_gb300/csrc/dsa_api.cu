@@ -468,6 +468,73 @@ dsa_status dsa_dense_mm_bf16(const uint16_t* a, const uint16_t* b, void* c, int3
   return launched(launch_dense_mm(p, wmap, amap, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_quantize_fp8(const void* x, int32_t x_fp32, int32_t rows, int32_t k,
+                            int32_t block_rows, uint8_t* codes, float* scales, void* stream) {
+  if (x == nullptr || codes == nullptr || scales == nullptr) return DSA_ERR_INVALID_ARG;
+  if (rows < 1 || k < 16 || k % 16 != 0) return DSA_ERR_INVALID_ARG;
+  if ((x_fp32 != 0 && x_fp32 != 1) || (block_rows != 1 && block_rows != 128)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return DSA_ERR_INVALID_ARG;
+  QuantizeParams p{};
+  p.x = x;
+  p.codes = codes;
+  p.scales = scales;
+  p.rows = rows;
+  p.k = k;
+  p.kblocks = (k + 127) / 128;
+  p.block_rows = block_rows;
+  p.x_fp32 = x_fp32;
+  if (static_cast<int64_t>(rows) * p.kblocks > INT32_MAX ||
+      (block_rows > 1 && (rows + static_cast<int64_t>(block_rows) - 1) / block_rows > 65535))
+    return DSA_ERR_UNSUPPORTED;
+  if (device_info() == nullptr) return DSA_ERR_CUDA;
+  return launched(launch_quantize_fp8(p, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_dense_mm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* b,
+                            const float* b_scale, void* c, int32_t m_rows, int32_t n_out, int32_t k,
+                            int32_t c_fp32, void* stream) {
+  if (a == nullptr || a_scale == nullptr || b == nullptr || b_scale == nullptr || c == nullptr)
+    return DSA_ERR_INVALID_ARG;
+  if (m_rows < 1 || n_out < 1 || k < 16 || k % 16 != 0) return DSA_ERR_INVALID_ARG;
+  if (c_fp32 != 0 && c_fp32 != 1) return DSA_ERR_INVALID_ARG;
+  if (m_rows > 65535 || n_out > 65535 * 128) return DSA_ERR_UNSUPPORTED;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
+
+  Fp8MmParams p{};
+  p.a_scale = a_scale;
+  p.b_scale = b_scale;
+  p.c = c;
+  p.err = dev->err;
+  p.m = m_rows;
+  p.n = n_out;
+  p.k = k;
+  p.c_fp32 = c_fp32;
+  p.wait_ns = wait_limit_ns();
+  plan_fp8_mm(p, dev->num_sms);
+
+  // Boxes of 128 bytes of k (the swizzle span, one block of scales); rows and
+  // columns past the tensors read as zero.
+  CUtensorMap wmap, amap;
+  auto map = [&](CUtensorMap* out, const uint8_t* t, int32_t rows, int32_t box_rows) {
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(k)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estride[2] = {1, 1};
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(t), dim, stride, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult cr = map(&wmap, b, n_out, 128);
+  if (cr == CUDA_SUCCESS) cr = map(&amap, a, m_rows, p.row_tile);
+  if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
+  return launched(launch_fp8_mm(p, wmap, amap, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
   if (plan == nullptr) return DSA_ERR_INVALID_ARG;
   const dsa_plan& p = *plan;

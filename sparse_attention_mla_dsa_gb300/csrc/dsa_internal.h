@@ -156,6 +156,37 @@ size_t dense_mm_workspace_bytes(int32_t n, int32_t k, int num_sms);
 cudaError_t launch_dense_mm(const DenseMmParams& p, const CUtensorMap& wmap,
                             const CUtensorMap& amap, cudaStream_t stream);
 
+struct QuantizeParams {
+  const void* x;          // [rows][k] bf16 or FP32
+  uint8_t* codes;         // [rows][k] E4M3
+  float* scales;          // [ceil(rows / block_rows)][kblocks]
+  int32_t rows, k;
+  int32_t kblocks;        // ceil(k / 128)
+  int32_t block_rows;     // 1 or 128
+  int32_t x_fp32;
+};
+cudaError_t launch_quantize_fp8(const QuantizeParams& p, cudaStream_t stream);
+
+struct Fp8MmParams {
+  const float* a_scale;   // [m][kblocks]
+  const float* b_scale;   // [ceil(n / 128)][kblocks]
+  void* c;                // [m][n] bf16 or fp32
+  int* err;
+  int32_t m, n, k;
+  int32_t c_fp32;
+  int32_t kblocks;        // ceil(k / 128)
+  int32_t row_tile;       // rows of a that a CTA multiplies
+  int32_t kb_per_split;   // K blocks per CTA
+  int32_t splits;         // K ranges per tile: the CTAs of a cluster
+  uint64_t wait_ns;
+};
+// Fills in kblocks / row_tile / kb_per_split / splits from (m, n, k) and the SM count.
+void plan_fp8_mm(Fp8MmParams& p, int num_sms);
+// `wmap` describes the weight [n][k], `amap` the activations [m][k], both bytes,
+// for boxes of 128 bytes of k by 128 and by row_tile rows.
+cudaError_t launch_fp8_mm(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
+                          cudaStream_t stream);
+
 struct DecodeParams {
   dsa_rows rows;
   const uint16_t* q;

@@ -1,0 +1,169 @@
+// quantize_fp8.cu -- bf16 or FP32 values to E4M3 codes with a power-of-two
+// scale for each block of 128 along k, of one row (activations, queries) or of
+// 128 rows (weights).
+//
+//   2^e = smallest power of two, 2^-126 at least, with max |x| <= 448 * 2^e
+//   code = E4M3_RNE(x / 2^e)
+// E4M3 keeps its three bits of mantissa whatever the scale, so a power of two
+// costs no precision against max / 448, and x / 2^e is exact (where it falls
+// below 2^-126 its code is 0 either way): the code is rounded once, and
+// values that are quantised again stay what they are.
+//
+// Bound by memory: 3 bytes an element from bf16, 5 from FP32.  Rows of 1: a
+// block is 16 bytes of each of 16 lanes (bf16) or of 32 (FP32), its largest
+// element is found by shuffles and its values stay in registers in between.
+// Tiles of 128 rows: one CTA a tile, which it holds in registers.
+#include "dsa_internal.h"
+#include "fp8_device.cuh"
+
+namespace dsa {
+namespace {
+
+using fp8::kBlock;
+
+constexpr int kThreads = 256;
+constexpr int kTileRows = 128;
+
+// 16 bytes of x: 8 bf16 or 4 FP32 values.
+template <bool kF32>
+struct Vec {
+  static constexpr int kElems = kF32 ? 4 : 8;
+  static constexpr int kLanes = kBlock / kElems;  // lanes of one block of a row
+  uint4 v;
+
+  // Bits of the largest |x| as a float, infinities and NaN left out.
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kF32) {
+        const uint32_t a = w[i] & 0x7FFFFFFFu;
+        m = max(m, a < 0x7F800000u ? a : 0u);
+      } else {
+        const uint32_t hi = w[i] & 0x7FFF0000u, lo = (w[i] << 16) & 0x7FFF0000u;
+        m = max(m, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
+      }
+    }
+    return m;
+  }
+
+  __device__ __forceinline__ void store_codes(uint8_t* dst, float inv) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (kF32) {
+      *reinterpret_cast<uint32_t*>(dst) =
+          fp8::e4m3x4(__uint_as_float(w[0]) * inv, __uint_as_float(w[1]) * inv,
+                      __uint_as_float(w[2]) * inv, __uint_as_float(w[3]) * inv);
+    } else {
+      uint32_t c[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = fp8::e4m3x4(__uint_as_float(w[2 * i] << 16) * inv, __uint_as_float(w[2 * i] & 0xFFFF0000u) * inv,
+                           __uint_as_float(w[2 * i + 1] << 16) * inv,
+                           __uint_as_float(w[2 * i + 1] & 0xFFFF0000u) * inv);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 load16(const void* p) { return ld_dep_u4(static_cast<const uint4*>(p)); }
+
+// kUnroll blocks a group of lanes, loaded together.
+template <bool kF32, int kUnroll>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantizeParams p) {
+  using V = Vec<kF32>;
+  constexpr int kGroups = kThreads / V::kLanes;  // blocks that a CTA works on at a time
+  const int group = threadIdx.x / V::kLanes, lane = threadIdx.x % V::kLanes;
+  const uint32_t kb = static_cast<uint32_t>(p.kblocks);
+  const uint32_t total = static_cast<uint32_t>(p.rows) * kb;  // below 2^31
+  const uint32_t b0 = blockIdx.x * (kGroups * kUnroll) + group;
+  grid_dep_launch();
+  grid_dep_wait();
+  V v[kUnroll];
+  int64_t at[kUnroll];  // -1: nothing of the tensor here
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t b = b0 + u * kGroups;
+    const uint32_t row = b / kb;
+    const int col = static_cast<int>(b - row * kb) * kBlock + lane * V::kElems;
+    at[u] = b < total && col < p.k ? static_cast<int64_t>(row) * p.k + col : -1;
+    v[u].v = make_uint4(0u, 0u, 0u, 0u);
+    if (at[u] >= 0) v[u].v = load16(static_cast<const char*>(p.x) + at[u] * (kF32 ? 4 : 2));
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    uint32_t top = v[u].top();
+#pragma unroll
+    for (int o = V::kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const uint32_t scale = fp8::scale_bits(top);
+    if (at[u] >= 0) {
+      v[u].store_codes(p.codes + at[u], fp8::inverse_scale(scale));
+      if (lane == 0) p.scales[b0 + u * kGroups] = __uint_as_float(scale);
+    }
+  }
+}
+
+// One CTA a tile of 128 x 128.
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantizeParams p) {
+  using V = Vec<kF32>;
+  constexpr int kRowsAtOnce = kThreads / V::kLanes;
+  constexpr int kVecs = kTileRows / kRowsAtOnce;
+  __shared__ uint32_t warp_top[kThreads / 32];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kTileRows + threadIdx.x / V::kLanes;
+  const int col = static_cast<int>(blockIdx.x) * kBlock + (threadIdx.x % V::kLanes) * V::kElems;
+  grid_dep_launch();
+  grid_dep_wait();
+  V v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int64_t row = row0 + i * kRowsAtOnce;
+    v[i].v = make_uint4(0u, 0u, 0u, 0u);
+    if (row < p.rows && col < p.k)
+      v[i].v = load16(static_cast<const char*>(p.x) + (row * p.k + col) * (kF32 ? 4 : 2));
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) top = max(top, v[i].top());
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_top[w]);
+  const uint32_t scale = fp8::scale_bits(top);
+  const float inv = fp8::inverse_scale(scale);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int64_t row = row0 + i * kRowsAtOnce;
+    if (row < p.rows && col < p.k) v[i].store_codes(p.codes + row * p.k + col, inv);
+  }
+  if (threadIdx.x == 0)
+    p.scales[static_cast<int64_t>(blockIdx.y) * p.kblocks + blockIdx.x] = __uint_as_float(scale);
+}
+
+template <bool kF32, int kUnroll>
+cudaError_t launch_rows(const QuantizeParams& p, cudaLaunchConfig_t& cfg) {
+  constexpr int64_t kPerCta = kThreads / Vec<kF32>::kLanes * kUnroll;
+  const int64_t total = static_cast<int64_t>(p.rows) * p.kblocks;
+  cfg.gridDim = dim3(static_cast<unsigned>((total + kPerCta - 1) / kPerCta), 1, 1);
+  return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kF32, kUnroll>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_fp8(const QuantizeParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.block_rows == kTileRows) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.kblocks), static_cast<unsigned>((p.rows + kTileRows - 1) / kTileRows), 1);
+    return p.x_fp32 ? cudaLaunchKernelEx(&cfg, quantize_tiles_kernel<true>, p)
+                    : cudaLaunchKernelEx(&cfg, quantize_tiles_kernel<false>, p);
+  }
+  return p.x_fp32 ? launch_rows<true, 4>(p, cfg) : launch_rows<false, 4>(p, cfg);
+}
+
+}  // namespace dsa
