@@ -474,6 +474,61 @@ dsa_status dsa_dense_mm_fp8(const uint8_t *a, const float *a_scale, const uint8_
                             int32_t c_fp32, void *stream);
 
 /*
+ * Indexer write side into an FP8 key cache (dsa_indexer_write, quantised as it is
+ * written): with t = idx_base[r] + positions[r] and y the LayerNorm (with bias)
+ * of k_raw[r] as there, in double and not rounded to bf16,
+ *   idx_scale[t] = the smallest power of two, 2^-126 at least, with
+ *                  max_d |y[d]| <= 448 idx_scale[t]  (over the finite y)
+ *   idx_k[t][d]  = E4M3_RNE(y[d] / idx_scale[t])
+ *   idx_gate[t]  = gate[r]                          (when gate != NULL)
+ *   k_raw [rows][index_dim] bf16, ln_w, ln_b [index_dim] bf16, 8-byte aligned
+ *   idx_k [idx_tokens][index_dim] E4M3, 4-byte aligned; idx_scale [idx_tokens] fp32;
+ *   idx_gate [idx_tokens] bf16; gate [rows] bf16 or NULL
+ * rows->positions is required; index_dim 64 or 128 (DSA_ERR_UNSUPPORTED otherwise).
+ * A row whose y is not finite has codes 0x7F or +-448 there.  Rows must not share
+ * an arena row.  Without idx_written each row stands for itself; with it the rows
+ * of a sequence (rows_per_seq consecutive ones, at most 32) are written together
+ * or not at all: not if one has not position seq_lens[r] - 1 or does not follow
+ * the one before (DSA_DEVERR_POSITION), lies outside [0, idx_tokens)
+ * (DSA_DEVERR_ARENA), or if the sequence's count is below its first position
+ * (DSA_DEVERR_BEHIND); if written, the count becomes the last position + 1 (more
+ * is the leftover of a rejected verify and is rewound).  An empty row of
+ * dsa_plan_rows (position 0, seq_len 0) is skipped without a record, a sequence of
+ * such rows keeps its count, and one that mixes them with others is refused
+ * (DSA_DEVERR_POSITION).
+ */
+dsa_status dsa_indexer_write_fp8(const dsa_rows *rows, const uint16_t *k_raw, const uint16_t *ln_w,
+                                 const uint16_t *ln_b, float eps, const uint16_t *gate,
+                                 const int64_t *idx_base, uint8_t *idx_k, float *idx_scale,
+                                 uint16_t *idx_gate, int64_t idx_tokens, int32_t index_dim,
+                                 int32_t *idx_written, int32_t rows_per_seq, void *stream);
+
+/*
+ * Index scores over that cache (dsa_index_scores with 8-bit keys and queries: half
+ * the bytes a key).  For each row r and token t in [0, seq_lens[r]), b = idx_base[r]:
+ *   scores[r*max_len + t] = idx_gate[b+t] * idx_scale[b+t]
+ *       * sum_h (head_w[r][h] * q_scale[r][h]) * max(0, sum_d e4m3(q[r][h][d]) * e4m3(idx_k[b+t][d]))
+ *   q [rows][index_heads][index_dim] E4M3 and q_scale [rows][index_heads] fp32
+ *     (dsa_quantize_fp8 of [rows * index_heads][index_dim] queries)
+ *   idx_k [idx_tokens][index_dim] E4M3, idx_scale [idx_tokens] fp32 (any values)
+ *   idx_gate [idx_tokens] bf16, or NULL: 1
+ * The other arguments, the shapes supported, flags (DSA_INDEX_INPUTS_BEFORE_PREDECESSOR
+ * or 0), what is checked on the device and the errors recorded are those of
+ * dsa_index_scores_ex; q and idx_k are 16-byte aligned.  max(0, NaN) is 0: a NaN
+ * code takes its head out of the sum.
+ * Numerics: the products are exact and accumulate in FP32 on the tensor cores; the
+ * heads are added in FP32 in order, then multiplied by the product of gate and
+ * scale.  Each row's result does not depend on rows_per_seq or on the other rows
+ * (bit for bit).
+ */
+dsa_status dsa_index_scores_fp8(const dsa_rows *rows, const uint8_t *q, const float *q_scale,
+                                const float *head_w, const uint8_t *idx_k, const float *idx_scale,
+                                const uint16_t *idx_gate, int64_t idx_tokens, const int64_t *idx_base,
+                                int32_t index_heads, int32_t index_dim, int32_t rows_per_seq,
+                                int32_t max_len, float *scores, const int32_t *idx_written,
+                                uint32_t flags, void *stream);
+
+/*
  * Row plan of a batch of requests: block tables grown and shrunk from a free
  * list, and the per-row metadata of the step (dsa_rows: positions, slots,
  * seq_lens, block_table; "glm5next_dsa/layer.rs", decode_k, the K-row

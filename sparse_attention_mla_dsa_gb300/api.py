@@ -87,6 +87,8 @@ def load() -> ctypes.CDLL:
         "dsa_select_pools": [RP, P, i32, P, i32, i32, i32, P, P],
         "dsa_expand_selection": [RP, P, i32, i32, P, i32, P],
         "dsa_quantize_fp8": [P, i32, i32, i32, i32, P, P, P],
+        "dsa_indexer_write_fp8": [RP, P, P, P, f32, P, P, P, P, P, i64, i32, P, i32, P],
+        "dsa_index_scores_fp8": [RP, P, P, P, P, P, P, i64, P, i32, i32, i32, i32, P, P, u32, P],
         "dsa_dense_mm_fp8": [P, P, P, P, P, i32, i32, i32, i32, P],
         "dsa_plan_rows": [ctypes.POINTER(Plan), P],
         "dsa_mla_chunk_fp8": [ctypes.POINTER(Seqs), P, P, i64, i32, i32, i32, f32, f32, P, P, P, sz, P],
@@ -428,6 +430,77 @@ def dsa_dense_mm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
                                  _ptr(b, torch.uint8, "b"), _ptr(b_scale, torch.float32, "b_scale"),
                                  _ptr(c, None, "c"), m, n, k, _value_type(c, "c"), _stream(stream))
     _check("dsa_dense_mm_fp8", st)
+
+
+def dsa_indexer_write_fp8(rows: Rows, k_raw: torch.Tensor, ln_w: torch.Tensor, ln_b: torch.Tensor,
+                          eps: float, idx_base: torch.Tensor, idx_k: torch.Tensor, idx_scale: torch.Tensor,
+                          idx_gate: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                          idx_written: torch.Tensor | None = None, rows_per_seq: int = 1,
+                          stream=None) -> None:
+    """dsa_indexer_write into an FP8 key cache: LayerNorm (with bias) of k_raw [R, D]
+    bf16, stored as E4M3 codes into idx_k [T, D] uint8 at row idx_base[r] +
+    positions[r] with its power-of-two scale in idx_scale [T] float32."""
+    _here(dict(k_raw=k_raw, ln_w=ln_w, ln_b=ln_b, idx_base=idx_base, idx_k=idx_k, idx_scale=idx_scale,
+               idx_gate=idx_gate, gate=gate, idx_written=idx_written))
+    R = rows.rows
+    if idx_k.dim() != 2:
+        raise ValueError(f"idx_k: expected two dimensions, got {tuple(idx_k.shape)}")
+    T, D = idx_k.shape
+    _shaped(k_raw, (R, D), "k_raw")
+    _shaped(ln_w, (D,), "ln_w")
+    _shaped(ln_b, (D,), "ln_b")
+    _shaped(idx_base, (R,), "idx_base")
+    _shaped(idx_scale, (T,), "idx_scale")
+    _shaped(idx_gate, (T,), "idx_gate")
+    _shaped(gate, (R,), "gate")
+    if idx_written is not None and rows_per_seq > 0:
+        _shaped(idx_written, (R // rows_per_seq,), "idx_written")
+    st = load().dsa_indexer_write_fp8(ctypes.byref(rows), _ptr(k_raw, torch.uint16, "k_raw"),
+                                      _ptr(ln_w, torch.uint16, "ln_w"), _ptr(ln_b, torch.uint16, "ln_b"),
+                                      float(eps), _ptr(gate, torch.uint16, "gate"),
+                                      _ptr(idx_base, torch.int64, "idx_base"),
+                                      _ptr(idx_k, torch.uint8, "idx_k"),
+                                      _ptr(idx_scale, torch.float32, "idx_scale"),
+                                      _ptr(idx_gate, torch.uint16, "idx_gate"), T, D,
+                                      _ptr(idx_written, torch.int32, "idx_written"), int(rows_per_seq),
+                                      _stream(stream))
+    _check("dsa_indexer_write_fp8", st)
+
+
+def dsa_index_scores_fp8(rows: Rows, q: torch.Tensor, q_scale: torch.Tensor, head_w: torch.Tensor,
+                         idx_k: torch.Tensor, idx_scale: torch.Tensor, idx_gate: torch.Tensor | None,
+                         idx_base: torch.Tensor, rows_per_seq: int, max_len: int, scores: torch.Tensor,
+                         idx_written: torch.Tensor | None = None, stream=None,
+                         inputs_early: bool = False) -> None:
+    """dsa_index_scores over an FP8 key cache: queries q [R, H, D] uint8 codes with
+    q_scale [R, H] float32 (dsa_quantize_fp8), keys idx_k [T, D] uint8 with idx_scale
+    [T] float32 (dsa_indexer_write_fp8), idx_gate [T] bf16 or None for 1, scores
+    [R, max_len] float32.  ``idx_written``, ``inputs_early``: as dsa_index_scores."""
+    _here(dict(q=q, q_scale=q_scale, head_w=head_w, idx_k=idx_k, idx_scale=idx_scale, idx_gate=idx_gate,
+               idx_base=idx_base, scores=scores, idx_written=idx_written))
+    R = rows.rows
+    if q.dim() != 3 or idx_k.dim() != 2 or q.shape[0] != R or q.shape[2] != idx_k.shape[1]:
+        raise ValueError(f"shapes q {tuple(q.shape)}, idx_k {tuple(idx_k.shape)}, rows {R}")
+    heads, dim, T = q.shape[1], q.shape[2], idx_k.shape[0]
+    _shaped(q_scale, (R, heads), "q_scale")
+    _shaped(head_w, (R, heads), "head_w")
+    _shaped(idx_scale, (T,), "idx_scale")
+    _shaped(idx_gate, (T,), "idx_gate")
+    _shaped(idx_base, (R,), "idx_base")
+    _shaped(scores, (R, int(max_len)), "scores")
+    if idx_written is not None and rows_per_seq > 0:
+        _shaped(idx_written, (R // rows_per_seq,), "idx_written")
+    st = load().dsa_index_scores_fp8(ctypes.byref(rows), _ptr(q, torch.uint8, "q"),
+                                     _ptr(q_scale, torch.float32, "q_scale"),
+                                     _ptr(head_w, torch.float32, "head_w"), _ptr(idx_k, torch.uint8, "idx_k"),
+                                     _ptr(idx_scale, torch.float32, "idx_scale"),
+                                     _ptr(idx_gate, torch.uint16, "idx_gate"), T,
+                                     _ptr(idx_base, torch.int64, "idx_base"), heads, dim, int(rows_per_seq),
+                                     int(max_len), _ptr(scores, torch.float32, "scores"),
+                                     _ptr(idx_written, torch.int32, "idx_written"),
+                                     DSA_INDEX_INPUTS_BEFORE_PREDECESSOR if inputs_early else 0,
+                                     _stream(stream))
+    _check("dsa_index_scores_fp8", st)
 
 
 _BITS32 = (torch.int32, torch.uint32)

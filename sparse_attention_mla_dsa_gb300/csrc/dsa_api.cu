@@ -90,6 +90,35 @@ dsa_status check_rows(const dsa_rows* rows, bool need_table) {
 
 dsa_status launched(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
+// What the score calls over bf16 and over FP8 keys share: the rows, their
+// launch groups, and the plan that follows from the shape.
+void set_index_rows(IndexParams& p, const DeviceInfo& dev, const dsa_rows& rows, int32_t rows_per_seq,
+                    int32_t index_heads, int32_t index_dim, int32_t max_len, uint32_t flags) {
+  p.seq_lens = rows.seq_lens;
+  p.err = dev.err;
+  p.rows = rows.rows;
+  p.rows_per_seq = rows_per_seq;
+  // Rows of one sequence share each key tile in groups of at most 64 score
+  // columns (a wider group makes the per-token epilogue, not HBM, the limit,
+  // and its q operand leaves room for one CTA per SM; the groups of a
+  // sequence run side by side and share the key tiles through L2); a head
+  // count that is not a multiple of 16 runs one row per launch group so that
+  // no 16-column TMEM load straddles two rows.
+  int sub = 64 / index_heads;
+  if (index_heads % 16 != 0) sub = 1;
+  sub = sub < 1 ? 1 : (sub > 32 ? 32 : sub);
+  if (sub > rows_per_seq) sub = rows_per_seq;
+  p.sub_rows = sub;
+  p.subs_per_seq = (rows_per_seq + sub - 1) / sub;
+  p.heads = index_heads;
+  p.dim = index_dim;
+  p.npad = ((sub * index_heads + 15) / 16) * 16;
+  p.max_len = max_len;
+  p.wait_ns = wait_limit_ns();
+  p.inputs_early = (flags & DSA_INDEX_INPUTS_BEFORE_PREDECESSOR) != 0 ? 1 : 0;
+  plan_index_scores(p, dev.num_sms);
+}
+
 }  // namespace
 
 int* device_error_word() {
@@ -163,36 +192,14 @@ dsa_status dsa_index_scores_ex(const dsa_rows* rows, const float* q_idx, const f
   if (!encode) return DSA_ERR_CUDA;
 
   IndexParams p{};
-  p.seq_lens = rows->seq_lens;
   p.q_idx = q_idx;
   p.head_w = head_w;
   p.gate = idx_gate;
   p.idx_base = idx_base;
   p.idx_written = idx_written;
   p.scores = scores;
-  p.err = dev->err;
   p.idx_tokens = idx_tokens;
-  p.rows = rows->rows;
-  p.rows_per_seq = rows_per_seq;
-  // Rows of one sequence share each key tile in groups of at most 64 score
-  // columns (a wider group makes the per-token epilogue, not HBM, the limit,
-  // and its q operand leaves room for one CTA per SM; the groups of a
-  // sequence run side by side and share the key tiles through L2); a head
-  // count that is not a multiple of 16 runs one row per launch group so that
-  // no 16-column TMEM load straddles two rows.
-  int sub = 64 / index_heads;
-  if (index_heads % 16 != 0) sub = 1;
-  sub = sub < 1 ? 1 : (sub > 32 ? 32 : sub);
-  if (sub > rows_per_seq) sub = rows_per_seq;
-  p.sub_rows = sub;
-  p.subs_per_seq = (rows_per_seq + sub - 1) / sub;
-  p.heads = index_heads;
-  p.dim = index_dim;
-  p.npad = ((sub * index_heads + 15) / 16) * 16;
-  p.max_len = max_len;
-  p.wait_ns = wait_limit_ns();
-  p.inputs_early = (flags & DSA_INDEX_INPUTS_BEFORE_PREDECESSOR) != 0 ? 1 : 0;
-  plan_index_scores(p, dev->num_sms);
+  set_index_rows(p, *dev, *rows, rows_per_seq, index_heads, index_dim, max_len, flags);
 
   // Key arena [idx_tokens, index_dim] bf16, boxes of 128 tokens x 64 dims
   // (128 bytes, the swizzle span); rows past the arena read as zero.
@@ -205,6 +212,59 @@ dsa_status dsa_index_scores_ex(const dsa_rows* rows, const float* q_idx, const f
                        gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
+  return launched(launch_index_scores(p, kmap, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_index_scores_fp8(const dsa_rows* rows, const uint8_t* q, const float* q_scale,
+                                const float* head_w, const uint8_t* idx_k, const float* idx_scale,
+                                const uint16_t* idx_gate, int64_t idx_tokens, const int64_t* idx_base,
+                                int32_t index_heads, int32_t index_dim, int32_t rows_per_seq,
+                                int32_t max_len, float* scores, const int32_t* idx_written,
+                                uint32_t flags, void* stream) {
+  if ((flags & ~DSA_INDEX_INPUTS_BEFORE_PREDECESSOR) != 0) return DSA_ERR_INVALID_ARG;
+  dsa_status st = check_rows(rows, false);
+  if (st != DSA_OK) return st;
+  if (q == nullptr || q_scale == nullptr || head_w == nullptr || idx_k == nullptr || idx_scale == nullptr ||
+      idx_base == nullptr || scores == nullptr || idx_tokens < 1 || max_len < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (rows_per_seq < 1 || rows->rows % rows_per_seq != 0) return DSA_ERR_INVALID_ARG;
+  if (index_dim != 64 && index_dim != 128) return DSA_ERR_UNSUPPORTED;
+  if (index_heads < 1 || index_heads > 256) return DSA_ERR_UNSUPPORTED;
+  if (idx_tokens > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(idx_k, 16) || !aligned(q_scale, 4) || !aligned(head_w, 4) ||
+      !aligned(idx_scale, 4) || !aligned(idx_gate, 2) || !aligned(idx_base, 8) || !aligned(scores, 4) ||
+      !aligned(idx_written, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (max_len == 0) return DSA_OK;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  const TensorMapEncoder encode = encode_tiled();
+  if (!encode) return DSA_ERR_CUDA;
+
+  IndexParams p{};
+  p.q_codes = q;
+  p.q_scale = q_scale;
+  p.k_scale = idx_scale;
+  p.head_w = head_w;
+  p.gate = idx_gate;
+  p.idx_base = idx_base;
+  p.idx_written = idx_written;
+  p.scores = scores;
+  p.idx_tokens = idx_tokens;
+  set_index_rows(p, *dev, *rows, rows_per_seq, index_heads, index_dim, max_len, flags);
+
+  // Key cache [idx_tokens, index_dim] bytes, boxes of 128 whole keys (a key is
+  // the swizzle span); keys past the cache read as zero.
+  CUtensorMap kmap;
+  const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(index_dim), static_cast<cuuint64_t>(idx_tokens)};
+  const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(index_dim)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(index_dim), 128};
+  const cuuint32_t estride[2] = {1, 1};
+  const CUresult cr = encode(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(idx_k), gdim,
+                             gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             index_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
   return launched(launch_index_scores(p, kmap, static_cast<cudaStream_t>(stream)));
 }
@@ -466,6 +526,48 @@ dsa_status dsa_dense_mm_bf16(const uint16_t* a, const uint16_t* b, void* c, int3
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
   return launched(launch_dense_mm(p, wmap, amap, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_indexer_write_fp8(const dsa_rows* rows, const uint16_t* k_raw, const uint16_t* ln_w,
+                                 const uint16_t* ln_b, float eps, const uint16_t* gate,
+                                 const int64_t* idx_base, uint8_t* idx_k, float* idx_scale,
+                                 uint16_t* idx_gate, int64_t idx_tokens, int32_t index_dim,
+                                 int32_t* idx_written, int32_t rows_per_seq, void* stream) {
+  dsa_status st = check_rows(rows, false);
+  if (st != DSA_OK) return st;
+  if (rows->positions == nullptr || k_raw == nullptr || ln_w == nullptr || ln_b == nullptr ||
+      idx_base == nullptr || idx_k == nullptr || idx_scale == nullptr || idx_tokens < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (gate != nullptr && idx_gate == nullptr) return DSA_ERR_INVALID_ARG;
+  if (index_dim != 64 && index_dim != 128) return DSA_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(k_raw, 8) || !aligned(ln_w, 8) || !aligned(ln_b, 8) || !aligned(idx_k, 4) ||
+      !aligned(idx_scale, 4) || !aligned(gate, 2) || !aligned(idx_gate, 2) || !aligned(idx_base, 8) ||
+      !aligned(idx_written, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (idx_written != nullptr && (rows_per_seq < 1 || rows_per_seq > 32 || rows->rows % rows_per_seq != 0))
+    return DSA_ERR_INVALID_ARG;
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  IndexerWriteFp8Params p{};
+  p.positions = rows->positions;
+  p.seq_lens = rows->seq_lens;
+  p.idx_base = idx_base;
+  p.k_raw = k_raw;
+  p.ln_w = ln_w;
+  p.ln_b = ln_b;
+  p.gate = gate;
+  p.idx_k = idx_k;
+  p.idx_scale = idx_scale;
+  p.idx_gate = idx_gate;
+  p.idx_written = idx_written;
+  p.idx_tokens = idx_tokens;
+  p.rows = rows->rows;
+  p.rows_per_seq = idx_written != nullptr ? rows_per_seq : 1;
+  p.dim = index_dim;
+  p.eps = eps;
+  p.err = dev->err;
+  return launched(launch_indexer_write_fp8(p, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_quantize_fp8(const void* x, int32_t x_fp32, int32_t rows, int32_t k,

@@ -78,6 +78,9 @@ struct IndexParams {
   uint64_t wait_ns;
   int32_t inputs_early;   // inputs complete before the kernel before started: only the
                           // score stores (and the exit) wait for it
+  const uint8_t* q_codes; // FP8 form: queries as codes (q_idx unused), else nullptr
+  const float* q_scale;   // [rows][heads]
+  const float* k_scale;   // [idx_tokens]
 };
 // Fills in direct / ctas / stages / tmem_cols / smem_bytes from the shape.
 void plan_index_scores(IndexParams& p, int num_sms);
@@ -135,6 +138,27 @@ struct IndexerWriteParams {
   int* err;
 };
 cudaError_t launch_indexer_write(const IndexerWriteParams& p, cudaStream_t stream);
+
+struct IndexerWriteFp8Params {
+  const uint32_t* positions;
+  const int32_t* seq_lens;
+  const int64_t* idx_base;
+  const uint16_t* k_raw;   // [rows][dim] bf16
+  const uint16_t* ln_w;    // [dim] bf16
+  const uint16_t* ln_b;    // [dim] bf16
+  const uint16_t* gate;    // [rows] bf16 or nullptr
+  uint8_t* idx_k;          // [idx_tokens][dim] E4M3
+  float* idx_scale;        // [idx_tokens]
+  uint16_t* idx_gate;      // [idx_tokens] bf16
+  int32_t* idx_written;    // [sequences] rows written per sequence, or nullptr
+  int64_t idx_tokens;
+  int32_t rows;
+  int32_t rows_per_seq;    // rows of one sequence, with idx_written (1 without)
+  int32_t dim;
+  float eps;
+  int* err;
+};
+cudaError_t launch_indexer_write_fp8(const IndexerWriteFp8Params& p, cudaStream_t stream);
 
 struct DenseMmParams {
   const uint16_t* a;      // [m][k] bf16 activations

@@ -37,10 +37,18 @@
 //              epilogue (one TMEM lane quarter each).
 // The arithmetic of every score is the same whichever CTA or segment
 // computes it, so a row's scores do not depend on the other rows.
+//
+// kFp8 is the same over an FP8 key cache (dsa_index_scores_fp8): keys and
+// queries are E4M3 codes with one FP32 scale a key and a (row, head),
+//     s_r(t) = gate(t) ks(t) * sum_h (w_r[h] qs_r[h]) * relu(q8_r[h] . k8(t))
+// (a scale is not negative, so it passes through the ReLU), whose products one
+// FP8 MMA forms exactly: half the key bytes and an eighth of the MMA time, the
+// query operand is copied, not split, and the scales ride on the head weights
+// and the gate.
 #include <climits>
 
-#include "dsa_device.cuh"
 #include "dsa_internal.h"
+#include "fp8_device.cuh"
 
 namespace dsa {
 namespace {
@@ -232,16 +240,40 @@ __device__ __forceinline__ long long scan_prefix(long long v, long long* scratch
   return (warp == 1 ? s0 : 0) + x - v;
 }
 
+// First query element of row r, as its type.
+template <bool kFp8, int D>
+__device__ __forceinline__ auto q_row(const IndexParams& p, int r) {
+  const int64_t at = static_cast<int64_t>(r) * p.heads * D;
+  if constexpr (kFp8) return p.q_codes + at;
+  else return p.q_idx + at;
+}
+
+// Descriptor of an FP8 operand, K-major with rows of D bytes: D = 128 as bf16's
+// sub-tiles, D = 64 in the 64-byte swizzle (8-row groups 512 B apart).
+template <int D>
+__device__ __forceinline__ uint64_t key_desc(uint32_t saddr) {
+  if constexpr (D == 128) return umma_desc_sw128_kmajor(saddr);
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(512 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;
+  return d;
+}
+
 // kDirect: a launch small enough for a few tiles per CTA in a single wave --
 // CTA (x, y) scores tiles [x*dt, x*dt + dt) of group y (dt = direct_tiles,
 // one stage each), needs no scan, and warp 0 loads the group's rows once,
 // issues the tiles' copies and posts their record itself.
-template <int D, bool kDirect>
+// kFp8: rows of an operand are D bytes (one 128-byte swizzle span, or for D = 64
+// one of 64 bytes) instead of D bf16 in 64-element sub-tiles.
+template <int D, bool kDirect, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     index_scores_kernel(const __grid_constant__ CUtensorMap kmap, const IndexParams p) {
-  constexpr int kSub = D / 64;                       // 64-element K sub-tiles per operand
-  constexpr uint32_t kStageBytes = kTileM * D * 2;   // one 128 x D bf16 key tile
-  constexpr int kKSteps = D / 16;
+  constexpr int kSub = kFp8 ? 1 : D / 64;            // K sub-tiles per operand (one copy each)
+  constexpr uint32_t kStageBytes = kTileM * D * (kFp8 ? 1 : 2);  // one 128 x D key tile
+  constexpr int kKSteps = D / (kFp8 ? 32 : 16);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -250,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---------------------------------------------------------------- layout
   const int npad = p.npad;
-  const uint32_t b_bytes = static_cast<uint32_t>(npad) * D * 2;  // one of hi / lo
+  const uint32_t b_bytes = static_cast<uint32_t>(npad) * D * (kFp8 ? 1 : 2);  // one of hi / lo
   uint8_t* stage_base = smem;
   uint8_t* b_hi = smem + p.stages * kStageBytes;
-  uint8_t* b_lo = b_hi + b_bytes;
+  uint8_t* b_lo = kFp8 ? b_hi : b_hi + b_bytes;
   float* w_s = reinterpret_cast<float*>(b_lo + b_bytes);
   IndexCtl* ctl = reinterpret_cast<IndexCtl*>(w_s + npad);
   const int stages = p.stages;
@@ -320,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if ((kDirect || groups == 1) && !inputs_early) {
     const GroupRows gr = group_rows(p, kDirect ? blockIdx.y : 0);
-    const float* qsrc = p.q_idx + static_cast<int64_t>(gr.r0) * p.heads * D;
-    for (int off = threadIdx.x * 32; off < gr.nrows * p.heads * D; off += kThreads * 32)
-      prefetch_l2(qsrc + off);
+    constexpr int kLine = kFp8 ? 128 : 32;  // elements of a 128-byte line
+    for (int off = threadIdx.x * kLine; off < gr.nrows * p.heads * D; off += kThreads * kLine)
+      prefetch_l2(q_row<kFp8, D>(p, gr.r0) + off);
     if (threadIdx.x < gr.nrows) prefetch_l2(p.seq_lens + gr.r0 + threadIdx.x);
   }
   // The barriers are initialised before any warp can arrive on or wait for
@@ -496,10 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = static_cast<int>(min(static_cast<long long>(tg - t0), remaining));
       // q rows and head weights of the segment into L2 for the epilogue's build.
       const int nreal = gr.nrows * p.heads;
-      const float* qsrc = p.q_idx + static_cast<int64_t>(gr.r0) * p.heads * D;
       if (k > 0) {  // segment 0's operand is being built already
-        for (int off = lane * 32; off < nreal * D; off += 32 * 32) prefetch_l2(qsrc + off);
-        if (lane * 32 < nreal) prefetch_l2(p.head_w + static_cast<int64_t>(gr.r0) * p.heads + lane * 32);
+        constexpr int kLine = kFp8 ? 128 : 32;
+        for (int off = lane * kLine; off < nreal * D; off += 32 * kLine)
+          prefetch_l2(q_row<kFp8, D>(p, gr.r0) + off);
+        if (lane * 32 < nreal) {
+          prefetch_l2(p.head_w + static_cast<int64_t>(gr.r0) * p.heads + lane * 32);
+          if constexpr (kFp8) prefetch_l2(p.q_scale + static_cast<int64_t>(gr.r0) * p.heads + lane * 32);
+        }
       }
       const int slot = k % kSegRing;
       int w_ok = 1;
@@ -556,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && my_tiles > 0) {
     // ============================================================ MMA issuer
     if (lane == 0) {
-      const uint32_t idesc = umma_idesc_bf16(kTileM, npad);
+      const uint32_t idesc = kFp8 ? fp8::idesc_e4m3(kTileM, npad) : umma_idesc_bf16(kTileM, npad);
       const uint32_t a0 = smem_u32(stage_base), bh = smem_u32(b_hi), bl = smem_u32(b_lo);
       long long done = 0;
       int i = 0;
@@ -580,8 +616,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + a * npad;
           const uint32_t a_stage = a0 + s * kStageBytes;
+          if constexpr (kFp8) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+            for (int kk = 0; kk < kKSteps; ++kk)
+              fp8::umma_e4m3(d_tmem, key_desc<D>(a_stage + kk * 32), key_desc<D>(bh + kk * 32), idesc, kk != 0);
+          }
+#pragma unroll
+          for (int half = 0; half < (kFp8 ? 0 : 2); ++half) {
             const uint32_t b_base = half ? bl : bh;
 #pragma unroll
             for (int kk = 0; kk < kKSteps; ++kk) {
@@ -610,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane_tok = quarter * 32 + lane;
     const int heads = p.heads;
     const int cols_per_row = (heads % 16 == 0) ? heads : npad;  // heads%16 != 0 -> one row
-    const int vec_per_row = D / 8;
+    const int vec_per_row = D / (kFp8 ? 16 : 8);
     const int nvec = npad * vec_per_row;
     constexpr int kBatch = 8;
     constexpr int kWPer = 256 / kEpiThreads;  // head-weight columns per thread (npad <= 256)
@@ -622,13 +663,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp's arrival on qready.
     auto build_q = [&](int r0, int nrows) {
       const int nreal = nrows * heads;
-      const float* qsrc = p.q_idx + static_cast<int64_t>(r0) * heads * D;
       float wv[kWPer];
 #pragma unroll
       for (int e = 0; e < kWPer; ++e) {
         const int col = et + e * kEpiThreads;
         wv[e] = col < nreal ? p.head_w[static_cast<int64_t>(r0) * heads + col] : 0.0f;
+        if constexpr (kFp8)
+          if (col < nreal) wv[e] *= p.q_scale[static_cast<int64_t>(r0) * heads + col];
       }
+      if constexpr (kFp8) {
+        // The codes as they are, 16 bytes a thread, into the swizzle of key_desc.
+        const uint4* src = reinterpret_cast<const uint4*>(q_row<kFp8, D>(p, r0));
+        for (int v0 = et; v0 < nvec; v0 += 4 * kEpiThreads) {
+          uint4 u[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int v = v0 + b * kEpiThreads;
+            u[b] = v < nvec && v / vec_per_row < nreal ? ld_dep_u4(src + v) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int v = v0 + b * kEpiThreads;
+            if (v >= nvec) break;
+            const int row = v / vec_per_row, chunk = v % vec_per_row;
+            const int place = D == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+            *reinterpret_cast<uint4*>(b_hi + row * D + place * 16) = u[b];
+          }
+        }
+      } else {
+      const float* qsrc = q_row<kFp8, D>(p, r0);
       for (int v0 = et; v0 < nvec; v0 += kBatch * kEpiThreads) {
         float4 u[kBatch][2];
 #pragma unroll
@@ -666,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(b_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(b_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+      }
       }
 #pragma unroll
       for (int e = 0; e < kWPer; ++e) {
@@ -725,16 +789,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // hides behind the TMA and the MMAs (plain loads: the gates may come
       // from the kernel before, which the wait at the top has ordered unless
       // the caller declared them complete before it).
+      // (kFp8: the key's scale likewise.)
       auto load_gate = [&](int j) {
         const int t = (t_first + j) * kTileM + lane_tok;
+        if constexpr (kFp8)
+          if (p.gate == nullptr) return static_cast<uint16_t>(0x3F80);  // 1
         return (j < n && t < max_len_group) ? p.gate[base + t] : static_cast<uint16_t>(0);
       };
+      auto load_scale = [&](int j) {
+        const int t = (t_first + j) * kTileM + lane_tok;
+        return (j < n && t < max_len_group) ? p.k_scale[base + t] : 0.0f;
+      };
       uint16_t g_next = load_gate(0);
+      float ks_next = 0.0f;
+      if constexpr (kFp8) ks_next = load_scale(0);
       for (int j = 0; j < n && ok; ++j, ++i) {
         const int a = i & 1;
         const int t = (t_first + j) * kTileM + lane_tok;
-        const float gt = __bfloat162float(__ushort_as_bfloat16(g_next));
+        float gt = __bfloat162float(__ushort_as_bfloat16(g_next));
         g_next = load_gate(j + 1);
+        if constexpr (kFp8) {
+          gt *= ks_next;
+          ks_next = load_scale(j + 1);
+        }
         int wok = 1;
         if (lane == 0) wok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, p.wait_ns) ? 1 : 0;
         wok = __shfl_sync(0xFFFFFFFFu, wok, 0);
@@ -815,8 +892,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 void plan_index_scores(IndexParams& p, int num_sms) {
-  const uint32_t stage_bytes = kTileM * p.dim * 2;
-  const uint32_t b_bytes = 2u * p.npad * p.dim * 2;
+  const bool is_fp8 = p.q_codes != nullptr;
+  const uint32_t stage_bytes = kTileM * p.dim * (is_fp8 ? 1 : 2);
+  const uint32_t b_bytes = static_cast<uint32_t>(p.npad) * p.dim * (is_fp8 ? 1 : 4);
   const uint32_t fixed = b_bytes + p.npad * 4 + sizeof(IndexCtl) + 1024;  // + alignment slack
   const uint32_t two_per_sm = 113u * 1024u, one_per_sm = 226u * 1024u;
   int stages = 0, per_sm = 1;
@@ -826,7 +904,8 @@ void plan_index_scores(IndexParams& p, int num_sms) {
   } else {
     stages = static_cast<int>((one_per_sm - fixed) / stage_bytes);
   }
-  stages = stages > 4 ? 4 : stages;
+  const int most = is_fp8 ? kMaxStages : 4;
+  stages = stages > most ? most : stages;
   if (stages < 1) stages = 1;
 
   // A launch whose tiles fit one wave even at the longest possible rows runs
@@ -855,8 +934,11 @@ cudaError_t launch_index_scores(const IndexParams& p, const CUtensorMap& kmap,
   if (groups <= 0 || p.max_len <= 0) return cudaSuccess;
   if (groups > INT_MAX / 2) return cudaErrorInvalidConfiguration;
   cudaError_t e;
-  auto kernel = p.direct ? (p.dim == 64 ? index_scores_kernel<64, true> : index_scores_kernel<128, true>)
-                        : (p.dim == 64 ? index_scores_kernel<64, false> : index_scores_kernel<128, false>);
+  auto kernel = p.direct ? (p.dim == 64 ? index_scores_kernel<64, true, false> : index_scores_kernel<128, true, false>)
+                        : (p.dim == 64 ? index_scores_kernel<64, false, false> : index_scores_kernel<128, false, false>);
+  if (p.q_codes != nullptr)
+    kernel = p.direct ? (p.dim == 64 ? index_scores_kernel<64, true, true> : index_scores_kernel<128, true, true>)
+                      : (p.dim == 64 ? index_scores_kernel<64, false, true> : index_scores_kernel<128, false, true>);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -84,6 +84,44 @@ def test_dense_mm_refusals(lib):
     assert f(*(good[:6] + [65535 * 128 + 1] + good[7:])) == UNSUPPORTED
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_blocks_per_seq", ctypes.c_int32),
+                ("bt_stride", ctypes.c_int32), ("block_size", ctypes.c_int32), ("rows", ctypes.c_int32)]
+
+
+def _all_refused(f, good, bads):
+    for at, v, want in bads:
+        args = list(good)
+        args[at] = v
+        assert f(*args) == want, (at, v)
+
+
+def test_indexer_write_refusals(lib):
+    f = _fn(lib, "dsa_indexer_write_fp8", "ppppfppppplipip")
+    rows = _Rows(X, None, X, None, 0, 0, 0, 6)
+    good = [ctypes.byref(rows), X, X, X, 1e-6, X, X, X, X, X, 1000, 128, X, 2, None]
+    _all_refused(f, good, [(i, None, INVALID) for i in (0, 1, 2, 3, 6, 7, 8, 9)]
+                 + [(4, -1.0, INVALID), (4, float("nan"), INVALID), (10, 0, INVALID), (13, 4, INVALID),
+                    (13, 0, INVALID), (13, 33, INVALID), (11, 96, UNSUPPORTED)]
+                 + [(1, X + 4, INVALID), (2, X + 2, INVALID), (7, X + 2, INVALID), (8, X + 1, INVALID),
+                    (6, X + 4, INVALID), (12, X + 2, INVALID)])
+    _all_refused(f, good, [(0, ctypes.byref(_Rows(None, None, X, None, 0, 0, 0, 6)), INVALID),
+                           (0, ctypes.byref(_Rows(X, None, X, None, 0, 0, 0, 0)), INVALID),
+                           (0, ctypes.byref(_Rows(X, None, X, None, 0, 0, 0, 65536)), UNSUPPORTED)])
+
+
+def test_index_scores_refusals(lib):
+    f = _fn(lib, "dsa_index_scores_fp8", "ppppppplpiiiippup")
+    rows = _Rows(None, None, X, None, 0, 0, 0, 6)
+    good = [ctypes.byref(rows), X, X, X, X, X, X, 1000, X, 32, 128, 2, 500, X, X, 0, None]
+    _all_refused(f, good, [(i, None, INVALID) for i in (0, 1, 2, 3, 4, 5, 8, 13)]
+                 + [(7, 0, INVALID), (11, 4, INVALID), (11, 0, INVALID), (12, -1, INVALID), (15, 2, INVALID),
+                    (9, 0, UNSUPPORTED), (9, 257, UNSUPPORTED), (10, 32, UNSUPPORTED), (7, 2 ** 31, UNSUPPORTED)]
+                 + [(1, X + 8, INVALID), (4, X + 8, INVALID), (5, X + 2, INVALID), (6, X + 1, INVALID)])
+    assert f(*(good[:12] + [0] + good[13:])) == OK                # no tokens: nothing to do
+
+
 def test_binding_refuses_host_tensors():
     from sparse_attention_mla_dsa_gb300 import api
     x = torch.zeros((2, 128), dtype=torch.bfloat16)
