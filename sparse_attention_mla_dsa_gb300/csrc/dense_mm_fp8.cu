@@ -266,19 +266,28 @@ __global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
       for (int c = 0; c < kRows; ++c) part[c * kTileN + row_n] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
     }
     fp8::cluster_sync();
-    // Output (row, column) pairs shared out among the cluster's epilogue threads.
-    const int rows_here = min(kRows, p.m - m0);
-    if (warp >= 2 && n0 + et < p.n) {
-      for (int c = split; c < rows_here; c += p.splits) {
-        const uint32_t at = smem_u32(part + c * kTileN + et);
-        float v[kMaxSplits];
+    // The sums of the ranges, four columns and a row a thread, the rows shared out
+    // among the cluster's warps.
+    const int rows_here = min(kRows, p.m - m0), n = n0 + lane * 4;
+    if (warp >= 2 && n < p.n) {
+      for (int c = split * (kEpiThreads / 32) + warp - 2; c < rows_here; c += p.splits * (kEpiThreads / 32)) {
+        float4 v[kMaxSplits];
 #pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r) v[r] = r < p.splits ? fp8::ld_cluster_f32(at, r) : 0.0f;
-        float sum = v[0];
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < p.splits) v[r] = fp8::ld_cluster_f4(part + c * kTileN + lane * 4, r);
+        float4 sum = v[0];
 #pragma unroll
         for (int r = 1; r < kMaxSplits; ++r)
-          if (r < p.splits) sum += v[r];
-        store_c(p, m0 + c, n0 + et, sum);
+          if (r < p.splits) {
+            sum.x += v[r].x;
+            sum.y += v[r].y;
+            sum.z += v[r].z;
+            sum.w += v[r].w;
+          }
+        store_c(p, m0 + c, n, sum.x);
+        if (n + 1 < p.n) store_c(p, m0 + c, n + 1, sum.y);
+        if (n + 2 < p.n) store_c(p, m0 + c, n + 2, sum.z);
+        if (n + 3 < p.n) store_c(p, m0 + c, n + 3, sum.w);
       }
     }
     fp8::cluster_sync();  // nobody reads this CTA's shared memory any more
@@ -287,6 +296,419 @@ __global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
+}
+
+// ------------------------------------------------------------------ many rows
+// Tiles of 256 activation rows x 256 weight rows for a pair of CTAs (a cluster of
+// two, cta_group::2): CTA r multiplies rows 128 r .. 128 r + 127 of the tile by all
+// 256 weight rows, of which it copies half, so 32 KB a CTA and block of k feed the
+// tensor core for 544 clocks; a CTA by itself would need 48.  Activation rows are M:
+//   A = 128 rows of each CTA x 128 of k,  B = 2 x 64 weight rows of each CTA x 128 of k
+//   D = 128 x 128 FP32 in each CTA's TMEM (lane = row, column = weight row) for either
+//       half of the weight rows, two of each in turn
+// so a thread of the epilogue has one row and columns of one row of weight scales:
+// one factor a block of k.
+//
+// What bounds it is how soon an accumulator is read, scaled and free again.  By
+// halves the MMAs of three others, not of one, run meanwhile; and sixteen warps of 64
+// columns each hide the loads' latency that eight of 128 do not (1,024 x 4,096 x
+// 32,768: 121 us with eight).  The activation scales come through shared memory,
+// turned there by two warps: a load by the epilogue would touch a line for each row.
+// The outputs leave through shared memory by TMA, behind the next tile's MMAs.
+//
+// Persistent: one pair for every two SMs, tiles in turn.  Roles (640 threads a CTA):
+// warp 0 copies, warp 1 of the leader issues both CTAs' MMAs, warps 2-3 fetch the
+// scales, warps 4-19 are the epilogue (a TMEM lane quarter and 64 columns each) and
+// get the registers that the first four give up.
+namespace pair {
+
+constexpr int kTile = 256;
+constexpr int kThreads = 384;
+constexpr int kFirstEpiWarp = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kCols = 128;                        // columns of an epilogue warp
+constexpr int kFewRegs = 72, kManyRegs = 216;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register split");
+constexpr int kStages = 4;
+constexpr uint32_t kOperandBytes = 128 * kBlock;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kOutBytes = 32 * 128;          // 32 rows x 128 bytes of the output, two of them a warp
+constexpr int kScaleBlocks = 16;                  // blocks of k whose scales are fetched together
+constexpr int kScalePitch = 130;                  // floats between their rows
+constexpr uint32_t kTmemCols = 512;
+constexpr int kGroupTiles = 16;                   // row tiles that share a sweep of the weight
+
+struct __align__(8) Ctl {
+  uint64_t full[kStages];    // leader's: both CTAs' copies of a stage
+  uint64_t empty[kStages];
+  uint64_t tfull[4];         // [block of k % 2][half]
+  uint64_t tempty[4];        // leader's
+  uint64_t sfull[2];
+  uint64_t sempty[2];
+  uint64_t drain;
+  uint64_t never;
+  uint32_t tmem_base;
+  int abort_flag;
+  float sb[2][2][kScaleBlocks];                 // weight scales of the two halves
+  float sa[2][kScaleBlocks * kScalePitch];      // this CTA's rows' scales, [block][row]
+};
+constexpr uint32_t kCtlOff = kStages * kStageBytes + kEpiWarps * 2 * kOutBytes;
+constexpr uint32_t kSmemBytes = kCtlOff + sizeof(Ctl) + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024 && kCtlOff % 8 == 0, "shared memory budget");
+
+__device__ __forceinline__ bool aborted(Ctl* c) { return *reinterpret_cast<volatile int*>(&c->abort_flag) != 0; }
+// Bounded wait of one thread; a timeout is recorded and marks both CTAs, whose
+// later waits are skipped.  (All of it inline: around a call the accumulators'
+// registers could not stay where they are.)
+__device__ __forceinline__ bool wait(Ctl* c, uint64_t* bar, uint32_t parity, const Fp8MmParams& p) {
+  if (p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1; i < (1u << 30) && !aborted(c); ++i) {
+    if (mbar_try_wait_hint(bar, parity, p.wait_ns < kShortWaitNs ? 32 : kSuspendHintNs)) return true;
+    if (((i & 15u) == 0 || p.wait_ns < kShortWaitNs) && global_ns() - t0 > p.wait_ns) break;
+  }
+  if (!aborted(c)) record_error(p.err, DSA_DEVERR_TIMEOUT, -1);
+  for (uint32_t r = 0; r < 2; ++r)
+    asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(fp8::map_to(&c->abort_flag, r)), "r"(1) : "memory");
+  return false;
+}
+// Which of three phases are complete (bits 0-2).  A look at a barrier takes ~140
+// clocks beside the epilogue's warps; three in a row, and not one after the other's
+// answer, leave the issuing thread time for the MMAs.
+__device__ __forceinline__ uint32_t look3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint64_t* b2, uint32_t p12) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t.reg .b32 x, y, z;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %5;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%4], %5;\n\t"
+      "selp.b32 x, 1, 0, p;\n\tselp.b32 y, 2, 0, q;\n\tselp.b32 z, 4, 0, r;\n\t"
+      "or.b32 x, x, y;\n\tor.b32 %0, x, z;\n\t}"
+      : "=r"(r)
+      : "r"(smem_u32(b0)), "r"(p0), "r"(smem_u32(b1)), "r"(smem_u32(b2)), "r"(p12)
+      : "memory");
+  return r;
+}
+// The same for a whole warp: every lane polls, one goes on where it is not there yet.
+__device__ __forceinline__ bool wait_warp(Ctl* c, uint64_t* bar, uint32_t parity, int lane, const Fp8MmParams& p) {
+  const bool done = p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
+  if (__all_sync(0xFFFFFFFFu, done)) return true;
+  int ok = 1;
+  if (lane == 0) ok = wait(c, bar, parity, p) ? 1 : 0;
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+// A box into this CTA's shared memory, its bytes counted on the leader's barrier.
+__device__ __forceinline__ void copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Operands by the low words of their descriptors, which alone differ between MMAs
+// (in 16-byte units): an add for each, nothing else.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(acc), "n"(kDescHigh), "n"(fp8::idesc_e4m3(256, kTile / 2))
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued so far is complete.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t out;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
+  return out;
+}
+
+// Tile `t`'s first row and column: groups of kGroupTiles row tiles sweep the
+// weight together, so that both stay in L2 however many rows there are.
+struct Place {
+  int m, n;
+};
+__device__ __forceinline__ Place place(const Fp8MmParams& p, int t) {
+  const int mt = (p.m + kTile - 1) / kTile, nt = (p.n + kTile - 1) / kTile;
+  const int group = t / (kGroupTiles * nt), first = group * kGroupTiles;
+  const int wide = min(kGroupTiles, mt - first), at = t - group * kGroupTiles * nt;
+  return {(first + at % wide) * kTile, at / wide * kTile};
+}
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    fp8_mm_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                       const __grid_constant__ CUtensorMap cmap, const Fp8MmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  // (Both CTAs' shared memory starts at the same address, so that the leader's
+  // descriptors are right in the other CTA too.)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kCtlOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = fp8::cluster_rank();
+  const int tiles = ((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile);
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  grid_dep_launch();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&ctl->tfull[s], 1);
+      mbar_init(&ctl->tempty[s], kEpiWarps);  // half of the warps of both CTAs
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->sfull[s], 2);
+      mbar_init(&ctl->sempty[s], kEpiWarps);
+    }
+    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->never, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&wmap);
+    tma_prefetch_map(&amap);
+    tma_prefetch_map(&cmap);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  fp8::cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  grid_dep_wait();
+
+  if (warp < kFirstEpiWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      if (elect_one()) {
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+          const Place at = place(p, t);
+          for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+            const uint32_t s = i % kStages;
+            if (i >= kStages && !(ok = wait(ctl, &ctl->empty[s], (i / kStages - 1) & 1, p))) break;
+            const uint32_t dst = smem_u32(smem) + s * kStageBytes, bar = fp8::map_to(&ctl->full[s], 0);
+            // (The phase ends with this arrival at the earliest, so the other CTA's
+            // bytes may come before they are expected.)
+            if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * kStageBytes);
+            copy(dst, &amap, bar, kb * kBlock, at.m + static_cast<int>(rank) * 128);
+            copy(dst + kOperandBytes, &wmap, bar, kb * kBlock, at.n + static_cast<int>(rank) * 64);
+            copy(dst + kOperandBytes + kOperandBytes / 2, &wmap, bar, kb * kBlock,
+                 at.n + 128 + static_cast<int>(rank) * 64);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMAs
+      if (rank == 0 && elect_one()) {
+        const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += step) {
+          for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
+            const uint32_t s = i % kStages;
+            const uint32_t full_at = (i / kStages) & 1, empty_at = ((i >> 1) - 1) & 1;  // (i < 2: the phase before the first)
+            const uint32_t there =
+                look3(&ctl->full[s], full_at, &ctl->tempty[(i & 1) * 2], &ctl->tempty[(i & 1) * 2 + 1], empty_at);
+            ok = (there & 1) != 0 || wait(ctl, &ctl->full[s], full_at, p);
+            const uint32_t a = desc0 + s * (kStageBytes >> 4);
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+              const uint32_t d = (i & 1) * 2 + h;
+              ok = ok && ((there >> (1 + h) & 1) != 0 || wait(ctl, &ctl->tempty[d], empty_at, p));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kBlock / 32; ++kk)
+                mma(tmem + d * 128, a + kk * 2, a + ((kOperandBytes + h * (kOperandBytes / 2)) >> 4) + kk * 2, kk != 0);
+              if (h == 1) commit(&ctl->empty[s]);
+              commit(&ctl->tfull[d]);
+            }
+            if (!ok) break;
+          }
+        }
+        // Every MMA is complete before tensor memory is released.
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl->drain))
+            : "memory");
+        mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+      }
+    } else {
+      // ------------------------------------------------------------ scales
+      // 64 of the CTA's rows each, two rows x 16 blocks a load.
+      const int half = warp - 2, kb_in = lane & (kScaleBlocks - 1), odd = lane >> 4;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Place at = place(p, t);
+        // (Rows and columns outside the output are multiplied by scales of others.)
+        const int row0 = at.m + static_cast<int>(rank) * 128 + half * 64;
+        const float* sb = p.b_scale + static_cast<int64_t>(min(at.n / 128 + half, (p.n - 1) / 128)) * p.kblocks;
+        for (int kb0 = 0; kb0 < p.kblocks; kb0 += kScaleBlocks, ++g) {
+          if (g >= 2 && !(ok = wait_warp(ctl, &ctl->sempty[g & 1], (g / 2 - 1) & 1, lane, p))) break;
+          const int kb = min(kb0 + kb_in, p.kblocks - 1);
+          float* dst = ctl->sa[g & 1] + kb_in * kScalePitch + half * 64 + odd;
+#pragma unroll 1
+          for (int r = 0; r < 64; r += 16) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              v[u] = p.a_scale[static_cast<int64_t>(min(row0 + odd + r + 2 * u, p.m - 1)) * p.kblocks + kb];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dst[r + 2 * u] = v[u];
+          }
+          if (lane < kScaleBlocks) ctl->sb[g & 1][half][lane] = sb[kb];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->sfull[g & 1]);
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
+    uint8_t* outs = smem + kStages * kStageBytes + (warp - kFirstEpiWarp) * 2 * kOutBytes;
+    const uint32_t tempty = fp8::map_to(&ctl->tempty[half], 0);  // and 16 bytes on
+    const bool by_tma = (static_cast<int64_t>(p.n) * (p.c_fp32 ? 4 : 2)) % 16 == 0;
+    uint32_t i = 0, g = 0;
+    // (After a wait that gave up the warps go on, with waits that no longer wait, and
+    // store nothing.)
+    for (int t = first; t < tiles; t += step) {
+      float acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+      for (int kb0 = 0; kb0 < p.kblocks; kb0 += kScaleBlocks, ++g) {
+        wait_warp(ctl, &ctl->sfull[g & 1], (g / 2) & 1, lane, p);
+        const float* sa = ctl->sa[g & 1] + quarter * 32 + lane;
+        const float* sb = ctl->sb[g & 1][half];
+        const int n = min(kScaleBlocks, p.kblocks - kb0);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++i) {
+          const uint32_t d = i & 1;
+          const float f = sa[j * kScalePitch] * sb[j];
+          wait_warp(ctl, &ctl->tfull[2 * d + half], (i >> 1) & 1, lane, p);
+          tc_fence_after();
+          const uint32_t src = src0 + d * kTile;
+          uint32_t v[2][32];
+          fp8::tmem_issue32(src, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            fp8::tmem_wait32(v[c & 1]);
+            if (c < 3) {
+              fp8::tmem_issue32(src + (c + 1) * 32, v[(c + 1) & 1]);
+            } else {  // read: the accumulator is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0)
+                asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(tempty + d * 16) : "memory");
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[c * 32 + e] = fmaf(__uint_as_float(v[c & 1][e]), f, acc[c * 32 + e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->sempty[g & 1]);
+      }
+      if (__any_sync(0xFFFFFFFFu, aborted(ctl))) break;
+      const Place at = place(p, t);
+      const int row0 = at.m + static_cast<int>(rank) * 128 + quarter * 32, col0 = at.n + half * kCols;
+      const int cols = p.n - col0;  // of this warp's in the output
+      if (row0 >= p.m || cols <= 0) continue;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) {
+        if (by_tma && !p.c_fp32 && (c & 32) != 0) continue;  // (64 columns at a time)
+        uint8_t* out = outs + ((by_tma && !p.c_fp32 ? c / 64 : c / 32) & 1) * kOutBytes;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        if (by_tma) {
+          // 128 bytes of each row (64 bf16 columns or 32 FP32 ones), in the 128-byte
+          // swizzle; what lies outside the output is not stored.
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint4 w;
+            if (p.c_fp32) {
+              const int b = c + e * 4;
+              w = make_uint4(__float_as_uint(acc[b]), __float_as_uint(acc[b + 1]), __float_as_uint(acc[b + 2]),
+                             __float_as_uint(acc[b + 3]));
+            } else {
+              const int b = (c & 64) + e * 8;
+              w = make_uint4(bf16x2(acc[b], acc[b + 1]), bf16x2(acc[b + 2], acc[b + 3]),
+                             bf16x2(acc[b + 4], acc[b + 5]), bf16x2(acc[b + 6], acc[b + 7]));
+            }
+            *reinterpret_cast<uint4*>(out + lane * 128 + ((e ^ (lane & 7)) * 16)) = w;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&cmap)),
+                "r"(col0 + c), "r"(row0), "r"(smem_u32(out))
+                : "memory");
+        } else {
+          // Rows that are not multiples of 16 bytes: turned in shared memory, so that
+          // neighbouring lanes store neighbouring columns.
+          float* turn = reinterpret_cast<float*>(out);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) turn[lane * 32 + (e ^ lane)] = acc[c + e];
+          __syncwarp();
+          if (c + lane < cols)
+            for (int r = 0; r < min(32, p.m - row0); ++r) store_c(p, row0 + r, col0 + c + lane, turn[r * 32 + (lane ^ r)]);
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are complete
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // After a wait that gave up, copies of this CTA may be in flight that no barrier
+  // accounts for: half a second is far more than they take.
+  if (threadIdx.x == 0 && aborted(ctl)) mbar_wait(&ctl->never, 0, kDrainWaitNs);
+  fp8::cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+}  // namespace pair
+
+cudaError_t launch_pairs(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
+                         const CUtensorMap& cmap, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(pair::fp8_mm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(pair::kSmemBytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * p.pairs), 1, 1);
+  cfg.blockDim = dim3(pair::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = pair::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pair::fp8_mm_pair_kernel, wmap, amap, cmap, p);
 }
 
 template <int kRows>
@@ -317,7 +739,16 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   p.kblocks = (p.k + kBlock - 1) / kBlock;
-  p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : p.m <= 64 ? 64 : 128;
+  const int64_t pair_tiles = static_cast<int64_t>((p.m + pair::kTile - 1) / pair::kTile) *
+                             ((p.n + pair::kTile - 1) / pair::kTile);
+  p.pairs = 0;
+  if (p.m > 64 && (pair_tiles * 4 >= num_sms)) {
+    p.row_tile = 128;
+    p.splits = 1;
+    p.pairs = static_cast<int32_t>(pair_tiles < num_sms / 2 ? pair_tiles : num_sms / 2);
+    return;
+  }
+  p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
   // k is split only where the tiles alone leave SMs idle, with two blocks of it
   // a CTA at least.  Up to 64 rows the split must not depend on m.
   const int64_t tiles = static_cast<int64_t>((p.n + kTileN - 1) / kTileN) * ((p.m + p.row_tile - 1) / p.row_tile);
@@ -330,7 +761,8 @@ void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
 }
 
 cudaError_t launch_fp8_mm(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
-                          cudaStream_t stream) {
+                          const CUtensorMap& cmap, cudaStream_t stream) {
+  if (p.pairs > 0) return launch_pairs(p, wmap, amap, cmap, stream);
   switch (p.row_tile) {
     case 16: return launch_rows<16>(p, wmap, amap, stream);
     case 32: return launch_rows<32>(p, wmap, amap, stream);

@@ -631,10 +631,21 @@ dsa_status dsa_dense_mm_fp8(const uint8_t* a, const float* a_scale, const uint8_
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  CUresult cr = map(&wmap, b, n_out, 128);
+  CUresult cr = map(&wmap, b, n_out, p.pairs > 0 ? 64 : 128);
   if (cr == CUDA_SUCCESS) cr = map(&amap, a, m_rows, p.row_tile);
+  CUtensorMap cmap = amap;  // (not used)
+  const int32_t c_bytes = c_fp32 ? 4 : 2;
+  if (cr == CUDA_SUCCESS && p.pairs > 0 && static_cast<int64_t>(n_out) * c_bytes % 16 == 0) {
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(n_out), static_cast<cuuint64_t>(m_rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(n_out) * c_bytes};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / c_bytes), 32};
+    const cuuint32_t estride[2] = {1, 1};
+    cr = encode(&cmap, c_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c, dim,
+                stride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
   if (cr != CUDA_SUCCESS) return DSA_ERR_INVALID_ARG;
-  return launched(launch_fp8_mm(p, wmap, amap, static_cast<cudaStream_t>(stream)));
+  return launched(launch_fp8_mm(p, wmap, amap, cmap, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_plan_rows(const dsa_plan* plan, void* stream) {
