@@ -377,18 +377,53 @@ def _table(t: torch.Tensor, rows: int, name: str) -> tuple[int, int, int]:
     return t.data_ptr(), t.shape[1], t.stride(0) if rows > 1 else t.shape[1]
 
 
-def _here(tensors: dict) -> None:
-    """Every tensor given is on the current device."""
-    _current(_on_device(tensors))
+_U8, _F32, _I32, _I64 = (torch.uint8,), (torch.float32,), (torch.int32,), (torch.int64,)
+_current_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _value_type(t: torch.Tensor, name: str) -> int:
-    """1 for FP32, 0 for bf16 (as bfloat16 or its bits)."""
-    if t.dtype is torch.float32:
-        return 1
-    if t.dtype not in _BITS16:
-        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
-    return 0
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The current device, which is t's."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if device != _current_index():
+        raise ValueError(f"{name}: on cuda:{device}, the current device is cuda:{_current_index()}")
+    return device
+
+
+def _take(t: torch.Tensor, types: tuple, shape: tuple, device: int, name: str) -> int:
+    """Pointer of a contiguous tensor of one of some types, a shape and a device
+    (every check of an argument in one pass: a small call waits for them)."""
+    if t.dtype not in types:
+        raise ValueError(f"{name}: expected {types[-1]}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _take_or_none(t, types: tuple, shape: tuple, device: int, name: str) -> int | None:
+    return None if t is None else _take(t, types, shape, device, name)
+
+
+def _counts(idx_written, rows: int, rows_per_seq: int, device: int) -> int | None:
+    """idx_written, one count a sequence (a bad rows_per_seq is the library's to refuse)."""
+    if idx_written is None:
+        return None
+    shape = (rows // rows_per_seq,) if rows_per_seq > 0 else idx_written.shape
+    return _take(idx_written, _I32, shape, device, "idx_written")
+
+
+def _stream_on(stream, device: int) -> int | None:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
+_VALUES = _BITS16 + (torch.float32,)
 
 
 def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -397,20 +432,23 @@ def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     bf16 or float32.  ``block_rows`` 1: a scale for each 128 of k of a row, scales
     [..., ceil(k / 128)] (or [...] where that is 1).  128 (x [rows, k]): for each 128
     x 128, scales [ceil(rows / 128), ceil(k / 128)]."""
-    _here(dict(x=x, codes=codes, scales=scales))
-    fp32 = _value_type(x, "x")
-    if x.dim() < 1 or (block_rows != 1 and x.dim() != 2):
-        raise ValueError(f"x: unexpected shape {tuple(x.shape)}")
-    k, kb = x.shape[-1], (x.shape[-1] + 127) // 128
-    _shaped(codes, tuple(x.shape), "codes")
+    shape, device = x.shape, _device_of(x, "x")
+    if len(shape) < 1 or (block_rows != 1 and len(shape) != 2):
+        raise ValueError(f"x: unexpected shape {tuple(shape)}")
+    k = shape[-1]
+    kb = (k + 127) // 128
     if block_rows != 1:
-        _shaped(scales, ((x.shape[0] + block_rows - 1) // block_rows, kb), "scales")
-    elif kb != 1 or tuple(scales.shape) != tuple(x.shape[:-1]):
-        _shaped(scales, tuple(x.shape[:-1]) + (kb,), "scales")
-    st = load().dsa_quantize_fp8(_ptr(x, None, "x"), fp32, x.numel() // max(k, 1), k, int(block_rows),
-                                 _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.float32, "scales"),
-                                 _stream(stream))
-    _check("dsa_quantize_fp8", st)
+        want = ((shape[0] + block_rows - 1) // block_rows, kb)
+    else:
+        want = shape[:-1] + (kb,)
+        if kb == 1 and scales.dim() == len(shape) - 1:
+            want = shape[:-1]
+    rows = x.numel() // k if k else 0
+    st = load().dsa_quantize_fp8(_take(x, _VALUES, shape, device, "x"), x.dtype is torch.float32, rows, k,
+                                 block_rows, _take(codes, _U8, shape, device, "codes"),
+                                 _take(scales, _F32, want, device, "scales"), _stream_on(stream, device))
+    if st:
+        raise DsaError("dsa_quantize_fp8", st)
 
 
 def dsa_dense_mm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
@@ -418,18 +456,17 @@ def dsa_dense_mm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
     """c[m][n] = sum_k (a[m][k] a_scale[m][k / 128]) (b[n][k] b_scale[n / 128][k / 128]):
     E4M3 codes (uint8) a [M, K] and weight b [N, K], float32 scales [M, ceil(K / 128)]
     and [ceil(N / 128), ceil(K / 128)], c [M, N] bf16 or float32."""
-    _here(dict(a=a, a_scale=a_scale, b=b, b_scale=b_scale, c=c))
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+    if a.dim() != 2 or b.dim() != 2:
         raise ValueError(f"shapes a {tuple(a.shape)}, b {tuple(b.shape)}")
-    (m, k), n = a.shape, b.shape[0]
+    (m, k), n, device = a.shape, b.shape[0], _device_of(a, "a")
     kb = (k + 127) // 128
-    _shaped(a_scale, (m, kb), "a_scale")
-    _shaped(b_scale, ((n + 127) // 128, kb), "b_scale")
-    _shaped(c, (m, n), "c")
-    st = load().dsa_dense_mm_fp8(_ptr(a, torch.uint8, "a"), _ptr(a_scale, torch.float32, "a_scale"),
-                                 _ptr(b, torch.uint8, "b"), _ptr(b_scale, torch.float32, "b_scale"),
-                                 _ptr(c, None, "c"), m, n, k, _value_type(c, "c"), _stream(stream))
-    _check("dsa_dense_mm_fp8", st)
+    st = load().dsa_dense_mm_fp8(_take(a, _U8, (m, k), device, "a"), _take(a_scale, _F32, (m, kb), device, "a_scale"),
+                                 _take(b, _U8, (n, k), device, "b"),
+                                 _take(b_scale, _F32, ((n + 127) // 128, kb), device, "b_scale"),
+                                 _take(c, _VALUES, (m, n), device, "c"), m, n, k, c.dtype is torch.float32,
+                                 _stream_on(stream, device))
+    if st:
+        raise DsaError("dsa_dense_mm_fp8", st)
 
 
 def dsa_indexer_write_fp8(rows: Rows, k_raw: torch.Tensor, ln_w: torch.Tensor, ln_b: torch.Tensor,
@@ -440,31 +477,21 @@ def dsa_indexer_write_fp8(rows: Rows, k_raw: torch.Tensor, ln_w: torch.Tensor, l
     """dsa_indexer_write into an FP8 key cache: LayerNorm (with bias) of k_raw [R, D]
     bf16, stored as E4M3 codes into idx_k [T, D] uint8 at row idx_base[r] +
     positions[r] with its power-of-two scale in idx_scale [T] float32."""
-    _here(dict(k_raw=k_raw, ln_w=ln_w, ln_b=ln_b, idx_base=idx_base, idx_k=idx_k, idx_scale=idx_scale,
-               idx_gate=idx_gate, gate=gate, idx_written=idx_written))
-    R = rows.rows
     if idx_k.dim() != 2:
         raise ValueError(f"idx_k: expected two dimensions, got {tuple(idx_k.shape)}")
-    T, D = idx_k.shape
-    _shaped(k_raw, (R, D), "k_raw")
-    _shaped(ln_w, (D,), "ln_w")
-    _shaped(ln_b, (D,), "ln_b")
-    _shaped(idx_base, (R,), "idx_base")
-    _shaped(idx_scale, (T,), "idx_scale")
-    _shaped(idx_gate, (T,), "idx_gate")
-    _shaped(gate, (R,), "gate")
-    if idx_written is not None and rows_per_seq > 0:
-        _shaped(idx_written, (R // rows_per_seq,), "idx_written")
-    st = load().dsa_indexer_write_fp8(ctypes.byref(rows), _ptr(k_raw, torch.uint16, "k_raw"),
-                                      _ptr(ln_w, torch.uint16, "ln_w"), _ptr(ln_b, torch.uint16, "ln_b"),
-                                      float(eps), _ptr(gate, torch.uint16, "gate"),
-                                      _ptr(idx_base, torch.int64, "idx_base"),
-                                      _ptr(idx_k, torch.uint8, "idx_k"),
-                                      _ptr(idx_scale, torch.float32, "idx_scale"),
-                                      _ptr(idx_gate, torch.uint16, "idx_gate"), T, D,
-                                      _ptr(idx_written, torch.int32, "idx_written"), int(rows_per_seq),
-                                      _stream(stream))
-    _check("dsa_indexer_write_fp8", st)
+    R, (T, D), device = rows.rows, idx_k.shape, _device_of(idx_k, "idx_k")
+    st = load().dsa_indexer_write_fp8(ctypes.byref(rows), _take(k_raw, _BITS16, (R, D), device, "k_raw"),
+                                      _take(ln_w, _BITS16, (D,), device, "ln_w"),
+                                      _take(ln_b, _BITS16, (D,), device, "ln_b"), eps,
+                                      _take_or_none(gate, _BITS16, (R,), device, "gate"),
+                                      _take(idx_base, _I64, (R,), device, "idx_base"),
+                                      _take(idx_k, _U8, (T, D), device, "idx_k"),
+                                      _take(idx_scale, _F32, (T,), device, "idx_scale"),
+                                      _take_or_none(idx_gate, _BITS16, (T,), device, "idx_gate"), T, D,
+                                      _counts(idx_written, R, rows_per_seq, device),
+                                      rows_per_seq, _stream_on(stream, device))
+    if st:
+        raise DsaError("dsa_indexer_write_fp8", st)
 
 
 def dsa_index_scores_fp8(rows: Rows, q: torch.Tensor, q_scale: torch.Tensor, head_w: torch.Tensor,
@@ -476,31 +503,22 @@ def dsa_index_scores_fp8(rows: Rows, q: torch.Tensor, q_scale: torch.Tensor, hea
     q_scale [R, H] float32 (dsa_quantize_fp8), keys idx_k [T, D] uint8 with idx_scale
     [T] float32 (dsa_indexer_write_fp8), idx_gate [T] bf16 or None for 1, scores
     [R, max_len] float32.  ``idx_written``, ``inputs_early``: as dsa_index_scores."""
-    _here(dict(q=q, q_scale=q_scale, head_w=head_w, idx_k=idx_k, idx_scale=idx_scale, idx_gate=idx_gate,
-               idx_base=idx_base, scores=scores, idx_written=idx_written))
-    R = rows.rows
-    if q.dim() != 3 or idx_k.dim() != 2 or q.shape[0] != R or q.shape[2] != idx_k.shape[1]:
-        raise ValueError(f"shapes q {tuple(q.shape)}, idx_k {tuple(idx_k.shape)}, rows {R}")
-    heads, dim, T = q.shape[1], q.shape[2], idx_k.shape[0]
-    _shaped(q_scale, (R, heads), "q_scale")
-    _shaped(head_w, (R, heads), "head_w")
-    _shaped(idx_scale, (T,), "idx_scale")
-    _shaped(idx_gate, (T,), "idx_gate")
-    _shaped(idx_base, (R,), "idx_base")
-    _shaped(scores, (R, int(max_len)), "scores")
-    if idx_written is not None and rows_per_seq > 0:
-        _shaped(idx_written, (R // rows_per_seq,), "idx_written")
-    st = load().dsa_index_scores_fp8(ctypes.byref(rows), _ptr(q, torch.uint8, "q"),
-                                     _ptr(q_scale, torch.float32, "q_scale"),
-                                     _ptr(head_w, torch.float32, "head_w"), _ptr(idx_k, torch.uint8, "idx_k"),
-                                     _ptr(idx_scale, torch.float32, "idx_scale"),
-                                     _ptr(idx_gate, torch.uint16, "idx_gate"), T,
-                                     _ptr(idx_base, torch.int64, "idx_base"), heads, dim, int(rows_per_seq),
-                                     int(max_len), _ptr(scores, torch.float32, "scores"),
-                                     _ptr(idx_written, torch.int32, "idx_written"),
+    if q.dim() != 3 or idx_k.dim() != 2:
+        raise ValueError(f"shapes q {tuple(q.shape)}, idx_k {tuple(idx_k.shape)}")
+    R, heads, (T, dim), device = rows.rows, q.shape[1], idx_k.shape, _device_of(idx_k, "idx_k")
+    st = load().dsa_index_scores_fp8(ctypes.byref(rows), _take(q, _U8, (R, heads, dim), device, "q"),
+                                     _take(q_scale, _F32, (R, heads), device, "q_scale"),
+                                     _take(head_w, _F32, (R, heads), device, "head_w"),
+                                     _take(idx_k, _U8, (T, dim), device, "idx_k"),
+                                     _take(idx_scale, _F32, (T,), device, "idx_scale"),
+                                     _take_or_none(idx_gate, _BITS16, (T,), device, "idx_gate"), T,
+                                     _take(idx_base, _I64, (R,), device, "idx_base"), heads, dim, rows_per_seq,
+                                     max_len, _take(scores, _F32, (R, max_len), device, "scores"),
+                                     _counts(idx_written, R, rows_per_seq, device),
                                      DSA_INDEX_INPUTS_BEFORE_PREDECESSOR if inputs_early else 0,
-                                     _stream(stream))
-    _check("dsa_index_scores_fp8", st)
+                                     _stream_on(stream, device))
+    if st:
+        raise DsaError("dsa_index_scores_fp8", st)
 
 
 _BITS32 = (torch.int32, torch.uint32)
