@@ -104,7 +104,9 @@ void set_index_rows(IndexParams& p, const DeviceInfo& dev, const dsa_rows& rows,
   // sequence run side by side and share the key tiles through L2); a head
   // count that is not a multiple of 16 runs one row per launch group so that
   // no 16-column TMEM load straddles two rows.
-  int sub = 64 / index_heads;
+  // FP8 keys take two sets of epilogue warps and half the bytes a key, so groups of
+  // 128 columns.
+  int sub = (p.q_codes != nullptr ? 128 : 64) / index_heads;
   if (index_heads % 16 != 0) sub = 1;
   sub = sub < 1 ? 1 : (sub > 32 ? 32 : sub);
   if (sub > rows_per_seq) sub = rows_per_seq;

@@ -28,13 +28,14 @@
 // segment boundary.  CTAs that score the same tiles for different groups of
 // one sequence run concurrently and share the key tiles through L2.
 //
-// CTA roles (192 threads):
+// CTA roles (192 threads, with FP8 keys 320):
 //   warp 0     walks the CTA's segments (row lengths checked per segment,
 //              one record per segment in a small ring) and issues the key
 //              TMA loads (lane 0);
 //   warp 1     owns TMEM and issues the MMAs (lane 0);
 //   warps 2-5  build each segment's q operand and head weights, then run the
-//              epilogue (one TMEM lane quarter each).
+//              epilogue (one TMEM lane quarter each); with FP8 keys warps 2-9, two
+//              sets that take the tiles in turn.
 // The arithmetic of every score is the same whichever CTA or segment
 // computes it, so a row's scores do not depend on the other rows.
 //
@@ -54,8 +55,8 @@ namespace dsa {
 namespace {
 
 constexpr int kTileM = 128;
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;  // warps 2-5
+template <bool kFp8>
+constexpr int kEpiOf = kFp8 ? 256 : 128;  // epilogue threads: warps 2-5, with FP8 keys 2-9
 constexpr int kMaxStages = 6;
 constexpr int kMaxSubRows = 32;
 constexpr int kSegRing = 4;       // segment records in flight
@@ -105,8 +106,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return out;
 }
 
-// Named barrier of the four epilogue warps, returning the OR of `pred` over
+// Named barrier of the epilogue warps, returning the OR of `pred` over
 // them (the same value in every thread, so they all leave a loop together).
+template <int kEpiThreads>
 __device__ __forceinline__ bool epi_sync_or(bool pred) {
   int out;
   asm volatile(
@@ -119,6 +121,7 @@ __device__ __forceinline__ bool epi_sync_or(bool pred) {
       : "memory");
   return out != 0;
 }
+template <int kEpiThreads>
 __device__ __forceinline__ void epi_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
 }
@@ -218,6 +221,7 @@ __device__ __forceinline__ void scan_sync() {
 // Named barrier of warp 1 and the epilogue warps: the CTA's range and the
 // TMEM address (written by tcgen05.alloc) are handed over here, with the
 // tcgen05 fences on both sides of it.
+template <int kEpiThreads>
 __device__ __forceinline__ void tmem_sync() {
   asm volatile("bar.sync 3, %0;" ::"n"(32 + kEpiThreads) : "memory");
 }
@@ -269,11 +273,13 @@ __device__ __forceinline__ uint64_t key_desc(uint32_t saddr) {
 // kFp8: rows of an operand are D bytes (one 128-byte swizzle span, or for D = 64
 // one of 64 bytes) instead of D bf16 in 64-element sub-tiles.
 template <int D, bool kDirect, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
     index_scores_kernel(const __grid_constant__ CUtensorMap kmap, const IndexParams p) {
   constexpr int kSub = kFp8 ? 1 : D / 64;            // K sub-tiles per operand (one copy each)
   constexpr uint32_t kStageBytes = kTileM * D * (kFp8 ? 1 : 2);  // one 128 x D key tile
   constexpr int kKSteps = D / (kFp8 ? 32 : 16);
+  constexpr int kEpiThreads = kEpiOf<kFp8>, kThreads = 64 + kEpiThreads;
+  constexpr int kSets = kEpiThreads / 128;           // epilogue sets of four warps, tiles in turn
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&ctl->tfull[a], 1);
-      mbar_init(&ctl->tempty[a], kEpiThreads / 32);
+      mbar_init(&ctl->tempty[a], 4);  // the warps of a set
     }
     mbar_init(&ctl->qready, kEpiThreads / 32);
     for (int k = 0; k < kSegRing; ++k) {
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
       }
       tc_fence_before();
-      tmem_sync();  // every path of warp 1 and of the epilogue warps passes it once
+      tmem_sync<kEpiThreads>();  // every path of warp 1 and of the epilogue warps passes it once
       tc_fence_after();
       if (my_tiles > 0) tmem_base = ctl->tmem_base;
     }
@@ -646,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every epilogue warp passes the same named barriers in the same order
     // whatever happens (a timed-out wait only makes the warp skip work), and
     // they leave the segment loop together.
-    const int et = threadIdx.x - 64;            // 0..127
+    const int et = threadIdx.x - 64;
+    const int set = (warp - 2) >> 2;            // takes the accumulator of that number where there are two
     const int quarter = warp & 3;               // TMEM lanes 32*quarter .. = tokens
     const int lane_tok = quarter * 32 + lane;
     const int heads = p.heads;
@@ -751,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The range and the TMEM address from warps 0-1 (the scan has no waits,
     // so warp 1 always gets here).
     tc_fence_before();
-    tmem_sync();
+    tmem_sync<kEpiThreads>();
     tc_fence_after();
     my_tiles = ctl->my_tiles;
     if (my_tiles > 0) tmem_base = ctl->tmem_base;
@@ -775,15 +782,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Leave together when this CTA is done or any warp failed.  The barrier
       // also orders the previous segment's reads of w_s before its rewrite.
-      if (epi_sync_or(w != 1)) break;
+      if (epi_sync_or<kEpiThreads>(w != 1)) break;
       const Seg& sg = ctl->seg[slot];
       const int r0 = sg.r0, nrows = sg.nrows, n = sg.ntiles, t_first = sg.t_first;
       const int max_len_group = sg.max_len;
       const int64_t base = sg.base;
-      // Later segments: the previous segment's MMAs are complete (this warp
-      // consumed its last accumulator), so the operand can be rewritten.
+      // Later segments: the previous segment's MMAs are complete (the warps
+      // consumed its last accumulators), so the operand can be rewritten.
       if (k > 0) build_q(r0, nrows);
-      epi_sync();                // w_s complete before any warp reads it
+      epi_sync<kEpiThreads>();   // w_s complete before any warp reads it
 
       // Each tile's gate is loaded one tile ahead, so the load's DRAM latency
       // hides behind the TMA and the MMAs (plain loads: the gates may come
@@ -800,17 +807,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = (t_first + j) * kTileM + lane_tok;
         return (j < n && t < max_len_group) ? p.k_scale[base + t] : 0.0f;
       };
-      uint16_t g_next = load_gate(0);
+      // A set's first tile of the segment (tile i of the CTA has accumulator i & 1).
+      const int j_first = kSets == 1 ? 0 : (i ^ set) & 1;
+      const int i_end = i + n;
+      i += j_first;
+      uint16_t g_next = load_gate(j_first);
       float ks_next = 0.0f;
-      if constexpr (kFp8) ks_next = load_scale(0);
-      for (int j = 0; j < n && ok; ++j, ++i) {
+      if constexpr (kFp8) ks_next = load_scale(j_first);
+      for (int j = j_first; j < n && ok; j += kSets, i += kSets) {
         const int a = i & 1;
         const int t = (t_first + j) * kTileM + lane_tok;
         float gt = __bfloat162float(__ushort_as_bfloat16(g_next));
-        g_next = load_gate(j + 1);
+        g_next = load_gate(j + kSets);
         if constexpr (kFp8) {
           gt *= ks_next;
-          ks_next = load_scale(j + 1);
+          ks_next = load_scale(j + kSets);
         }
         int wok = 1;
         if (lane == 0) wok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, p.wait_ns) ? 1 : 0;
@@ -829,6 +840,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sum = 0.0f;
           const int c_begin = jr * cols_per_row, c_end = c_begin + cols_per_row;
           int c0 = c_begin;
+          if constexpr (kFp8) {
+            // Four sums of every fourth head: one would be a chain of 64 dependent
+            // additions, longer than the MMAs of its tile.
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto add = [&](float4 w, const float* v) {
+              part[0] = fmaf(w.x, fmaxf(v[0], 0.0f), part[0]);
+              part[1] = fmaf(w.y, fmaxf(v[1], 0.0f), part[1]);
+              part[2] = fmaf(w.z, fmaxf(v[2], 0.0f), part[2]);
+              part[3] = fmaf(w.w, fmaxf(v[3], 0.0f), part[3]);
+            };
+            for (; c0 + 32 <= c_end; c0 += 32) {
+              float v[32];
+              tmem_load32(acc + c0, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) add(*reinterpret_cast<const float4*>(w_s + c0 + 4 * e), v + 4 * e);
+            }
+            if (c0 < c_end) {
+              float v[16];
+              tmem_load16(acc + c0, v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) add(*reinterpret_cast<const float4*>(w_s + c0 + 4 * e), v + 4 * e);
+            }
+            sum = (part[0] + part[1]) + (part[2] + part[3]);
+          } else {
           for (; c0 + 32 <= c_end; c0 += 32) {
             float v[32];
             tmem_load32(acc + c0, v);
@@ -855,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum = fmaf(w.w, fmaxf(v[4 * e + 3], 0.0f), sum);
             }
           }
+          }
           if (t < sg.row_len[jr]) {
             if (!waited) {  // (inputs_early) the first store waits for the kernel before
               grid_dep_wait();
@@ -873,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->segfree[slot]);
+      i = i_end;
       done += n;
     }
   }
@@ -897,8 +934,11 @@ void plan_index_scores(IndexParams& p, int num_sms) {
   const uint32_t b_bytes = static_cast<uint32_t>(p.npad) * p.dim * (is_fp8 ? 1 : 4);
   const uint32_t fixed = b_bytes + p.npad * 4 + sizeof(IndexCtl) + 1024;  // + alignment slack
   const uint32_t two_per_sm = 113u * 1024u, one_per_sm = 226u * 1024u;
+  uint32_t cols = 32;
+  while (cols < 2u * p.npad) cols <<= 1;
+  p.tmem_cols = cols;
   int stages = 0, per_sm = 1;
-  if (fixed + 2 * stage_bytes <= two_per_sm) {
+  if (fixed + 2 * stage_bytes <= two_per_sm && cols <= 256) {
     stages = static_cast<int>((two_per_sm - fixed) / stage_bytes);
     per_sm = 2;
   } else {
@@ -923,9 +963,6 @@ void plan_index_scores(IndexParams& p, int num_sms) {
   if (ctas > tiles_max * groups) ctas = tiles_max * groups;
   p.ctas = static_cast<int32_t>(ctas < 1 ? 1 : ctas);
 
-  uint32_t cols = 32;
-  while (cols < 2u * p.npad) cols <<= 1;
-  p.tmem_cols = cols;
 }
 
 cudaError_t launch_index_scores(const IndexParams& p, const CUtensorMap& kmap,
@@ -946,7 +983,7 @@ cudaError_t launch_index_scores(const IndexParams& p, const CUtensorMap& kmap,
   cfg.gridDim = p.direct ? dim3(static_cast<unsigned>((tiles_max + p.direct_tiles - 1) / p.direct_tiles),
                                 static_cast<unsigned>(groups), 1)
                          : dim3(static_cast<unsigned>(p.ctas), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(64 + (p.q_codes != nullptr ? kEpiOf<true> : kEpiOf<false>), 1, 1);
   cfg.dynamicSmemBytes = p.smem_bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {dependent_launch_attr()};
