@@ -397,11 +397,6 @@ __device__ __forceinline__ bool wait_warp(Ctl* c, uint64_t* bar, uint32_t parity
   if (lane == 0) ok = wait(c, bar, parity, p) ? 1 : 0;
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
 // A box into this CTA's shared memory, its bytes counted on the leader's barrier.
 __device__ __forceinline__ void copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
   asm volatile(
@@ -499,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 0) {
       // ------------------------------------------------------------ copies
-      if (elect_one()) {
+      if (fp8::elect_one()) {
         uint32_t i = 0;
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
@@ -520,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMAs
-      if (rank == 0 && elect_one()) {
+      if (rank == 0 && fp8::elect_one()) {
         const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
         uint32_t i = 0;
         bool ok = true;

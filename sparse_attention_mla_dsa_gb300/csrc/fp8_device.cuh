@@ -48,6 +48,43 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
+// The same with operands by the low words of their descriptors, which alone differ
+// between MMAs: an add for each, nothing else.
+template <uint32_t kHigh>
+__device__ __forceinline__ void umma_low(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kHigh)
+      : "memory");
+}
+
+// One lane of the whole warp.  A branch on it leaves the operands of MMAs and copies
+// in uniform registers, one on lane == 0 does not.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// Which of two phases are complete (bits 0-1).  A look at a barrier takes ~140
+// clocks beside an epilogue's warps; two in a row, and not one after the other's
+// answer, leave an issuing thread time for the MMAs.
+__device__ __forceinline__ uint32_t look2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "selp.b32 x, 1, 0, p;\n\tselp.b32 y, 2, 0, q;\n\tor.b32 %0, x, y;\n\t}"
+      : "=r"(r)
+      : "r"(smem_u32(b0)), "r"(p0), "r"(smem_u32(b1)), "r"(p1)
+      : "memory");
+  return r;
+}
+
 // (a.x * b.x + c.x, a.y * b.y + c.y), each rounded once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

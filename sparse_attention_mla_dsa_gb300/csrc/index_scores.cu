@@ -252,19 +252,12 @@ __device__ __forceinline__ auto q_row(const IndexParams& p, int r) {
   else return p.q_idx + at;
 }
 
-// Descriptor of an FP8 operand, K-major with rows of D bytes: D = 128 as bf16's
-// sub-tiles, D = 64 in the 64-byte swizzle (8-row groups 512 B apart).
+// High word of the descriptors of FP8 operands, K-major with rows of D bytes: D =
+// 128 as bf16's sub-tiles, D = 64 in the 64-byte swizzle (8-row groups 512 B apart).
+// The low word is the address in 16-byte units, with the (unused) leading offset 1.
 template <int D>
-__device__ __forceinline__ uint64_t key_desc(uint32_t saddr) {
-  if constexpr (D == 128) return umma_desc_sw128_kmajor(saddr);
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>(512 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(4) << 61;
-  return d;
-}
+constexpr uint32_t kKeyDescHigh = D == 128 ? (1024u >> 4) | (1u << 14) | (2u << 29) : (512u >> 4) | (1u << 14) | (4u << 29);
+__device__ __forceinline__ uint32_t key_desc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 
 // kDirect: a launch small enough for a few tiles per CTA in a single wave --
 // CTA (x, y) scores tiles [x*dt, x*dt + dt) of group y (dt = direct_tiles,
@@ -597,8 +590,52 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
         mbar_wait(&ctl->full[i % stages], (i / stages) & 1, kDrainWaitNs);
   } else if (warp == 1 && my_tiles > 0) {
     // ============================================================ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = kFp8 ? fp8::idesc_e4m3(kTileM, npad) : umma_idesc_bf16(kTileM, npad);
+    if (kFp8) {
+      // Beside the epilogue's warps every instruction of this thread counts: operands
+      // by the low words of their descriptors, both barriers looked at together.
+      if (fp8::elect_one()) {
+        const uint32_t idesc = fp8::idesc_e4m3(kTileM, npad);
+        const uint32_t a0 = key_desc_low(smem_u32(stage_base)), b0 = key_desc_low(smem_u32(b_hi));
+        long long done = 0;
+        uint32_t i = 0, s = 0, round = 0;   // tile, its stage, and how often that was filled before
+        bool ok = true;
+        for (int k = 0; ok && done < my_tiles; ++k) {
+          const int slot = k % kSegRing;
+          if (aborted(ctl) || !mbar_wait(&ctl->segfull[slot], (k / kSegRing) & 1, p.wait_ns) ||
+              !mbar_wait(&ctl->qready, k & 1, p.wait_ns)) {
+            if (!aborted(ctl)) set_abort(ctl, p.err, -1);
+            break;
+          }
+          const int n = ctl->seg[slot].ntiles;
+          for (int j = 0; j < n; ++j, ++i) {
+            const uint32_t a = i & 1, empty_at = ((i >> 1) - 1) & 1;  // (i < 2: the phase before the first)
+            const uint32_t there = fp8::look2(&ctl->full[s], round & 1, &ctl->tempty[a], empty_at);
+            if (((there & 1) == 0 && !mbar_wait(&ctl->full[s], round & 1, p.wait_ns)) ||
+                ((there & 2) == 0 && !mbar_wait(&ctl->tempty[a], empty_at, p.wait_ns))) {
+              if (!aborted(ctl)) set_abort(ctl, p.err, -1);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_low = a0 + s * (kStageBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKSteps; ++kk)
+              fp8::umma_low<kKeyDescHigh<D>>(tmem_base + a * npad, a_low + kk * 2, b0 + kk * 2, idesc, kk != 0);
+            umma_commit(&ctl->empty[s]);
+            umma_commit(&ctl->tfull[a]);
+            if (++s == static_cast<uint32_t>(stages)) {
+              s = 0;
+              ++round;
+            }
+          }
+          done += n;
+        }
+        // Every MMA issued by this thread is complete before TMEM is released.
+        umma_commit(&ctl->drain);
+        mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+      }
+    } else if (lane == 0) {
+      const uint32_t idesc = umma_idesc_bf16(kTileM, npad);
       const uint32_t a0 = smem_u32(stage_base), bh = smem_u32(b_hi), bl = smem_u32(b_lo);
       long long done = 0;
       int i = 0;
@@ -622,13 +659,8 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + a * npad;
           const uint32_t a_stage = a0 + s * kStageBytes;
-          if constexpr (kFp8) {
 #pragma unroll
-            for (int kk = 0; kk < kKSteps; ++kk)
-              fp8::umma_e4m3(d_tmem, key_desc<D>(a_stage + kk * 32), key_desc<D>(bh + kk * 32), idesc, kk != 0);
-          }
-#pragma unroll
-          for (int half = 0; half < (kFp8 ? 0 : 2); ++half) {
+          for (int half = 0; half < 2; ++half) {
             const uint32_t b_base = half ? bl : bh;
 #pragma unroll
             for (int kk = 0; kk < kKSteps; ++kk) {
@@ -833,7 +865,45 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
         }
         tc_fence_after();
         const uint32_t acc = lane_addr + a * npad;
-        for (int jr = 0; jr < nrows; ++jr) {
+        bool scored = false;
+        if constexpr (kFp8) {
+          if ((heads & 31) == 0) {
+            // 32 columns at a time, all of one row.  Four sums of every fourth head: one would be a chain of
+            // dependent additions, longer than the MMAs of its tile.
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            int jr = 0, left = heads;
+            float* dst = p.scores + static_cast<int64_t>(r0) * p.max_len + t;
+            const int cols = nrows * heads;
+            for (int c = 0; c < cols; c += 32) {
+              float v[32];
+              tmem_load32(acc + c, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 w = *reinterpret_cast<const float4*>(w_s + c + 4 * e);
+                part[0] = fmaf(w.x, fmaxf(v[4 * e], 0.0f), part[0]);
+                part[1] = fmaf(w.y, fmaxf(v[4 * e + 1], 0.0f), part[1]);
+                part[2] = fmaf(w.z, fmaxf(v[4 * e + 2], 0.0f), part[2]);
+                part[3] = fmaf(w.w, fmaxf(v[4 * e + 3], 0.0f), part[3]);
+              }
+              left -= 32;
+              if (left == 0) {
+                if (t < sg.row_len[jr]) {
+                  if (!waited) {
+                    grid_dep_wait();
+                    waited = true;
+                  }
+                  *dst = gt * ((part[0] + part[1]) + (part[2] + part[3]));
+                }
+                part[0] = part[1] = part[2] = part[3] = 0.0f;
+                left = heads;
+                dst += p.max_len;
+                ++jr;
+              }
+            }
+            scored = true;
+          }
+        }
+        for (int jr = 0; jr < nrows && !scored; ++jr) {
           // Columns in ascending order, 32 per TMEM read (16 at an odd end).
           // Columns past the real ones hold 0 (zero q rows) with weight 0, so
           // they add +-0 and leave the sum as it is (it is never -0).
@@ -841,9 +911,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
           const int c_begin = jr * cols_per_row, c_end = c_begin + cols_per_row;
           int c0 = c_begin;
           if constexpr (kFp8) {
-            // Four sums of every fourth head: one would be a chain of 64 dependent
-            // additions, longer than the MMAs of its tile.
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // (as above)
             auto add = [&](float4 w, const float* v) {
               part[0] = fmaf(w.x, fmaxf(v[0], 0.0f), part[0]);
               part[1] = fmaf(w.y, fmaxf(v[1], 0.0f), part[1]);
