@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
     // whatever happens (a timed-out wait only makes the warp skip work), and
     // they leave the segment loop together.
     const int et = threadIdx.x - 64;
-    const int set = (warp - 2) >> 2;            // takes the accumulator of that number where there are two
+    const int set = (warp - 2) >> 2;            // takes every other tile where there are two
     const int quarter = warp & 3;               // TMEM lanes 32*quarter .. = tokens
     const int lane_tok = quarter * 32 + lane;
     const int heads = p.heads;
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
         const int t = (t_first + j) * kTileM + lane_tok;
         return (j < n && t < max_len_group) ? p.k_scale[base + t] : 0.0f;
       };
-      // A set's first tile of the segment (tile i of the CTA has accumulator i & 1).
+      // A set's first tile of the segment.
       const int j_first = kSets == 1 ? 0 : (i ^ set) & 1;
       const int i_end = i + n;
       i += j_first;
@@ -865,6 +865,11 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
         }
         tc_fence_after();
         const uint32_t acc = lane_addr + a * npad;
+        auto free_acc = [&](int a) {  // it is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->tempty[a]);
+        };
         bool scored = false;
         if constexpr (kFp8) {
           if ((heads & 31) == 0) {
@@ -877,6 +882,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
             for (int c = 0; c < cols; c += 32) {
               float v[32];
               tmem_load32(acc + c, v);
+              if (c + 32 == cols) free_acc(a);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float4 w = *reinterpret_cast<const float4*>(w_s + c + 4 * e);
@@ -967,9 +973,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
             p.scores[static_cast<int64_t>(r0 + jr) * p.max_len + t] = gt * sum;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->tempty[a]);
+        if (!scored) free_acc(a);
         if (__shfl_sync(0xFFFFFFFFu, aborted(ctl) ? 1 : 0, 0)) {
           ok = false;
           break;
