@@ -21,8 +21,9 @@ namespace {
 
 using fp8::kBlock;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTileRows = 128;
+constexpr int kTileThreads = 512;
 
 // 16 bytes of x: 8 bf16 or 4 FP32 values.
 template <bool kF32>
@@ -105,11 +106,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantizeP
 
 // One CTA a tile of 128 x 128.
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const QuantizeParams p) {
+__global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const QuantizeParams p) {
   using V = Vec<kF32>;
-  constexpr int kRowsAtOnce = kThreads / V::kLanes;
+  constexpr int kRowsAtOnce = kTileThreads / V::kLanes;
   constexpr int kVecs = kTileRows / kRowsAtOnce;
-  __shared__ uint32_t warp_top[kThreads / 32];
+  __shared__ uint32_t warp_top[kTileThreads / 32];
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kTileRows + threadIdx.x / V::kLanes;
   const int col = static_cast<int>(blockIdx.x) * kBlock + (threadIdx.x % V::kLanes) * V::kElems;
   grid_dep_launch();
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const Quantize
   if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_top[w]);
+  for (int w = 0; w < kTileThreads / 32; ++w) top = max(top, warp_top[w]);
   const uint32_t scale = fp8::scale_bits(top);
   const float inv = fp8::inverse_scale(scale);
 #pragma unroll
@@ -159,6 +160,7 @@ cudaError_t launch_quantize_fp8(const QuantizeParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (p.block_rows == kTileRows) {
+    cfg.blockDim = dim3(kTileThreads, 1, 1);
     cfg.gridDim = dim3(static_cast<unsigned>(p.kblocks), static_cast<unsigned>((p.rows + kTileRows - 1) / kTileRows), 1);
     return p.x_fp32 ? cudaLaunchKernelEx(&cfg, quantize_tiles_kernel<true>, p)
                     : cudaLaunchKernelEx(&cfg, quantize_tiles_kernel<false>, p);
