@@ -38,7 +38,7 @@ template <int kRows>
 struct Shape {
   static constexpr int kStages = kRows <= 32 ? 5 : 4;
   static constexpr uint32_t kStageBytes = kWBytes + kRows * kBlock;
-  static constexpr int kSlots = kRows <= 64 ? 4 : 2;  // accumulators in TMEM
+  static constexpr int kSlots = 4;                    // accumulators in TMEM
   static constexpr uint32_t kTmemCols = kRows * kSlots;
   static_assert(kStageBytes % 1024 == 0 && kTmemCols >= 32 && kTmemCols <= 256, "two CTAs an SM");
 };
@@ -73,8 +73,28 @@ __device__ __forceinline__ void store_c(const Fp8MmParams& p, int64_t m, int n, 
     static_cast<uint16_t*>(p.c)[m * p.n + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t out;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
+  return out;
+}
+// Columns n .. n + 3 (n a multiple of 4), those that there are.
+__device__ __forceinline__ void store_c4(const Fp8MmParams& p, int64_t m, int n, float4 v) {
+  if ((p.n & 3) == 0) {
+    if (p.c_fp32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.c) + m * p.n + n) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.c) + m * p.n + n) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    return;
+  }
+  store_c(p, m, n, v.x);
+  if (n + 1 < p.n) store_c(p, m, n + 1, v.y);
+  if (n + 2 < p.n) store_c(p, m, n + 2, v.z);
+  if (n + 3 < p.n) store_c(p, m, n + 3, v.w);
+}
+
 template <int kRows>
-__global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
     fp8_mm_rows_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                        const Fp8MmParams p) {
   using S = Shape<kRows>;
@@ -147,26 +167,30 @@ __global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
         mbar_wait(&ctl->full[i % S::kStages], (i / S::kStages) & 1, kDrainWaitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (fp8::elect_one()) {
       constexpr uint32_t idesc = fp8::idesc_e4m3(kTileN, kRows);
-      const uint32_t base = smem_u32(smem);
+      const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
+      uint32_t s = 0, round = 0;  // block i's stage, and how often that was filled before
       for (int i = 0; i < nkb; ++i) {
-        const int s = i % S::kStages, t = i % S::kSlots;
-        if (aborted(&ctl->abort_flag)) break;
-        if (!mbar_wait(&ctl->full[s], (i / S::kStages) & 1, p.wait_ns) ||
-            (i >= S::kSlots && !mbar_wait(&ctl->tempty[t], ((i / S::kSlots) - 1) & 1, p.wait_ns))) {
+        const uint32_t t = i % S::kSlots;
+        const uint32_t empty_at = (i / S::kSlots - 1) & 1;  // (the first ones: the phase before the first)
+        const uint32_t there = fp8::look2(&ctl->full[s], round & 1, &ctl->tempty[t], empty_at);
+        if (((there & 1) == 0 && !mbar_wait(&ctl->full[s], round & 1, p.wait_ns)) ||
+            ((there & 2) == 0 && !mbar_wait(&ctl->tempty[t], empty_at, p.wait_ns))) {
           set_abort(&ctl->abort_flag, p.err, tile);
           break;
         }
         tc_fence_after();
-        const uint32_t w_addr = base + s * S::kStageBytes;
-        const uint32_t a_addr = w_addr + kWBytes;
+        const uint32_t w = desc0 + s * (S::kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBlock / 32; ++kk)
-          fp8::umma_e4m3(tmem + t * kRows, umma_desc_sw128_kmajor(w_addr + kk * 32),
-                         umma_desc_sw128_kmajor(a_addr + kk * 32), idesc, kk != 0);
+          fp8::umma_low<fp8::kDescHigh>(tmem + t * kRows, w + kk * 2, w + (kWBytes >> 4) + kk * 2, idesc, kk != 0);
         umma_commit(&ctl->empty[s]);
         umma_commit(&ctl->tfull[t]);
+        if (++s == S::kStages) {
+          s = 0;
+          ++round;
+        }
       }
       umma_commit(&ctl->drain);
       mbar_wait(&ctl->drain, 0, kDrainWaitNs);
@@ -284,10 +308,7 @@ __global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
             sum.z += v[r].z;
             sum.w += v[r].w;
           }
-        store_c(p, m0 + c, n, sum.x);
-        if (n + 1 < p.n) store_c(p, m0 + c, n + 1, sum.y);
-        if (n + 2 < p.n) store_c(p, m0 + c, n + 2, sum.z);
-        if (n + 3 < p.n) store_c(p, m0 + c, n + 3, sum.w);
+        store_c4(p, m0 + c, n, sum);
       }
     }
     fp8::cluster_sync();  // nobody reads this CTA's shared memory any more
@@ -309,17 +330,24 @@ __global__ void __launch_bounds__(kThreads, kRows <= 64 ? 2 : 1)
 // so a thread of the epilogue has one row and columns of one row of weight scales:
 // one factor a block of k.
 //
-// What bounds it is how soon an accumulator is read, scaled and free again.  By
-// halves the MMAs of three others, not of one, run meanwhile; and sixteen warps of 64
-// columns each hide the loads' latency that eight of 128 do not (1,024 x 4,096 x
-// 32,768: 121 us with eight).  The activation scales come through shared memory,
+// What bounds it is how soon an accumulator is read, scaled and free again (by
+// halves the MMAs of three others, not of one, run meanwhile) and that the epilogue's
+// reads of TMEM take turns with the MMAs: without them the MMAs of a block take 660
+// clocks beside their copies, with them 820.  Eight epilogue warps of 128 columns and
+// not sixteen of 64 (108 us for 1,024 x 4,096 x 32,768, 111 with sixteen): beside
+// their instructions the one thread that issues the MMAs has to find room, which is
+// also why it looks at three barriers at once and adds to descriptors' low words only
+// (one after the other, 121 us).  The activation scales come through shared memory,
 // turned there by two warps: a load by the epilogue would touch a line for each row.
 // The outputs leave through shared memory by TMA, behind the next tile's MMAs.
 //
-// Persistent: one pair for every two SMs, tiles in turn.  Roles (640 threads a CTA):
-// warp 0 copies, warp 1 of the leader issues both CTAs' MMAs, warps 2-3 fetch the
-// scales, warps 4-19 are the epilogue (a TMEM lane quarter and 64 columns each) and
-// get the registers that the first four give up.
+// Persistent: one pair for every two SMs, tiles in turn.  (Two or four pairs that share
+// a tile's blocks of k, their sums added through distributed shared memory: 512 x 4,096
+// x 4,096 16.6 us for 17.3, 128 x 2,048 x 4,096 11.9 where row tiles take 8.0: not kept.)
+//
+// Roles (384 threads a CTA): warp 0 copies, warp 1 of the leader issues both CTAs'
+// MMAs, warps 2-3 fetch the scales, warps 4-11 are the epilogue (a TMEM lane quarter
+// and half of the columns each) and get the registers that the first four give up.
 namespace pair {
 
 constexpr int kTile = 256;
@@ -407,14 +435,13 @@ __device__ __forceinline__ void copy(uint32_t dst, const CUtensorMap* map, uint3
 }
 // Operands by the low words of their descriptors, which alone differ between MMAs
 // (in 16-byte units): an add for each, nothing else.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %3, 0;\n\t"
       "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(acc), "n"(kDescHigh), "n"(fp8::idesc_e4m3(256, kTile / 2))
+      "r"(a), "r"(b), "r"(acc), "n"(fp8::kDescHigh), "n"(fp8::idesc_e4m3(256, kTile / 2))
       : "memory");
 }
 // Arrives on `bar` of both CTAs once every MMA issued so far is complete.
@@ -425,12 +452,6 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t out;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
-  return out;
-}
-
 // Tile `t`'s first row and column: groups of kGroupTiles row tiles sweep the
 // weight together, so that both stay in L2 however many rows there are.
 struct Place {
@@ -734,20 +755,24 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   p.kblocks = (p.k + kBlock - 1) / kBlock;
+  // Many rows: pairs, from three tiles for every sixteen SMs on.  32 tiles (512 x 4,096 x
+  // 4,096) take 17.3 us, by row tiles 19.4; 16 (256 x 4,096 x 4,096) 17.1 and 13.4.
   const int64_t pair_tiles = static_cast<int64_t>((p.m + pair::kTile - 1) / pair::kTile) *
                              ((p.n + pair::kTile - 1) / pair::kTile);
   p.pairs = 0;
-  if (p.m > 64 && (pair_tiles * 4 >= num_sms)) {
+  if (p.m > 64 && pair_tiles * 16 >= 3 * num_sms) {
     p.row_tile = 128;
     p.splits = 1;
     p.pairs = static_cast<int32_t>(pair_tiles < num_sms / 2 ? pair_tiles : num_sms / 2);
     return;
   }
   p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
-  // k is split only where the tiles alone leave SMs idle, with two blocks of it
-  // a CTA at least.  Up to 64 rows the split must not depend on m.
+  // k is split until two CTAs an SM are in the launch, with two blocks of it each at
+  // least (32 rows, 4,096 x 32,768: 24.9 us; 28.3 with one an SM and a few more, 31.8
+  // with fewer than one; 4,096 of k by ranges of 4, 8 and 16 blocks: 5.0, 6.1, 9.0 us).
+  // Up to 64 rows the split must not depend on m.
   const int64_t tiles = static_cast<int64_t>((p.n + kTileN - 1) / kTileN) * ((p.m + p.row_tile - 1) / p.row_tile);
-  int splits = tiles < num_sms ? static_cast<int>((num_sms + tiles - 1) / tiles) : 1;
+  int splits = tiles < 2 * num_sms ? static_cast<int>(2 * num_sms / tiles) : 1;
   splits = splits < kMaxSplits ? splits : kMaxSplits;
   const int most = p.kblocks / 2 > 1 ? p.kblocks / 2 : 1;
   splits = splits < most ? splits : most;
@@ -761,8 +786,7 @@ cudaError_t launch_fp8_mm(const Fp8MmParams& p, const CUtensorMap& wmap, const C
   switch (p.row_tile) {
     case 16: return launch_rows<16>(p, wmap, amap, stream);
     case 32: return launch_rows<32>(p, wmap, amap, stream);
-    case 64: return launch_rows<64>(p, wmap, amap, stream);
-    default: return launch_rows<128>(p, wmap, amap, stream);
+    default: return launch_rows<64>(p, wmap, amap, stream);
   }
 }
 

@@ -37,19 +37,11 @@ __device__ __forceinline__ float inverse_scale(uint32_t scale) {
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] * B[smem]^T over 32 of k, issued by one thread.
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same with operands by the low words of their descriptors, which alone differ
-// between MMAs: an add for each, nothing else.
+// High word of umma_desc_sw128_kmajor.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// D[tmem] (+)= A[smem] * B[smem]^T over 32 of k, issued by one thread; operands by
+// the low words of their descriptors, which alone differ between MMAs: an add for
+// each, nothing else.
 template <uint32_t kHigh>
 __device__ __forceinline__ void umma_low(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(

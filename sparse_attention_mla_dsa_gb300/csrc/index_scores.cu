@@ -256,7 +256,7 @@ __device__ __forceinline__ auto q_row(const IndexParams& p, int r) {
 // 128 as bf16's sub-tiles, D = 64 in the 64-byte swizzle (8-row groups 512 B apart).
 // The low word is the address in 16-byte units, with the (unused) leading offset 1.
 template <int D>
-constexpr uint32_t kKeyDescHigh = D == 128 ? (1024u >> 4) | (1u << 14) | (2u << 29) : (512u >> 4) | (1u << 14) | (4u << 29);
+constexpr uint32_t kKeyDescHigh = D == 128 ? fp8::kDescHigh : (512u >> 4) | (1u << 14) | (4u << 29);
 __device__ __forceinline__ uint32_t key_desc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 
 // kDirect: a launch small enough for a few tiles per CTA in a single wave --
