@@ -319,6 +319,360 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+// ------------------------------------------------------------------ shared by the tiles below
+constexpr uint32_t kOutBytes = 32 * 128;          // 32 rows x 128 bytes of the output
+constexpr int kScaleBlocks = 16;                  // blocks of k whose scales are fetched together
+constexpr int kScalePitch = 130;                  // floats between their rows
+
+// Bounded waits; a timeout is recorded and marks the CTA, whose later waits are
+// skipped.  (All of it inline: around a call the accumulators' registers could not
+// stay where they are.)
+struct Waits {
+  int* flag;
+  int* err;
+  uint64_t limit_ns;
+  __device__ __forceinline__ bool aborted() const { return *reinterpret_cast<volatile int*>(flag) != 0; }
+  // Of one thread, without marking.
+  __device__ __forceinline__ bool polled(uint64_t* bar, uint32_t parity) const {
+    if (limit_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1; i < (1u << 30) && !aborted(); ++i) {
+      if (mbar_try_wait_hint(bar, parity, limit_ns < kShortWaitNs ? 32 : kSuspendHintNs)) return true;
+      if (((i & 15u) == 0 || limit_ns < kShortWaitNs) && global_ns() - t0 > limit_ns) break;
+    }
+    if (!aborted()) record_error(err, DSA_DEVERR_TIMEOUT, -1);
+    return false;
+  }
+  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+    if (polled(bar, parity)) return true;
+    *reinterpret_cast<volatile int*>(flag) = 1;
+    return false;
+  }
+  // Of a whole warp: every lane polls, one goes on where it is not there yet.
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, int lane) const {
+    const bool done = limit_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    int ok = 1;
+    if (lane == 0) ok = one(bar, parity) ? 1 : 0;
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+  }
+};
+
+// Scales of 64 activation rows (half of 128, from row m0 on) in the kScaleBlocks
+// blocks from kb0 on, turned to [block][row]: a warp takes two rows x 16 blocks a
+// load.  Rows and blocks outside the tensor get scales of others.
+__device__ __forceinline__ void fetch_scales(const Fp8MmParams& p, float* sa, int m0, int half, int lane, int kb0) {
+  const int kb_in = lane & (kScaleBlocks - 1), odd = lane >> 4;
+  const int row0 = m0 + half * 64 + odd, kb = min(kb0 + kb_in, p.kblocks - 1);
+  float* dst = sa + kb_in * kScalePitch + half * 64 + odd;
+#pragma unroll 1
+  for (int r = 0; r < 64; r += 16) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p.a_scale[static_cast<int64_t>(min(row0 + r + 2 * u, p.m - 1)) * p.kblocks + kb];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) dst[r + 2 * u] = v[u];
+  }
+}
+
+// A warp's 32 rows (a lane each) x kCols columns of the output, through kBufs buffers
+// of kOutBytes; what lies outside the output is not stored.  The copies out may still
+// run when it returns.
+template <int kCols, int kBufs>
+__device__ __forceinline__ void store_tile(const Fp8MmParams& p, const CUtensorMap& cmap, const float (&acc)[kCols],
+                                           uint8_t* outs, int row0, int col0, int lane) {
+  const bool by_tma = (static_cast<int64_t>(p.n) * (p.c_fp32 ? 4 : 2)) % 16 == 0;
+#pragma unroll
+  for (int c = 0; c < kCols; c += 32) {
+    if (by_tma && !p.c_fp32 && (c & 32) != 0) continue;  // (64 columns at a time)
+    uint8_t* out = outs + ((by_tma && !p.c_fp32 ? c / 64 : c / 32) % kBufs) * kOutBytes;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBufs - 1) : "memory");
+    __syncwarp();
+    if (by_tma) {
+      // 128 bytes of each row (64 bf16 columns or 32 FP32 ones), in the 128-byte swizzle.
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint4 w;
+        if (p.c_fp32) {
+          const int b = c + e * 4;
+          w = make_uint4(__float_as_uint(acc[b]), __float_as_uint(acc[b + 1]), __float_as_uint(acc[b + 2]),
+                         __float_as_uint(acc[b + 3]));
+        } else {
+          const int b = (c & ~63) + e * 8;
+          w = make_uint4(bf16x2(acc[b], acc[b + 1]), bf16x2(acc[b + 2], acc[b + 3]),
+                         bf16x2(acc[b + 4], acc[b + 5]), bf16x2(acc[b + 6], acc[b + 7]));
+        }
+        *reinterpret_cast<uint4*>(out + lane * 128 + ((e ^ (lane & 7)) * 16)) = w;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&cmap)),
+            "r"(col0 + c), "r"(row0), "r"(smem_u32(out))
+            : "memory");
+    } else {
+      // Rows that are not multiples of 16 bytes: turned in shared memory, so that
+      // neighbouring lanes store neighbouring columns.
+      float* turn = reinterpret_cast<float*>(out);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) turn[lane * 32 + (e ^ lane)] = acc[c + e];
+      __syncwarp();
+      if (col0 + c + lane < p.n)
+        for (int r = 0; r < min(32, p.m - row0); ++r) store_c(p, row0 + r, col0 + c + lane, turn[r * 32 + (lane ^ r)]);
+      __syncwarp();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ some rows more
+// Tiles of 128 activation rows x 128 weight rows, a CTA each, for what is too much for
+// the row tiles above and too little for the pairs below.  Activation rows are M:
+//   A = 128 activation rows x 128 of k,  B = 128 weight rows x 128 of k
+//   D = 128 x 128 FP32 (lane = activation row, column = weight row), four in turn
+// so a thread of the epilogue has one row and columns of one row of weight scales: one
+// factor a block of k, where row tiles read one for every column from shared memory,
+// whose bandwidth then bounds them (256 x 4,096 x 32,768: 69 us by row tiles).  Up to
+// four CTAs, a cluster, share a tile's blocks of k as above.
+//
+// Roles (384 threads): warp 0 copies, warp 1 issues the MMAs, warps 2-3 fetch the
+// activation scales and turn them in shared memory, warps 4-11 are the epilogue (a
+// TMEM lane quarter and 64 columns each).
+namespace block {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 384;
+constexpr int kFirstEpiWarp = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kCols = 64;                         // columns of an epilogue warp
+constexpr int kMaxSplits = 4;
+constexpr int kStages = 6;
+constexpr uint32_t kOperandBytes = 128 * kBlock;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kSlots = 4;
+constexpr uint32_t kTmemCols = kSlots * kTile;
+constexpr int kPartPitch = kTile + 4;             // floats between rows of a range's sums
+constexpr int kAtOnce = 4;                        // rows of sums that a thread has on their way
+
+struct __align__(8) Ctl {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t tfull[kSlots];
+  uint64_t tempty[kSlots];
+  uint64_t sfull[2];
+  uint64_t sempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  float sb[2][kScaleBlocks];
+  float sa[2][kScaleBlocks * kScalePitch];        // [block][row]
+};
+constexpr uint32_t kCtlOff = kStages * kStageBytes;
+constexpr uint32_t kSmemBytes = kCtlOff + sizeof(Ctl) + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024 && kCtlOff % 8 == 0, "shared memory budget");
+static_assert(128 * kPartPitch * 4 <= kCtlOff && kEpiWarps * kOutBytes <= kCtlOff, "sums and outputs take the place of the stages");
+
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_mm_block_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                        const __grid_constant__ CUtensorMap cmap, const Fp8MmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kCtlOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x, m0 = blockIdx.y * kTile, n0 = blockIdx.z * kTile;
+  const int kb_begin = split * p.kb_per_split;
+  const int nkb = min(p.kb_per_split, p.kblocks - kb_begin);  // >= 1 by the plan
+  const Waits waits{&ctl->abort_flag, p.err, p.wait_ns};
+  grid_dep_launch();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (uint32_t s = 0; s < kSlots; ++s) {
+      mbar_init(&ctl->tfull[s], 1);
+      mbar_init(&ctl->tempty[s], kEpiWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->sfull[s], 2);
+      mbar_init(&ctl->sempty[s], kEpiWarps);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&wmap);
+    tma_prefetch_map(&amap);
+    tma_prefetch_map(&cmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  float acc[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+  const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+  if (warp == 0) {
+    // -------------------------------------------------------------- copies
+    if (fp8::elect_one()) {
+      uint64_t policy;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+      auto copy = [&](int i, const CUtensorMap* map, uint32_t at, int row) {
+        const int s = i % kStages;
+        tma_load_2d(smem + s * kStageBytes + at, map, &ctl->full[s], (kb_begin + i) * kBlock, row, policy);
+      };
+      // (The weight before the dependency wait, as above.)
+      const int early = min(nkb, kStages);
+      for (int i = 0; i < early; ++i) {
+        mbar_arrive_expect_tx(&ctl->full[i], kStageBytes);
+        copy(i, &wmap, kOperandBytes, n0);
+      }
+      grid_dep_wait();
+      for (int i = 0; i < early; ++i) copy(i, &amap, 0, m0);
+      int issued = early;
+      for (; issued < nkb; ++issued) {
+        const int s = issued % kStages;
+        if (!waits.one(&ctl->empty[s], (issued / kStages - 1) & 1)) break;
+        mbar_arrive_expect_tx(&ctl->full[s], kStageBytes);
+        copy(issued, &wmap, kOperandBytes, n0);
+        copy(issued, &amap, 0, m0);
+      }
+      // Never leave with a copy in flight: wait (bounded) for the last loads.
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        mbar_wait(&ctl->full[i % kStages], (i / kStages) & 1, kDrainWaitNs);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMAs
+    if (fp8::elect_one()) {
+      constexpr uint32_t idesc = fp8::idesc_e4m3(kTile, kTile);
+      const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
+      uint32_t s = 0, round = 0;
+      for (int i = 0; i < nkb; ++i) {
+        const uint32_t d = i % kSlots, empty_at = (i / kSlots - 1) & 1;  // (the first ones: the phase before the first)
+        const uint32_t there = fp8::look2(&ctl->full[s], round & 1, &ctl->tempty[d], empty_at);
+        if (((there & 1) == 0 && !waits.one(&ctl->full[s], round & 1)) ||
+            ((there & 2) == 0 && !waits.one(&ctl->tempty[d], empty_at)))
+          break;
+        tc_fence_after();
+        const uint32_t a = desc0 + s * (kStageBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 32; ++kk)
+          fp8::umma_low<fp8::kDescHigh>(tmem + d * kTile, a + kk * 2, a + (kOperandBytes >> 4) + kk * 2, idesc, kk != 0);
+        umma_commit(&ctl->empty[s]);
+        umma_commit(&ctl->tfull[d]);
+        if (++s == kStages) {
+          s = 0;
+          ++round;
+        }
+      }
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+    }
+  } else if (warp < kFirstEpiWarp) {
+    // -------------------------------------------------------------- scales
+    grid_dep_wait();
+    const float* sb = p.b_scale + static_cast<int64_t>(blockIdx.z) * p.kblocks;
+    for (int kb0 = 0, g = 0; kb0 < nkb; kb0 += kScaleBlocks, ++g) {
+      if (g >= 2 && !waits.warp(&ctl->sempty[g & 1], (g / 2 - 1) & 1, lane)) break;
+      fetch_scales(p, ctl->sa[g & 1], m0, warp - 2, lane, kb_begin + kb0);
+      if (warp == 2 && lane < kScaleBlocks) ctl->sb[g & 1][lane] = sb[min(kb_begin + kb0 + lane, p.kblocks - 1)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sfull[g & 1]);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
+    // (After a wait that gave up the warps go on, with waits that no longer wait.)
+    for (int kb0 = 0, g = 0, i = 0; kb0 < nkb; kb0 += kScaleBlocks, ++g) {
+      waits.warp(&ctl->sfull[g & 1], (g / 2) & 1, lane);
+      const float* sa = ctl->sa[g & 1] + quarter * 32 + lane;
+      const float* sb = ctl->sb[g & 1];
+      const int n = min(kScaleBlocks, nkb - kb0);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, ++i) {
+        const uint32_t d = i % kSlots;
+        const float f = sa[j * kScalePitch] * sb[j];
+        waits.warp(&ctl->tfull[d], (i / kSlots) & 1, lane);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float v[32];
+          fp8::tmem_load32(src + d * kTile + c, v);
+          if (c + 32 == kCols) {  // read: the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty[d]);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[c + e] = fmaf(v[e], f, acc[c + e]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sempty[g & 1]);
+    }
+    grid_dep_wait();  // the kernel before may still read the output
+    const int row0 = m0 + quarter * 32, col0 = n0 + half * kCols;
+    // The last accumulator has been read, so every copy and MMA is complete and the
+    // stages are free.
+    if (p.splits > 1) {
+      float4* part = reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * kPartPitch + half * kCols);
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) part[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+    } else if (row0 < p.m && col0 < p.n && !__any_sync(0xFFFFFFFFu, waits.aborted())) {
+      store_tile<kCols, 1>(p, cmap, acc, smem + (warp - kFirstEpiWarp) * kOutBytes, row0, col0, lane);
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are complete
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (p.splits > 1) {
+    fp8::cluster_sync();
+    // The sums of the ranges, four columns of a row a thread, the rows shared out among
+    // the cluster's CTAs.
+    const int e = threadIdx.x - kFirstEpiWarp * 32, n = n0 + (e & 31) * 4;
+    const int rows = (kTile + p.splits - 1) / p.splits, r_end = min(min((split + 1) * rows, kTile), p.m - m0);
+    if (warp >= kFirstEpiWarp && n < p.n)
+      for (int r0 = split * rows + (e >> 5); r0 < r_end; r0 += 8 * kAtOnce) {
+        float4 v[kAtOnce][kMaxSplits];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int q = 0; q < kMaxSplits; ++q)
+            if (q < p.splits && r0 + 8 * u < r_end)
+              v[u][q] = fp8::ld_cluster_f4(reinterpret_cast<float*>(smem) + (r0 + 8 * u) * kPartPitch + (e & 31) * 4, q);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (r0 + 8 * u >= r_end) break;
+          float4 sum = v[u][0];
+#pragma unroll
+          for (int q = 1; q < kMaxSplits; ++q)
+            if (q < p.splits) {
+              sum.x += v[u][q].x;
+              sum.y += v[u][q].y;
+              sum.z += v[u][q].z;
+              sum.w += v[u][q].w;
+            }
+          store_c4(p, m0 + r0 + 8 * u, n, sum);
+        }
+      }
+    fp8::cluster_sync();  // nobody reads this CTA's shared memory any more
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace block
+
 // ------------------------------------------------------------------ many rows
 // Tiles of 256 activation rows x 256 weight rows for a pair of CTAs (a cluster of
 // two, cta_group::2): CTA r multiplies rows 128 r .. 128 r + 127 of the tile by all
@@ -360,9 +714,6 @@ static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * 168, "register spli
 constexpr int kStages = 4;
 constexpr uint32_t kOperandBytes = 128 * kBlock;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr uint32_t kOutBytes = 32 * 128;          // 32 rows x 128 bytes of the output, two of them a warp
-constexpr int kScaleBlocks = 16;                  // blocks of k whose scales are fetched together
-constexpr int kScalePitch = 130;                  // floats between their rows
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGroupTiles = 16;                   // row tiles that share a sweep of the weight
 
@@ -384,22 +735,22 @@ constexpr uint32_t kCtlOff = kStages * kStageBytes + kEpiWarps * 2 * kOutBytes;
 constexpr uint32_t kSmemBytes = kCtlOff + sizeof(Ctl) + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024 && kCtlOff % 8 == 0, "shared memory budget");
 
-__device__ __forceinline__ bool aborted(Ctl* c) { return *reinterpret_cast<volatile int*>(&c->abort_flag) != 0; }
-// Bounded wait of one thread; a timeout is recorded and marks both CTAs, whose
-// later waits are skipped.  (All of it inline: around a call the accumulators'
-// registers could not stay where they are.)
-__device__ __forceinline__ bool wait(Ctl* c, uint64_t* bar, uint32_t parity, const Fp8MmParams& p) {
-  if (p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1; i < (1u << 30) && !aborted(c); ++i) {
-    if (mbar_try_wait_hint(bar, parity, p.wait_ns < kShortWaitNs ? 32 : kSuspendHintNs)) return true;
-    if (((i & 15u) == 0 || p.wait_ns < kShortWaitNs) && global_ns() - t0 > p.wait_ns) break;
+// Waits that mark both CTAs of the pair.
+struct PairWaits : Waits {
+  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+    if (polled(bar, parity)) return true;
+    for (uint32_t r = 0; r < 2; ++r)
+      asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(fp8::map_to(flag, r)), "r"(1) : "memory");
+    return false;
   }
-  if (!aborted(c)) record_error(p.err, DSA_DEVERR_TIMEOUT, -1);
-  for (uint32_t r = 0; r < 2; ++r)
-    asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(fp8::map_to(&c->abort_flag, r)), "r"(1) : "memory");
-  return false;
-}
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, int lane) const {
+    const bool done = limit_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    int ok = 1;
+    if (lane == 0) ok = one(bar, parity) ? 1 : 0;
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+  }
+};
 // Which of three phases are complete (bits 0-2).  A look at a barrier takes ~140
 // clocks beside the epilogue's warps; three in a row, and not one after the other's
 // answer, leave the issuing thread time for the MMAs.
@@ -416,14 +767,6 @@ __device__ __forceinline__ uint32_t look3(uint64_t* b0, uint32_t p0, uint64_t* b
       : "r"(smem_u32(b0)), "r"(p0), "r"(smem_u32(b1)), "r"(smem_u32(b2)), "r"(p12)
       : "memory");
   return r;
-}
-// The same for a whole warp: every lane polls, one goes on where it is not there yet.
-__device__ __forceinline__ bool wait_warp(Ctl* c, uint64_t* bar, uint32_t parity, int lane, const Fp8MmParams& p) {
-  const bool done = p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
-  if (__all_sync(0xFFFFFFFFu, done)) return true;
-  int ok = 1;
-  if (lane == 0) ok = wait(c, bar, parity, p) ? 1 : 0;
-  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 // A box into this CTA's shared memory, its bytes counted on the leader's barrier.
 __device__ __forceinline__ void copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
@@ -476,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t rank = fp8::cluster_rank();
   const int tiles = ((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const PairWaits waits{{&ctl->abort_flag, p.err, p.wait_ns}};
   grid_dep_launch();
 
   if (threadIdx.x == 0) {
@@ -522,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const Place at = place(p, t);
           for (int kb = 0; kb < p.kblocks; ++kb, ++i) {
             const uint32_t s = i % kStages;
-            if (i >= kStages && !(ok = wait(ctl, &ctl->empty[s], (i / kStages - 1) & 1, p))) break;
+            if (i >= kStages && !(ok = waits.one(&ctl->empty[s], (i / kStages - 1) & 1))) break;
             const uint32_t dst = smem_u32(smem) + s * kStageBytes, bar = fp8::map_to(&ctl->full[s], 0);
             // (The phase ends with this arrival at the earliest, so the other CTA's
             // bytes may come before they are expected.)
@@ -546,12 +890,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t full_at = (i / kStages) & 1, empty_at = ((i >> 1) - 1) & 1;  // (i < 2: the phase before the first)
             const uint32_t there =
                 look3(&ctl->full[s], full_at, &ctl->tempty[(i & 1) * 2], &ctl->tempty[(i & 1) * 2 + 1], empty_at);
-            ok = (there & 1) != 0 || wait(ctl, &ctl->full[s], full_at, p);
+            ok = (there & 1) != 0 || waits.one(&ctl->full[s], full_at);
             const uint32_t a = desc0 + s * (kStageBytes >> 4);
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) {
               const uint32_t d = (i & 1) * 2 + h;
-              ok = ok && ((there >> (1 + h) & 1) != 0 || wait(ctl, &ctl->tempty[d], empty_at, p));
+              ok = ok && ((there >> (1 + h) & 1) != 0 || waits.one(&ctl->tempty[d], empty_at));
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -571,29 +915,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     } else {
       // ------------------------------------------------------------ scales
-      // 64 of the CTA's rows each, two rows x 16 blocks a load.
-      const int half = warp - 2, kb_in = lane & (kScaleBlocks - 1), odd = lane >> 4;
+      // 64 of the CTA's rows each, and the weight scales of half of the columns.
+      const int half = warp - 2;
       uint32_t g = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const Place at = place(p, t);
-        // (Rows and columns outside the output are multiplied by scales of others.)
-        const int row0 = at.m + static_cast<int>(rank) * 128 + half * 64;
         const float* sb = p.b_scale + static_cast<int64_t>(min(at.n / 128 + half, (p.n - 1) / 128)) * p.kblocks;
         for (int kb0 = 0; kb0 < p.kblocks; kb0 += kScaleBlocks, ++g) {
-          if (g >= 2 && !(ok = wait_warp(ctl, &ctl->sempty[g & 1], (g / 2 - 1) & 1, lane, p))) break;
-          const int kb = min(kb0 + kb_in, p.kblocks - 1);
-          float* dst = ctl->sa[g & 1] + kb_in * kScalePitch + half * 64 + odd;
-#pragma unroll 1
-          for (int r = 0; r < 64; r += 16) {
-            float v[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              v[u] = p.a_scale[static_cast<int64_t>(min(row0 + odd + r + 2 * u, p.m - 1)) * p.kblocks + kb];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) dst[r + 2 * u] = v[u];
-          }
-          if (lane < kScaleBlocks) ctl->sb[g & 1][half][lane] = sb[kb];
+          if (g >= 2 && !(ok = waits.warp(&ctl->sempty[g & 1], (g / 2 - 1) & 1, lane))) break;
+          fetch_scales(p, ctl->sa[g & 1], at.m + static_cast<int>(rank) * 128, half, lane, kb0);
+          if (lane < kScaleBlocks) ctl->sb[g & 1][half][lane] = sb[min(kb0 + lane, p.kblocks - 1)];
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sfull[g & 1]);
         }
@@ -606,7 +938,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t src0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
     uint8_t* outs = smem + kStages * kStageBytes + (warp - kFirstEpiWarp) * 2 * kOutBytes;
     const uint32_t tempty = fp8::map_to(&ctl->tempty[half], 0);  // and 16 bytes on
-    const bool by_tma = (static_cast<int64_t>(p.n) * (p.c_fp32 ? 4 : 2)) % 16 == 0;
     uint32_t i = 0, g = 0;
     // (After a wait that gave up the warps go on, with waits that no longer wait, and
     // store nothing.)
@@ -615,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
       for (int kb0 = 0; kb0 < p.kblocks; kb0 += kScaleBlocks, ++g) {
-        wait_warp(ctl, &ctl->sfull[g & 1], (g / 2) & 1, lane, p);
+        waits.warp(&ctl->sfull[g & 1], (g / 2) & 1, lane);
         const float* sa = ctl->sa[g & 1] + quarter * 32 + lane;
         const float* sb = ctl->sb[g & 1][half];
         const int n = min(kScaleBlocks, p.kblocks - kb0);
@@ -623,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int j = 0; j < n; ++j, ++i) {
           const uint32_t d = i & 1;
           const float f = sa[j * kScalePitch] * sb[j];
-          wait_warp(ctl, &ctl->tfull[2 * d + half], (i >> 1) & 1, lane, p);
+          waits.warp(&ctl->tfull[2 * d + half], (i >> 1) & 1, lane);
           tc_fence_after();
           const uint32_t src = src0 + d * kTile;
           uint32_t v[2][32];
@@ -646,53 +977,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->sempty[g & 1]);
       }
-      if (__any_sync(0xFFFFFFFFu, aborted(ctl))) break;
+      if (__any_sync(0xFFFFFFFFu, waits.aborted())) break;
       const Place at = place(p, t);
       const int row0 = at.m + static_cast<int>(rank) * 128 + quarter * 32, col0 = at.n + half * kCols;
-      const int cols = p.n - col0;  // of this warp's in the output
-      if (row0 >= p.m || cols <= 0) continue;
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        if (by_tma && !p.c_fp32 && (c & 32) != 0) continue;  // (64 columns at a time)
-        uint8_t* out = outs + ((by_tma && !p.c_fp32 ? c / 64 : c / 32) & 1) * kOutBytes;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-        if (by_tma) {
-          // 128 bytes of each row (64 bf16 columns or 32 FP32 ones), in the 128-byte
-          // swizzle; what lies outside the output is not stored.
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint4 w;
-            if (p.c_fp32) {
-              const int b = c + e * 4;
-              w = make_uint4(__float_as_uint(acc[b]), __float_as_uint(acc[b + 1]), __float_as_uint(acc[b + 2]),
-                             __float_as_uint(acc[b + 3]));
-            } else {
-              const int b = (c & 64) + e * 8;
-              w = make_uint4(bf16x2(acc[b], acc[b + 1]), bf16x2(acc[b + 2], acc[b + 3]),
-                             bf16x2(acc[b + 4], acc[b + 5]), bf16x2(acc[b + 6], acc[b + 7]));
-            }
-            *reinterpret_cast<uint4*>(out + lane * 128 + ((e ^ (lane & 7)) * 16)) = w;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0)
-            asm volatile(
-                "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
-                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&cmap)),
-                "r"(col0 + c), "r"(row0), "r"(smem_u32(out))
-                : "memory");
-        } else {
-          // Rows that are not multiples of 16 bytes: turned in shared memory, so that
-          // neighbouring lanes store neighbouring columns.
-          float* turn = reinterpret_cast<float*>(out);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) turn[lane * 32 + (e ^ lane)] = acc[c + e];
-          __syncwarp();
-          if (c + lane < cols)
-            for (int r = 0; r < min(32, p.m - row0); ++r) store_c(p, row0 + r, col0 + c + lane, turn[r * 32 + (lane ^ r)]);
-        }
-      }
+      if (row0 < p.m && col0 < p.n) store_tile<kCols, 2>(p, cmap, acc, outs, row0, col0, lane);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are complete
   }
@@ -701,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   // After a wait that gave up, copies of this CTA may be in flight that no barrier
   // accounts for: half a second is far more than they take.
-  if (threadIdx.x == 0 && aborted(ctl)) mbar_wait(&ctl->never, 0, kDrainWaitNs);
+  if (threadIdx.x == 0 && waits.aborted()) mbar_wait(&ctl->never, 0, kDrainWaitNs);
   fp8::cluster_sync();
   if (warp == 1) {
     tc_fence_after();
@@ -710,6 +998,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 }  // namespace pair
+
+cudaLaunchAttribute cluster_attr(int ctas) {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = static_cast<unsigned>(ctas);
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
+cudaError_t launch_blocks(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
+                          const CUtensorMap& cmap, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(block::fp8_mm_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(block::kSmemBytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>((p.m + block::kTile - 1) / block::kTile),
+                     static_cast<unsigned>((p.n + block::kTile - 1) / block::kTile));
+  cfg.blockDim = dim3(block::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = block::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {dependent_launch_attr(), cluster_attr(p.splits)};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, block::fp8_mm_block_kernel, wmap, amap, cmap, p);
+}
 
 cudaError_t launch_pairs(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
                          const CUtensorMap& cmap, cudaStream_t stream) {
@@ -741,11 +1055,7 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2] = {dependent_launch_attr(), {}};
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {dependent_launch_attr(), cluster_attr(p.splits)};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, wmap, amap, p);
@@ -755,25 +1065,32 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   p.kblocks = (p.k + kBlock - 1) / kBlock;
-  // Many rows: pairs, from three tiles for every sixteen SMs on.  32 tiles (512 x 4,096 x
-  // 4,096) take 17.3 us, by row tiles 19.4; 16 (256 x 4,096 x 4,096) 17.1 and 13.4.
-  const int64_t pair_tiles = static_cast<int64_t>((p.m + pair::kTile - 1) / pair::kTile) *
-                             ((p.n + pair::kTile - 1) / pair::kTile);
+  // Up to 64 rows: row tiles.  More: pairs from more than one tile of 128 x 128 an SM
+  // on (1,024 x 4,096 x 4,096: 18.4 us, by CTAs 23.8; 512 x 4,096 x 4,096, 128 tiles,
+  // 17.3 and 12.8), below that a CTA or some for each of those tiles, unless they come
+  // to fewer than seven blocks of k an SM, where row tiles, two CTAs an SM, start and
+  // end sooner (128 x 2,048 x 4,096, 512 blocks: 7.9 us, 8.7 by 128 x 128; 200 x 4,096 x
+  // 4,096, 2,048 blocks: 13.8 and 10.9).
+  const int64_t mt = (p.m + block::kTile - 1) / block::kTile, nt = (p.n + block::kTile - 1) / block::kTile;
   p.pairs = 0;
-  if (p.m > 64 && pair_tiles * 16 >= 3 * num_sms) {
+  p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
+  if (p.m > 64 && mt * nt > num_sms) {
+    const int64_t pair_tiles = (mt + 1) / 2 * ((nt + 1) / 2);
     p.row_tile = 128;
     p.splits = 1;
+    p.kb_per_split = p.kblocks;
     p.pairs = static_cast<int32_t>(pair_tiles < num_sms / 2 ? pair_tiles : num_sms / 2);
     return;
   }
-  p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
+  if (p.m > 64 && mt * nt * p.kblocks >= 7 * num_sms) p.row_tile = 128;
   // k is split until two CTAs an SM are in the launch, with two blocks of it each at
   // least (32 rows, 4,096 x 32,768: 24.9 us; 28.3 with one an SM and a few more, 31.8
   // with fewer than one; 4,096 of k by ranges of 4, 8 and 16 blocks: 5.0, 6.1, 9.0 us).
   // Up to 64 rows the split must not depend on m.
   const int64_t tiles = static_cast<int64_t>((p.n + kTileN - 1) / kTileN) * ((p.m + p.row_tile - 1) / p.row_tile);
-  int splits = tiles < 2 * num_sms ? static_cast<int>(2 * num_sms / tiles) : 1;
-  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  const int ctas = num_sms * (p.row_tile <= 64 ? 2 : 1), cluster = p.row_tile <= 64 ? kMaxSplits : block::kMaxSplits;
+  int splits = tiles < ctas ? static_cast<int>(ctas / tiles) : 1;
+  splits = splits < cluster ? splits : cluster;
   const int most = p.kblocks / 2 > 1 ? p.kblocks / 2 : 1;
   splits = splits < most ? splits : most;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
@@ -786,7 +1103,8 @@ cudaError_t launch_fp8_mm(const Fp8MmParams& p, const CUtensorMap& wmap, const C
   switch (p.row_tile) {
     case 16: return launch_rows<16>(p, wmap, amap, stream);
     case 32: return launch_rows<32>(p, wmap, amap, stream);
-    default: return launch_rows<64>(p, wmap, amap, stream);
+    case 64: return launch_rows<64>(p, wmap, amap, stream);
+    default: return launch_blocks(p, wmap, amap, cmap, stream);
   }
 }
 

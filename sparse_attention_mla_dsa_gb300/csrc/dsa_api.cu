@@ -637,7 +637,7 @@ dsa_status dsa_dense_mm_fp8(const uint8_t* a, const float* a_scale, const uint8_
   if (cr == CUDA_SUCCESS) cr = map(&amap, a, m_rows, p.row_tile);
   CUtensorMap cmap = amap;  // (not used)
   const int32_t c_bytes = c_fp32 ? 4 : 2;
-  if (cr == CUDA_SUCCESS && p.pairs > 0 && static_cast<int64_t>(n_out) * c_bytes % 16 == 0) {
+  if (cr == CUDA_SUCCESS && p.row_tile == 128 && static_cast<int64_t>(n_out) * c_bytes % 16 == 0) {
     const cuuint64_t dim[2] = {static_cast<cuuint64_t>(n_out), static_cast<cuuint64_t>(m_rows)};
     const cuuint64_t stride[1] = {static_cast<cuuint64_t>(n_out) * c_bytes};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / c_bytes), 32};

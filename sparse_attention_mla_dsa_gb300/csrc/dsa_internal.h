@@ -202,15 +202,15 @@ struct Fp8MmParams {
   int32_t row_tile;       // rows of a that a CTA multiplies
   int32_t kb_per_split;   // K blocks per CTA
   int32_t splits;         // K ranges per tile: the CTAs of a cluster
-  int32_t pairs;          // pairs of CTAs that share 256 x 256 tiles; 0: row_tile x 128 tiles, a CTA each
+  int32_t pairs;          // pairs of CTAs that share 256 x 256 tiles; 0: row_tile x 128 tiles, one or more CTAs each
   uint64_t wait_ns;
 };
 // Fills in kblocks / row_tile / kb_per_split / splits / pairs from (m, n, k) and the SM count.
 void plan_fp8_mm(Fp8MmParams& p, int num_sms);
 // `wmap` describes the weight [n][k], `amap` the activations [m][k], both bytes,
 // for boxes of 128 bytes of k by 128 (64 with pairs) and by row_tile rows; `cmap`,
-// with pairs and rows of c that are multiples of 16 bytes, the output for boxes of
-// 128 bytes by 32 rows.
+// with a row_tile of 128 and rows of c that are multiples of 16 bytes, the output for
+// boxes of 128 bytes by 32 rows.
 cudaError_t launch_fp8_mm(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
                           const CUtensorMap& cmap, cudaStream_t stream);
 

@@ -76,7 +76,8 @@ def _check(api, ops, out=torch.float32):
     (1, 1, 16), (1, 128, 128), (1, 2048, 4096), (2, 7, 48), (16, 128, 4096), (17, 129, 144), (31, 300, 272),
     (32, 2048, 1536), (33, 127, 1024), (64, 520, 640), (65, 257, 256), (100, 33, 4112), (128, 128, 128),
     (129, 1000, 400), (200, 96, 8192), (257, 513, 528), (300, 2048, 1536), (777, 1003, 208), (1024, 640, 384),
-    (1300, 2056, 272), (1281, 1999, 144), (300, 5200, 528), (2500, 1025, 128), (5000, 520, 48), (70, 20000, 256)])
+    (1300, 2056, 272), (1281, 1999, 144), (300, 5200, 528), (2500, 1025, 128), (5000, 520, 48), (70, 20000, 256),
+    (65, 4000, 4096), (100, 2500, 8192), (129, 1001, 12304), (400, 1000, 4112), (777, 1003, 4112), (128, 300, 32768)])
 def test_matches_64_bits(api, m, n, k, out):
     _check(api, _operands(m + n + k, m, n, k), out)
 
