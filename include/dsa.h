@@ -456,10 +456,9 @@ dsa_status dsa_quantize_fp8(const void *x, int32_t x_fp32, int32_t rows, int32_t
  *   c [m_rows][n_out] bf16 (c_fp32 = 0, round to nearest even) or fp32
  *     (c_fp32 = 1), 16-byte aligned, not overlapping an input
  * m_rows in [1, 65535] and n_out up to 65535 * 128 (DSA_ERR_UNSUPPORTED above);
- * k >= 16 and a multiple of 16 (DSA_ERR_INVALID_ARG).  No workspace.  The weight
- * and its scales are taken to be complete before the kernel issued just before
- * this call on the stream started (dsa_dense_mm_bf16 reads its weight likewise);
- * a and a_scale may be its output.
+ * k >= 16 and a multiple of 16 (DSA_ERR_INVALID_ARG).  No workspace.  Any
+ * operand may be the output of the kernel just before (unlike dsa_dense_mm_bf16's
+ * weight).
  * Numerics: a block's products are exact and accumulate in FP32 on the tensor
  * cores; each block's sum is multiplied by the product of its two scales
  * (rounded to FP32) and added in FP32, blocks in order, within each of the

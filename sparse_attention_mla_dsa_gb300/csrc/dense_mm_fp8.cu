@@ -137,22 +137,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t w_policy = l2_policy_evict_first();
       uint64_t a_policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(a_policy));
-      // The weight is an input that no kernel writes: its first tiles go out
-      // before the dependency wait, the activations' after it.
-      const int early = min(nkb, S::kStages);
-      for (int i = 0; i < early; ++i) {
-        mbar_arrive_expect_tx(&ctl->full[i], S::kStageBytes);
-        tma_load_2d(smem + i * S::kStageBytes, &wmap, &ctl->full[i], (kb_begin + i) * kBlock, n0, w_policy);
-      }
+      // Any operand may come from the kernel before (a weight just quantised), so
+      // nothing is loaded before the dependency wait; the first tiles of the weight
+      // are on their way to L2 meanwhile, where a write of that kernel lands too.
+      for (int i = 0; i < min(nkb, S::kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);
       grid_dep_wait();
-      for (int i = 0; i < early; ++i)
-        tma_load_2d(smem + i * S::kStageBytes + kWBytes, &amap, &ctl->full[i], (kb_begin + i) * kBlock, m0,
-                    a_policy);
-      int issued = early;
+      int issued = 0;
       for (; issued < nkb; ++issued) {
         if (aborted(&ctl->abort_flag)) break;
         const int s = issued % S::kStages;
-        if (!mbar_wait(&ctl->empty[s], ((issued / S::kStages) - 1) & 1, p.wait_ns)) {
+        if (issued >= S::kStages && !mbar_wait(&ctl->empty[s], ((issued / S::kStages) - 1) & 1, p.wait_ns)) {
           set_abort(&ctl->abort_flag, p.err, tile);
           break;
         }
@@ -528,18 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = i % kStages;
         tma_load_2d(smem + s * kStageBytes + at, map, &ctl->full[s], (kb_begin + i) * kBlock, row, policy);
       };
-      // (The weight before the dependency wait, as above.)
-      const int early = min(nkb, kStages);
-      for (int i = 0; i < early; ++i) {
-        mbar_arrive_expect_tx(&ctl->full[i], kStageBytes);
-        copy(i, &wmap, kOperandBytes, n0);
-      }
+      for (int i = 0; i < min(nkb, kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);  // (as above)
       grid_dep_wait();
-      for (int i = 0; i < early; ++i) copy(i, &amap, 0, m0);
-      int issued = early;
+      int issued = 0;
       for (; issued < nkb; ++issued) {
         const int s = issued % kStages;
-        if (!waits.one(&ctl->empty[s], (issued / kStages - 1) & 1)) break;
+        if (issued >= kStages && !waits.one(&ctl->empty[s], (issued / kStages - 1) & 1)) break;
         mbar_arrive_expect_tx(&ctl->full[s], kStageBytes);
         copy(issued, &wmap, kOperandBytes, n0);
         copy(issued, &amap, 0, m0);

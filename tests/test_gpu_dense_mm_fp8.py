@@ -199,6 +199,23 @@ def test_activations_written_by_the_kernel_just_before(api):
             assert torch.equal(c, want)
 
 
+@pytest.mark.parametrize("m,n,k", [(4, 4096, 4096), (200, 4096, 4096), (600, 8192, 1024)])
+def test_weight_written_by_the_kernel_just_before(api, m, n, k):
+    a, sa, _, _ = _dev(_operands(17, m, n, k))
+    ws = [torch.randn((n, k), device="cuda") for _ in range(2)]
+    b, sb = torch.empty((n, k), dtype=torch.uint8, device="cuda"), torch.empty((n // 128, k // 128), device="cuda")
+    c, want = torch.empty((m, n), device="cuda"), []
+    for w in ws:
+        api.dsa_quantize_fp8(w, b, sb, block_rows=128)
+        torch.cuda.synchronize()
+        api.dsa_dense_mm_fp8(a, sa, b, sb, c)
+        want.append(c.clone())
+    for i in range(20):
+        api.dsa_quantize_fp8(ws[i % 2], b, sb, block_rows=128)
+        api.dsa_dense_mm_fp8(a, sa, b, sb, c)
+        assert torch.equal(c, want[i % 2]), i
+
+
 def test_two_streams_at_once(api):
     sets = [_dev(_operands(20 + i, m, 1500, 2048)) for i, m in enumerate((8, 300))]
     want = []
