@@ -43,7 +43,7 @@
 // queries are E4M3 codes with one FP32 scale a key and a (row, head),
 //     s_r(t) = gate(t) ks(t) * sum_h (w_r[h] qs_r[h]) * relu(q8_r[h] . k8(t))
 // (a scale is not negative, so it passes through the ReLU), whose products one
-// FP8 MMA forms exactly: half the key bytes and an eighth of the MMA time, the
+// FP8 MMA forms exactly: half the key bytes and a quarter of the MMA time, the
 // query operand is copied, not split, and the scales ride on the head weights
 // and the gate.
 #include <climits>
@@ -730,45 +730,45 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
           }
         }
       } else {
-      const float* qsrc = q_row<kFp8, D>(p, r0);
-      for (int v0 = et; v0 < nvec; v0 += kBatch * kEpiThreads) {
-        float4 u[kBatch][2];
+        const float* qsrc = q_row<kFp8, D>(p, r0);
+        for (int v0 = et; v0 < nvec; v0 += kBatch * kEpiThreads) {
+          float4 u[kBatch][2];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int v = v0 + b * kEpiThreads;
-          const int row = v / vec_per_row, c8 = v % vec_per_row;
-          if (v < nvec && row < nreal) {
-            const float4* src = reinterpret_cast<const float4*>(qsrc + static_cast<int64_t>(row) * D + c8 * 8);
-            u[b][0] = ld_dep_f4(src);
-            u[b][1] = ld_dep_f4(src + 1);
-          } else {
-            u[b][0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            u[b][1] = u[b][0];
+          for (int b = 0; b < kBatch; ++b) {
+            const int v = v0 + b * kEpiThreads;
+            const int row = v / vec_per_row, c8 = v % vec_per_row;
+            if (v < nvec && row < nreal) {
+              const float4* src = reinterpret_cast<const float4*>(qsrc + static_cast<int64_t>(row) * D + c8 * 8);
+              u[b][0] = ld_dep_f4(src);
+              u[b][1] = ld_dep_f4(src + 1);
+            } else {
+              u[b][0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              u[b][1] = u[b][0];
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int v = v0 + b * kEpiThreads;
+            if (v >= nvec) break;
+            const int row = v / vec_per_row, c8 = v % vec_per_row;
+            const float x[8] = {u[b][0].x, u[b][0].y, u[b][0].z, u[b][0].w,
+                                u[b][1].x, u[b][1].y, u[b][1].z, u[b][1].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat16 h0 = __float2bfloat16_rn(x[2 * e]);
+              const __nv_bfloat16 h1 = __float2bfloat16_rn(x[2 * e + 1]);
+              const float r0f = x[2 * e] - __bfloat162float(h0);
+              const float r1f = x[2 * e + 1] - __bfloat162float(h1);
+              hi[e] = pack_bf16x2(__bfloat162float(h0), __bfloat162float(h1));
+              lo[e] = pack_bf16x2(r0f, r1f);
+            }
+            const int sb = (c8 * 8) / 64, chunk = c8 & 7;
+            const uint32_t off = sb * (npad * 128) + row * 128 + ((chunk ^ (row & 7)) * 16);
+            *reinterpret_cast<uint4*>(b_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(b_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int v = v0 + b * kEpiThreads;
-          if (v >= nvec) break;
-          const int row = v / vec_per_row, c8 = v % vec_per_row;
-          const float x[8] = {u[b][0].x, u[b][0].y, u[b][0].z, u[b][0].w,
-                              u[b][1].x, u[b][1].y, u[b][1].z, u[b][1].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat16 h0 = __float2bfloat16_rn(x[2 * e]);
-            const __nv_bfloat16 h1 = __float2bfloat16_rn(x[2 * e + 1]);
-            const float r0f = x[2 * e] - __bfloat162float(h0);
-            const float r1f = x[2 * e + 1] - __bfloat162float(h1);
-            hi[e] = pack_bf16x2(__bfloat162float(h0), __bfloat162float(h1));
-            lo[e] = pack_bf16x2(r0f, r1f);
-          }
-          const int sb = (c8 * 8) / 64, chunk = c8 & 7;
-          const uint32_t off = sb * (npad * 128) + row * 128 + ((chunk ^ (row & 7)) * 16);
-          *reinterpret_cast<uint4*>(b_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(b_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
       }
 #pragma unroll
       for (int e = 0; e < kWPer; ++e) {

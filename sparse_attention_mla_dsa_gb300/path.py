@@ -27,11 +27,14 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
 
 
 class DeviceWorkload:
-    """All inputs of a workload resident on one CUDA device, plus outputs."""
+    """All inputs of a workload resident on one CUDA device, plus outputs.
+    ``index_fp8``: the indexer's keys are kept as E4M3 codes with a scale a key
+    (half the bytes that S1 reads), and S1 quantises the step's queries."""
 
     def __init__(self, wl, device: str | torch.device = "cuda", pool: torch.Tensor | None = None,
-                 _clone_of: "DeviceWorkload | None" = None):
+                 _clone_of: "DeviceWorkload | None" = None, index_fp8: bool = False):
         self.wl = wl
+        self.index_fp8 = index_fp8 if _clone_of is None else _clone_of.index_fp8
         if _clone_of is not None:
             self._init_clone(_clone_of)
             return
@@ -58,6 +61,13 @@ class DeviceWorkload:
         self.lse = torch.empty((R, H), dtype=torch.float32, device=d)
         nbytes = api.dsa_workspace_bytes(R, H, wl.topk)
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=d)
+        self.idx_k8 = self.idx_scale = self.q8 = self.q_scale = None
+        if index_fp8:
+            self.idx_k8 = torch.empty(self.idx_k.shape, dtype=torch.uint8, device=d)
+            self.idx_scale = torch.empty(self.idx_k.shape[0], dtype=torch.float32, device=d)
+            self.q8 = torch.empty(self.q_idx.shape, dtype=torch.uint8, device=d)
+            self.q_scale = torch.empty(self.q_idx.shape[:2], dtype=torch.float32, device=d)
+            api.dsa_quantize_fp8(self.idx_k, self.idx_k8, self.idx_scale)
         self.out_target = None      # where S3 writes; None = self.out
         self.rows = api.make_rows(self.seq_lens, self.block_table, wl.block_size, self.slots,
                                   self.positions, shared_table=(wl.bt_stride == 0))
@@ -66,7 +76,7 @@ class DeviceWorkload:
         self.device = src.device
         for name in ("seq_lens", "positions", "slots", "block_table", "pool", "idx_k", "idx_gate",
                      "idx_base", "q_idx", "head_w", "Q", "kv_a", "norm_w", "scores", "sel", "out",
-                     "lse", "workspace"):
+                     "lse", "workspace", "idx_k8", "idx_scale", "q8", "q_scale"):
             t = getattr(src, name)
             setattr(self, name, None if t is None else t.clone())
         self.max_len = src.max_len
@@ -94,6 +104,12 @@ class DeviceWorkload:
         uploaded before the step) were complete before the kernel issued just
         before this call started, so the indexer may load and score them
         before its dependency wait (its stores still wait)."""
+        if self.index_fp8:  # its queries come from the kernel just before
+            api.dsa_quantize_fp8(self.q_idx, self.q8, self.q_scale, stream=stream)
+            api.dsa_index_scores_fp8(self.rows, self.q8, self.q_scale, self.head_w, self.idx_k8, self.idx_scale,
+                                     self.idx_gate, self.idx_base, self.wl.group_rows, self.max_len, self.scores,
+                                     stream=stream)
+            return
         api.dsa_index_scores(self.rows, self.q_idx, self.head_w, self.idx_k, self.idx_gate,
                              self.idx_base, self.wl.group_rows, self.max_len, self.scores,
                              stream=stream, inputs_early=inputs_early)

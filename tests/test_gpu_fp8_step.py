@@ -1,4 +1,4 @@
-"""The 8-bit operators together, as a decode step runs them: the layer input
+"""The 8-bit operators together, as a step runs them: the layer input
 quantised, projected to the indexer's key and queries, the key written into the
 FP8 cache, the queries quantised, the cache scored and the top tokens selected.
 Each stage is checked against the 64-bit form of the stage on what the stage
@@ -124,3 +124,34 @@ def test_steps_captured_once_and_replayed(api):
         step.positions += 2
         step.seq_lens += 2
         step.hidden.copy_(torch.randn(step.hidden.shape, device="cuda"))
+
+
+@pytest.mark.parametrize("name,kw", [("tiny", dict(len_div=4)), ("verify", dict(seqs=2, len_div=64)),
+                                     ("long", dict(seqs=3, len_div=32))])
+def test_decode_path_over_fp8_index_keys(api, oracle, name, kw):
+    from sparse_attention_mla_dsa_gb300 import path, workloads
+    from tests import parity
+    wl = workloads.scaled(name, **kw)
+    dw = path.DeviceWorkload(wl, index_fp8=True)
+    dw.step()
+    torch.cuda.synchronize()
+    assert api.dsa_get_error(reset=True)[0] == 0
+    scores, sel, out = dw.scores.cpu().numpy(), dw.sel.cpu().numpy(), dw.out_f32()
+    T, dim = wl.idx_k.shape
+    pool = wl.pool.copy()
+    if wl.kv_a is not None:
+        oracle.latent_write(pool, wl.kv_a, wl.norm_w, wl.slots, wl.eps, wl.kv_scale)
+    for r in range(wl.rows):
+        L, base = int(wl.seq_lens[r]), int(wl.idx_base[r])
+        k8, ks = ref.quantize(ref.bf16(wl.idx_k[base:base + L]))
+        q8, qs = ref.quantize(wl.q_idx[r])
+        want, size = ref.index_scores(q8, qs[:, 0], wl.head_w[r], k8, ks[:, 0], ref.bf16(wl.idx_gate[base:base + L]))
+        assert (np.abs(scores[r, :L] - want) <= 2.0 ** -14 * size).all()
+        assert np.array_equal(oracle.select_topk_row(scores[r, :L].astype(np.float64), L, wl.topk), sel[r])
+        o_ref, _ = oracle.mla_decode_row(wl.Q[r], pool, wl.block_table[r], wl.block_size, L, sel[r], wl.kv_scale, wl.sm_scale)
+        parity.assert_out(out[r], o_ref, f"{name} row {r}")
+    twin = dw.clone()
+    twin.scores.zero_()
+    twin.step()
+    for n in ("sel", "out"):
+        assert torch.equal(getattr(twin, n), getattr(dw, n))
