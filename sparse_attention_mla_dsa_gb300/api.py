@@ -433,17 +433,19 @@ def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     [..., ceil(k / 128)] (or [...] where that is 1).  128 (x [rows, k]): for each 128
     x 128, scales [ceil(rows / 128), ceil(k / 128)]."""
     shape, device = x.shape, _device_of(x, "x")
-    if len(shape) < 1 or (block_rows != 1 and len(shape) != 2):
+    dims = len(shape)
+    if dims < 1 or (block_rows != 1 and dims != 2):
         raise ValueError(f"x: unexpected shape {tuple(shape)}")
     k = shape[-1]
     kb = (k + 127) // 128
-    if block_rows != 1:
-        want = ((shape[0] + block_rows - 1) // block_rows, kb)
+    if dims == 2:
+        rows = shape[0]
+        want = (rows, kb) if block_rows == 1 else ((rows + block_rows - 1) // block_rows, kb)
     else:
+        rows = x.numel() // k if k else 0
         want = shape[:-1] + (kb,)
-        if kb == 1 and scales.dim() == len(shape) - 1:
-            want = shape[:-1]
-    rows = x.numel() // k if k else 0
+    if kb == 1 and block_rows == 1 and scales.dim() == dims - 1:
+        want = shape[:-1]
     st = load().dsa_quantize_fp8(_take(x, _VALUES, shape, device, "x"), x.dtype is torch.float32, rows, k,
                                  block_rows, _take(codes, _U8, shape, device, "codes"),
                                  _take(scales, _F32, want, device, "scales"), _stream_on(stream, device))

@@ -32,21 +32,24 @@ struct Vec {
   static constexpr int kLanes = kBlock / kElems;  // lanes of one block of a row
   uint4 v;
 
-  // Bits of the largest |x| as a float, infinities and NaN left out.
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kF32) {
-        const uint32_t a = w[i] & 0x7FFFFFFFu;
-        m = max(m, a < 0x7F800000u ? a : 0u);
-      } else {
-        const uint32_t hi = w[i] & 0x7FFF0000u, lo = (w[i] << 16) & 0x7FFF0000u;
-        m = max(m, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
-      }
-    }
-    return m;
+  // The largest |x| so far as maxima() keeps it: bits without signs, of two bf16
+  // values beside each other or of one float.
+  __device__ __forceinline__ uint32_t maxima() const {
+    constexpr uint32_t kMagnitude = kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    return larger(larger(v.x & kMagnitude, v.y & kMagnitude), larger(v.z & kMagnitude, v.w & kMagnitude));
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return kF32 ? max(a, b) : __vmaxu2(a, b); }
+  // The bits of that as a float; not below those of infinity if one of them is not finite.
+  static __device__ __forceinline__ uint32_t as_float(uint32_t m) {
+    return kF32 ? m : max(m & 0xFFFF0000u, m << 16);
+  }
+  // Without the infinities and NaN.
+  __device__ __forceinline__ Vec finite() const {
+    auto keep = [](uint32_t w) {
+      if constexpr (kF32) return (w & 0x7FFFFFFFu) < 0x7F800000u ? w : 0u;
+      return ((w & 0x7FFF0000u) < 0x7F800000u ? w & 0xFFFF0000u : 0u) | ((w & 0x7FFFu) < 0x7F80u ? w & 0xFFFFu : 0u);
+    };
+    return {make_uint4(keep(v.x), keep(v.y), keep(v.z), keep(v.w))};
   }
 
   __device__ __forceinline__ void store_codes(uint8_t* dst, float inv) const {
@@ -93,9 +96,13 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantizeP
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    uint32_t top = v[u].top();
+    auto over_lanes = [](uint32_t m) {
 #pragma unroll
-    for (int o = V::kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      for (int o = V::kLanes / 2; o > 0; o >>= 1) m = V::larger(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      return V::as_float(m);
+    };
+    uint32_t top = over_lanes(v[u].maxima());
+    if (__any_sync(0xFFFFFFFFu, top >= 0x7F800000u)) top = over_lanes(v[u].finite().maxima());
     const uint32_t scale = fp8::scale_bits(top);
     if (at[u] >= 0) {
       v[u].store_codes(p.codes + at[u], fp8::inverse_scale(scale));
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantizeP
 
 // One CTA a tile of 128 x 128.
 template <bool kF32>
-__global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const QuantizeParams p) {
+__global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const QuantizeParams p) {
   using V = Vec<kF32>;
   constexpr int kRowsAtOnce = kTileThreads / V::kLanes;
   constexpr int kVecs = kTileRows / kRowsAtOnce;
@@ -123,14 +130,22 @@ __global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const Quan
     if (row < p.rows && col < p.k)
       v[i].v = load16(static_cast<const char*>(p.x) + (row * p.k + col) * (kF32 ? 4 : 2));
   }
-  uint32_t top = 0;
+  auto over_tile = [&](bool all) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) top = max(top, v[i].top());
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-  __syncthreads();
+    for (int i = 0; i < kVecs; ++i) m = V::larger(m, all ? v[i].maxima() : v[i].finite().maxima());
+    m = __reduce_max_sync(0xFFFFFFFFu, V::as_float(m));
+    if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = m;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) top = max(top, warp_top[w]);
+    for (int w = 0; w < kTileThreads / 32; ++w) m = max(m, warp_top[w]);
+    return m;
+  };
+  uint32_t top = over_tile(true);
+  if (top >= 0x7F800000u) {  // (of the whole CTA)
+    __syncthreads();
+    top = over_tile(false);
+  }
   const uint32_t scale = fp8::scale_bits(top);
   const float inv = fp8::inverse_scale(scale);
 #pragma unroll
