@@ -856,8 +856,15 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
           ks_next = load_scale(j + kSets);
         }
         int wok = 1;
-        if (lane == 0) wok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, p.wait_ns) ? 1 : 0;
-        wok = __shfl_sync(0xFFFFFFFFu, wok, 0);
+        if constexpr (kFp8) {
+          // Every lane looks, one goes on where it is not there yet.
+          const bool there = p.wait_ns >= kShortWaitNs && mbar_try_wait(&ctl->tfull[a], (i >> 1) & 1);
+          wok = __all_sync(0xFFFFFFFFu, there) ? 2 : 1;
+        }
+        if (wok == 1) {
+          if (lane == 0) wok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, p.wait_ns) ? 1 : 0;
+          wok = __shfl_sync(0xFFFFFFFFu, wok, 0);
+        }
         if (!wok) {
           if (lane == 0) set_abort(ctl, p.err, r0);
           ok = false;
@@ -974,7 +981,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
           }
         }
         if (!scored) free_acc(a);
-        if (__shfl_sync(0xFFFFFFFFu, aborted(ctl) ? 1 : 0, 0)) {
+        if (!kFp8 && __shfl_sync(0xFFFFFFFFu, aborted(ctl) ? 1 : 0, 0)) {
           ok = false;
           break;
         }
