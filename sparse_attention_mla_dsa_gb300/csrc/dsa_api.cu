@@ -590,8 +590,9 @@ dsa_status dsa_quantize_fp8(const void* x, int32_t x_fp32, int32_t rows, int32_t
   if (static_cast<int64_t>(rows) * p.kblocks > INT32_MAX ||
       (block_rows > 1 && (rows + static_cast<int64_t>(block_rows) - 1) / block_rows > 65535))
     return DSA_ERR_UNSUPPORTED;
-  if (device_info() == nullptr) return DSA_ERR_CUDA;
-  return launched(launch_quantize_fp8(p, static_cast<cudaStream_t>(stream)));
+  const DeviceInfo* dev = device_info();
+  if (dev == nullptr) return DSA_ERR_CUDA;
+  return launched(launch_quantize_fp8(p, dev->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 dsa_status dsa_dense_mm_fp8(const uint8_t* a, const float* a_scale, const uint8_t* b,

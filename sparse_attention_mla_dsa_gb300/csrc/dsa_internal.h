@@ -189,7 +189,8 @@ struct QuantizeParams {
   int32_t block_rows;     // 1 or 128
   int32_t x_fp32;
 };
-cudaError_t launch_quantize_fp8(const QuantizeParams& p, cudaStream_t stream);
+// num_sms chooses the launch shape only; the results do not depend on it.
+cudaError_t launch_quantize_fp8(const QuantizeParams& p, int num_sms, cudaStream_t stream);
 
 struct Fp8MmParams {
   const float* a_scale;   // [m][kblocks]

@@ -136,3 +136,13 @@ def test_refusals(api):
     with pytest.raises(api.DsaError) as e:
         api.dsa_quantize_fp8(x[:, :24].contiguous(), codes[:, :24].contiguous(), scales[:, :1].contiguous())
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [157, 601, 1501])
+def test_more_blocks_at_a_time(api, rows, dtype):
+    """Numbers of blocks at which a group of lanes takes one, two and four of them."""
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn((rows, 4112), generator=g) * torch.randn((rows, 1), generator=g).mul(3).exp()
+    x[::7, 130], x[3::11, 4100], x[5::13, 1000:1300] = float("inf"), float("nan"), -float("inf")
+    _check(api, x.to(dtype).cuda(), 1)
