@@ -224,3 +224,26 @@ def test_refusals(api):
             api.dsa_indexer_write_fp8(**(good | bad))
         assert e.value.status == 1
     assert (c.idx_k == OLD).all()
+
+
+def test_weights_from_the_kernel_before(api):
+    """The norm's weight and bias are outputs of the kernel just before each write."""
+    c = Case(api, [0], [0], 1, 128, gate=False)
+    g = torch.Generator().manual_seed(2)
+    k_raw, one = c.k_raw.cuda(), torch.zeros((1, 16), dtype=torch.bfloat16, device="cuda")
+    one[0, 0] = 1
+    sides = torch.zeros((2, 256, 16), dtype=torch.bfloat16)
+    sides[:, :, 0] = torch.randn((2, 256), generator=g).to(torch.bfloat16)
+    dev = sides.cuda()
+    wb = torch.zeros((1, 256), dtype=torch.bfloat16, device="cuda")
+    workspace = torch.empty(max(api.dsa_dense_mm_workspace_bytes(256, 16), 256), dtype=torch.uint8, device="cuda")
+    got_k, got_s = torch.empty((40, 128), dtype=torch.uint8, device="cuda"), torch.empty(40, device="cuda")
+    for i in range(40):
+        api.dsa_dense_mm_bf16(one, dev[i % 2], wb, workspace)
+        api.dsa_indexer_write_fp8(c.rows, k_raw, wb[0, :128], wb[0, 128:], EPS, c.idx_base, got_k[i:i + 1],
+                                  got_s[i:i + 1])
+    torch.cuda.synchronize()
+    for i in range(40):
+        c.w, c.b = sides[i % 2, :128, 0].contiguous(), sides[i % 2, 128:, 0].contiguous()
+        k, s, _ = c.want([0])
+        assert np.array_equal(got_k[i].cpu().numpy(), k[0]) and got_s[i].item() == s[0], i
