@@ -424,6 +424,7 @@ def _stream_on(stream, device: int) -> int | None:
 
 
 _VALUES = _BITS16 + (torch.float32,)
+_UNSUPPORTED = 2                     # dsa_status; sizes that its arguments do not hold
 
 
 def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -440,12 +441,14 @@ def dsa_quantize_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     kb = (k + 127) // 128
     if dims == 2:
         rows = shape[0]
-        want = (rows, kb) if block_rows == 1 else ((rows + block_rows - 1) // block_rows, kb)
+        want = (rows, kb) if block_rows == 1 else ((rows - 1) // max(block_rows, 1) + 1, kb)
     else:
         rows = x.numel() // k if k else 0
         want = shape[:-1] + (kb,)
     if kb == 1 and block_rows == 1 and scales.dim() == dims - 1:
         want = shape[:-1]
+    if rows >> 31 or k >> 31:
+        raise DsaError("dsa_quantize_fp8", _UNSUPPORTED)
     st = load().dsa_quantize_fp8(_take(x, _VALUES, shape, device, "x"), x.dtype is torch.float32, rows, k,
                                  block_rows, _take(codes, _U8, shape, device, "codes"),
                                  _take(scales, _F32, want, device, "scales"), _stream_on(stream, device))
@@ -462,6 +465,8 @@ def dsa_dense_mm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
         raise ValueError(f"shapes a {tuple(a.shape)}, b {tuple(b.shape)}")
     (m, k), n, device = a.shape, b.shape[0], _device_of(a, "a")
     kb = (k + 127) // 128
+    if (m | n | k) >> 31:
+        raise DsaError("dsa_dense_mm_fp8", _UNSUPPORTED)
     st = load().dsa_dense_mm_fp8(_take(a, _U8, (m, k), device, "a"), _take(a_scale, _F32, (m, kb), device, "a_scale"),
                                  _take(b, _U8, (n, k), device, "b"),
                                  _take(b_scale, _F32, ((n + 127) // 128, kb), device, "b_scale"),
@@ -508,6 +513,8 @@ def dsa_index_scores_fp8(rows: Rows, q: torch.Tensor, q_scale: torch.Tensor, hea
     if q.dim() != 3 or idx_k.dim() != 2:
         raise ValueError(f"shapes q {tuple(q.shape)}, idx_k {tuple(idx_k.shape)}")
     R, heads, (T, dim), device = rows.rows, q.shape[1], idx_k.shape, _device_of(idx_k, "idx_k")
+    if max_len >> 31 > 0 or heads >> 31:
+        raise DsaError("dsa_index_scores_fp8", _UNSUPPORTED)
     st = load().dsa_index_scores_fp8(ctypes.byref(rows), _take(q, _U8, (R, heads, dim), device, "q"),
                                      _take(q_scale, _F32, (R, heads), device, "q_scale"),
                                      _take(head_w, _F32, (R, heads), device, "head_w"),

@@ -130,3 +130,33 @@ def test_binding_refuses_host_tensors():
     u = torch.zeros((2, 128), dtype=torch.uint8)
     with pytest.raises(ValueError):
         api.dsa_dense_mm_fp8(u, torch.zeros((2, 1)), u, torch.zeros((1, 1)), torch.zeros((2, 2)))
+
+
+class _Sized:
+    """What the binding looks at before a size is refused."""
+    dtype = torch.uint8
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+
+def test_binding_refuses_sizes_that_an_argument_does_not_hold(monkeypatch):
+    from sparse_attention_mla_dsa_gb300 import api
+    monkeypatch.setattr(api, "_current_index", lambda: 0)
+    t, much = _Sized(4, 32), 2 ** 32 + 1
+    rows = api.Rows()
+    rows.rows = 1
+    for call in (lambda: api.dsa_quantize_fp8(_Sized(much, 16), t, t),
+                 lambda: api.dsa_quantize_fp8(_Sized(1, 2 ** 32 + 16), t, t),
+                 lambda: api.dsa_dense_mm_fp8(_Sized(much, 16), t, t, t, t),
+                 lambda: api.dsa_dense_mm_fp8(t, t, _Sized(much, 32), t, t),
+                 lambda: api.dsa_index_scores_fp8(rows, _Sized(1, 32, 128), t, t, _Sized(9, 128), t, t, t, 1, much, t)):
+        with pytest.raises(api.DsaError) as e:
+            call()
+        assert e.value.status == UNSUPPORTED

@@ -146,3 +146,12 @@ def test_more_blocks_at_a_time(api, rows, dtype):
     x = torch.randn((rows, 4112), generator=g) * torch.randn((rows, 1), generator=g).mul(3).exp()
     x[::7, 130], x[3::11, 4100], x[5::13, 1000:1300] = float("inf"), float("nan"), -float("inf")
     _check(api, x.to(dtype).cuda(), 1)
+
+
+@pytest.mark.parametrize("block_rows", [0, 64, 2])
+def test_refused_block_rows(api, block_rows):
+    x = torch.zeros((1, 256), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(api.DsaError) as e:
+        api.dsa_quantize_fp8(x, torch.zeros((1, 256), dtype=torch.uint8, device="cuda"),
+                             torch.zeros((1, 2), device="cuda"), block_rows=block_rows)
+    assert e.value.status == 1
