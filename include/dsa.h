@@ -23,6 +23,12 @@
  *                          list, and every row's metadata, from the lengths
  *      dsa_mla_chunk_fp8   dense causal attention of the new tokens over the paged
  *                          latent cache (no selection)
+ * and the projections and the indexer over 8-bit operands with a scale for each
+ * block of 128, half the bytes of their bf16 forms:
+ *      dsa_quantize_fp8    bf16 or FP32 values to E4M3 codes and scales
+ *      dsa_dense_mm_fp8    projection of any number of rows
+ *      dsa_indexer_write_fp8  the indexer key's LayerNorm, quantised and stored
+ *      dsa_index_scores_fp8   S1 over those keys
  * Sources (spark_model documentation):
  * the "glm5next_dsa/layer.rs" source page (module header: decode data flow
  * and its traps; decode_k: latent write, per-row metadata, one attend for all
@@ -516,8 +522,8 @@ dsa_status dsa_indexer_write_fp8(const dsa_rows *rows, const uint16_t *k_raw, co
  * dsa_index_scores_ex; q and idx_k are 16-byte aligned.  max(0, NaN) is 0: a NaN
  * code takes its head out of the sum.
  * Numerics: the products are exact and accumulate in FP32 on the tensor cores; the
- * heads are added in FP32 in order, then multiplied by the product of gate and
- * scale.  Each row's result does not depend on rows_per_seq or on the other rows
+ * heads are added in FP32, every fourth one in order into one of four sums, and
+ * (s0 + s1) + (s2 + s3) is multiplied by the product of gate and scale.  Each row's result does not depend on rows_per_seq or on the other rows
  * (bit for bit).
  */
 dsa_status dsa_index_scores_fp8(const dsa_rows *rows, const uint8_t *q, const float *q_scale,
