@@ -19,6 +19,8 @@
 //
 // CTA roles (192 threads): warp 0 issues TMA, warp 1 owns TMEM and issues the
 // MMAs (one thread), warps 2-5 are the epilogue (one TMEM lane quarter each).
+#include <mutex>
+
 #include "dsa_internal.h"
 #include "fp8_device.cuh"
 
@@ -354,18 +356,21 @@ struct Waits {
 
 // Scales of 64 activation rows (half of 128, from row m0 on) in the kScaleBlocks
 // blocks from kb0 on, turned to [block][row]: a warp takes two rows x 16 blocks a
-// load.  Rows and blocks outside the tensor get scales of others.
+// load, kAtOnce of them at once: a round's latency is a small tile's (300 x 4,096 x
+// 4,096 13.1 us with 8, 10.9 with all 32).  Rows and blocks outside the tensor get
+// scales of others.
+template <int kAtOnce>
 __device__ __forceinline__ void fetch_scales(const Fp8MmParams& p, float* sa, int m0, int half, int lane, int kb0) {
   const int kb_in = lane & (kScaleBlocks - 1), odd = lane >> 4;
   const int row0 = m0 + half * 64 + odd, kb = min(kb0 + kb_in, p.kblocks - 1);
   float* dst = sa + kb_in * kScalePitch + half * 64 + odd;
 #pragma unroll 1
-  for (int r = 0; r < 64; r += 16) {
-    float v[8];
+  for (int r = 0; r < 64; r += 2 * kAtOnce) {
+    float v[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = p.a_scale[static_cast<int64_t>(min(row0 + r + 2 * u, p.m - 1)) * p.kblocks + kb];
+    for (int u = 0; u < kAtOnce; ++u) v[u] = p.a_scale[static_cast<int64_t>(min(row0 + r + 2 * u, p.m - 1)) * p.kblocks + kb];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) dst[r + 2 * u] = v[u];
+    for (int u = 0; u < kAtOnce; ++u) dst[r + 2 * u] = v[u];
   }
 }
 
@@ -447,7 +452,7 @@ constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr uint32_t kSlots = 4;
 constexpr uint32_t kTmemCols = kSlots * kTile;
 constexpr int kPartPitch = kTile + 4;             // floats between rows of a range's sums
-constexpr int kAtOnce = 4;                        // rows of sums that a thread has on their way
+constexpr int kAtOnce = 2;                        // rows of sums that a thread has on their way
 
 struct __align__(8) Ctl {
   uint64_t full[kStages];
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* sb = p.b_scale + static_cast<int64_t>(blockIdx.z) * p.kblocks;
     for (int kb0 = 0, g = 0; kb0 < nkb; kb0 += kScaleBlocks, ++g) {
       if (g >= 2 && !waits.warp(&ctl->sempty[g & 1], (g / 2 - 1) & 1, lane)) break;
-      fetch_scales(p, ctl->sa[g & 1], m0, warp - 2, lane, kb_begin + kb0);
+      fetch_scales<32>(p, ctl->sa[g & 1], m0, warp - 2, lane, kb_begin + kb0);
       if (warp == 2 && lane < kScaleBlocks) ctl->sb[g & 1][lane] = sb[min(kb_begin + kb0 + lane, p.kblocks - 1)];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->sfull[g & 1]);
@@ -912,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const float* sb = p.b_scale + static_cast<int64_t>(min(at.n / 128 + half, (p.n - 1) / 128)) * p.kblocks;
         for (int kb0 = 0; kb0 < p.kblocks; kb0 += kScaleBlocks, ++g) {
           if (g >= 2 && !(ok = waits.warp(&ctl->sempty[g & 1], (g / 2 - 1) & 1, lane))) break;
-          fetch_scales(p, ctl->sa[g & 1], at.m + static_cast<int>(rank) * 128, half, lane, kb0);
+          fetch_scales<16>(p, ctl->sa[g & 1], at.m + static_cast<int>(rank) * 128, half, lane, kb0);
           if (lane < kScaleBlocks) ctl->sb[g & 1][half][lane] = sb[min(kb0 + lane, p.kblocks - 1)];
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->sfull[g & 1]);
@@ -996,6 +1001,38 @@ cudaLaunchAttribute cluster_attr(int ctas) {
   return a;
 }
 
+// How many clusters of 1 .. 4 CTAs that fill an SM each the current device holds at
+// once: fewer than its SMs would, as the SMs of a cluster lie together (152, 76, 46, 36).
+struct ClustersAtOnce {
+  int of[block::kMaxSplits + 1];
+};
+const ClustersAtOnce& clusters_at_once(int num_sms) {
+  constexpr int kDevices = 64;          // (device_info refuses more)
+  static ClustersAtOnce counts[kDevices];
+  static std::once_flag counted[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+  std::call_once(counted[dev], [&] {
+    (void)cudaFuncSetAttribute(block::fp8_mm_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(block::kSmemBytes));
+    for (int s = 1; s <= block::kMaxSplits; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
+      cfg.blockDim = dim3(block::kThreads, 1, 1);
+      cfg.dynamicSmemBytes = block::kSmemBytes;
+      cudaLaunchAttribute attr[1] = {cluster_attr(s)};
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int& n = counts[dev].of[s];
+      if (cudaOccupancyMaxActiveClusters(&n, block::fp8_mm_block_kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = num_sms / s;
+      }
+    }
+  });
+  return counts[dev];
+}
+
 cudaError_t launch_blocks(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
                           const CUtensorMap& cmap, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(block::fp8_mm_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1054,11 +1091,11 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   p.kblocks = (p.k + kBlock - 1) / kBlock;
   // Up to 64 rows: row tiles.  More: pairs from more than one tile of 128 x 128 an SM
-  // on (1,024 x 4,096 x 4,096: 18.4 us, by CTAs 23.8; 512 x 4,096 x 4,096, 128 tiles,
-  // 17.3 and 12.8), below that a CTA or some for each of those tiles, unless they come
-  // to fewer than seven blocks of k an SM, where row tiles, two CTAs an SM, start and
-  // end sooner (128 x 2,048 x 4,096, 512 blocks: 7.9 us, 8.7 by 128 x 128; 200 x 4,096 x
-  // 4,096, 2,048 blocks: 13.8 and 10.9).
+  // on (1,024 x 4,096 x 4,096: 17.7 us, by CTAs 22.6; 512 x 4,096 x 4,096, 128 tiles,
+  // 17.3 and 11.9), below that a CTA or some for each of those tiles (777 x 1,024 x
+  // 2,048: 7.3 us, by row tiles 8.9; 1,000 x 2,048 x 512 4.2 and 5.7), unless they are
+  // fewer than eight, where k can be split further for row tiles (65 x 128 x 16,384: 9.3
+  // us, by 128 x 128 11.3; 100 x 512 x 2,048 5.2 and 5.6).
   const int64_t mt = (p.m + block::kTile - 1) / block::kTile, nt = (p.n + block::kTile - 1) / block::kTile;
   p.pairs = 0;
   p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
@@ -1070,15 +1107,18 @@ void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
     p.pairs = static_cast<int32_t>(pair_tiles < num_sms / 2 ? pair_tiles : num_sms / 2);
     return;
   }
-  if (p.m > 64 && mt * nt * p.kblocks >= 7 * num_sms) p.row_tile = 128;
-  // k is split until two CTAs an SM are in the launch, with two blocks of it each at
-  // least (32 rows, 4,096 x 32,768: 24.9 us; 28.3 with one an SM and a few more, 31.8
-  // with fewer than one; 4,096 of k by ranges of 4, 8 and 16 blocks: 5.0, 6.1, 9.0 us).
-  // Up to 64 rows the split must not depend on m.
+  if (p.m > 64 && mt * nt >= 8) p.row_tile = 128;
+  // k is split as far as the launch's clusters run at once, with two blocks of k in each
+  // range at least (32 rows, 4,096 x 32,768: 24.9 us; 28.3 with ranges for one CTA an SM
+  // and a few more, 31.8 for fewer; 4,096 of k by ranges of 4, 8 and 16 blocks: 5.0, 6.1,
+  // 9.0 us; 40 clusters of 7 row tiles, which take two turns, 12.2 us, of 6 8.2; 48 of 3
+  // tiles of 128 x 128 15.6, of 2 9.1).  Two CTAs of row tiles fit an SM.  Up to 64 rows
+  // the split must not depend on m.
   const int64_t tiles = static_cast<int64_t>((p.n + kTileN - 1) / kTileN) * ((p.m + p.row_tile - 1) / p.row_tile);
-  const int ctas = num_sms * (p.row_tile <= 64 ? 2 : 1), cluster = p.row_tile <= 64 ? kMaxSplits : block::kMaxSplits;
-  int splits = tiles < ctas ? static_cast<int>(ctas / tiles) : 1;
-  splits = splits < cluster ? splits : cluster;
+  const ClustersAtOnce& at_once = clusters_at_once(num_sms);
+  const bool rows = p.row_tile <= 64;
+  int splits = rows ? kMaxSplits : block::kMaxSplits;
+  while (splits > 1 && tiles > at_once.of[rows ? (splits + 1) / 2 : splits]) --splits;
   const int most = p.kblocks / 2 > 1 ? p.kblocks / 2 : 1;
   splits = splits < most ? splits : most;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
