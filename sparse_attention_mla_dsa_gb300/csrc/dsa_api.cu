@@ -105,7 +105,7 @@ void set_index_rows(IndexParams& p, const DeviceInfo& dev, const dsa_rows& rows,
   // count that is not a multiple of 16 runs one row per launch group so that
   // no 16-column TMEM load straddles two rows.
   // FP8 keys have two sets of epilogue warps and no query split in two, so groups of
-  // 128 columns (1,024 rows of 32 heads over 9,000 keys: 66 us, 84 with 64).
+  // 128 columns (1,024 rows of 32 heads over 9,000 keys: 66 us then, 84 with 64).
   int sub = (p.q_codes != nullptr ? 128 : 64) / index_heads;
   if (index_heads % 16 != 0) sub = 1;
   sub = sub < 1 ? 1 : (sub > 32 ? 32 : sub);

@@ -45,7 +45,13 @@
 // (a scale is not negative, so it passes through the ReLU), whose products one
 // FP8 MMA forms exactly: half the key bytes and a quarter of the MMA time, the
 // query operand is copied, not split, and the scales ride on the head weights
-// and the gate.
+// and the gate.  A decode is bound by the key bytes (64 requests of 4k to 128k, 64
+// heads, 296 MB: 47.9 us, 6.2 TB/s).  A prompt's chunk, whose rows share the keys, is
+// bound by the epilogue, a maximum and an addition for every head and token beside
+// the reads of TMEM and of the head weights (1,024 rows of 32 heads over 9,000 keys:
+// 62.3 us, where the MMAs alone would take 18): hence two sets of epilogue warps on
+// different tiles (the rows of each tile shared out between them: 78 us for 66),
+// accumulators that are free once read, not once added up, and four sums a row.
 #include <climits>
 
 #include "dsa_internal.h"
