@@ -1042,8 +1042,9 @@ const ClustersAtOnce& clusters_at_once(int num_sms) {
 
 cudaError_t launch_blocks(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
                           const CUtensorMap& cmap, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(block::fp8_mm_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(block::kSmemBytes));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block::fp8_mm_block_kernel),
+                             static_cast<int>(block::kSmemBytes), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>((p.m + block::kTile - 1) / block::kTile),
@@ -1059,8 +1060,9 @@ cudaError_t launch_blocks(const Fp8MmParams& p, const CUtensorMap& wmap, const C
 
 cudaError_t launch_pairs(const Fp8MmParams& p, const CUtensorMap& wmap, const CUtensorMap& amap,
                          const CUtensorMap& cmap, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(pair::fp8_mm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(pair::kSmemBytes));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(pair::fp8_mm_pair_kernel),
+                             static_cast<int>(pair::kSmemBytes), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * p.pairs), 1, 1);
@@ -1079,7 +1081,8 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
   const auto kernel = fp8_mm_rows_kernel<kRows>;
   constexpr uint32_t bytes = smem_bytes<kRows>();
   static_assert(bytes <= 227 * 1024 && kRows * kTileN * 4 <= Shape<kRows>::kStages * Shape<kRows>::kStageBytes, "");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(bytes), allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>((p.m + kRows - 1) / kRows),

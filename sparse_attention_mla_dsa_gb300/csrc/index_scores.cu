@@ -1061,7 +1061,9 @@ cudaError_t launch_index_scores(const IndexParams& p, const CUtensorMap& kmap,
   if (p.q_codes != nullptr)
     kernel = p.direct ? (p.dim == 64 ? index_scores_kernel<64, true, true> : index_scores_kernel<128, true, true>)
                       : (p.dim == 64 ? index_scores_kernel<64, false, true> : index_scores_kernel<128, false, true>);
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
+  static std::atomic<uint64_t> allowed[8];
+  e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmemBytes,
+                 allowed[(p.q_codes != nullptr ? 4 : 0) + (p.direct ? 2 : 0) + (p.dim == 64 ? 1 : 0)]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int64_t tiles_max = (static_cast<int64_t>(p.max_len) + kTileM - 1) / kTileM;
