@@ -440,7 +440,7 @@ __device__ __forceinline__ void store_tile(const Fp8MmParams& p, const CUtensorM
 //
 // Bound by 32 KB from L2 for each block and CTA and the epilogue's reads of TMEM (512 x
 // 4,096 x 4,096: 11.9 us, 1.4 PFLOP/s).  Where k is not a multiple of 128 a block of a
-// row lies in two lines of L2 (777 x 1,003 with k 4,112: 13.9 us, with 4,224 11.0).
+// row lies in two lines of L2 (777 x 1,003 with k 4,112: 12.8 us, with 4,224 10.9).
 //
 // Roles (384 threads): warp 0 copies, warp 1 issues the MMAs, warps 2-3 fetch the
 // activation scales and turn them in shared memory, warps 4-11 are the epilogue (a
