@@ -245,3 +245,30 @@ def test_refusals(api):
         api.dsa_dense_mm_fp8(a[:, :40].contiguous(), sa[:, :1].contiguous(), b[:, :40].contiguous(),
                              sb[:, :1].contiguous(), c)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("n", [60000, 60001])                # rows of 16 bytes, and not
+def test_offsets_past_32_bits(api, n):
+    """An output of more than 2^31 elements: its first and last rows against 64 bits."""
+    m, k = 40000, 32
+    ops = _operands(30, 64, n, k)
+    a = np.zeros((m, k), np.uint8)
+    sa = np.ones((m, 1), np.float32)
+    a[:32], a[-32:], sa[:32], sa[-32:] = ops[0][:32], ops[0][32:], ops[1][:32], ops[1][32:]
+    c = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    a, sa, b, sb = _dev((a, sa, *ops[2:]))
+    api.dsa_dense_mm_fp8(a, sa, b, sb, c)
+    got = torch.cat([c[:32], c[-32:]]).double().cpu().numpy()
+    assert not torch.any(c[32:-32] != 0)                     # (NaN is not 0 either)
+    del c
+    torch.cuda.empty_cache()
+    want, size = ref.product(*ops)
+    tol = (2.0 ** -15 + 9 * 2.0 ** -24) * size
+    assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-300).all()
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (20, 5120, 2048), (33, 7000, 2064), (7, 12000, 1040), (60, 4608, 912),        # row tiles in 6, 4, 2 and 3 ranges
+    (300, 2048, 2048), (65, 1024, 512), (400, 1500, 2320), (90, 1001, 1936)])     # 128 x 128 in 2, 2, 3 and 4
+def test_numbers_of_ranges(api, m, n, k):
+    _check(api, _operands(m + n, m, n, k))
