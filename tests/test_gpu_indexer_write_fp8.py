@@ -1,7 +1,7 @@
-"""dsa_indexer_write_fp8 against the 64-bit form: codes and scales equal.  Both
-sides take the norm in 64 bits and round once, so a code may differ only where
-the value lies within 1e-12 of a border between two codes; the count is asserted
-to be 0 for these inputs."""
+"""dsa_indexer_write_fp8 against the 64-bit form: codes and scales equal.  The
+kernel's are those of the norm in 64 bits, rounded once, so a code may differ only
+where the value lies within 1e-12 of a border between two codes; the count is
+asserted to be 0 for these inputs."""
 import numpy as np
 import pytest
 import torch
