@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb_begin = split * p.kb_per_split;
   const int nkb = min(p.kb_per_split, p.kblocks - kb_begin);  // >= 1 by the plan
   const int n0 = tile * kTileN;
-  grid_dep_launch();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -86,10 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&amap);
   }
-  if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_then_launch(&ctl->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

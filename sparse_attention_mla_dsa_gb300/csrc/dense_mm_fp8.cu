@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int kb_begin = split * p.kb_per_split;
   const int nkb = min(p.kb_per_split, p.kblocks - kb_begin);  // >= 1 by the plan
   const int n0 = tile * kTileN, m0 = blockIdx.y * kRows;
-  grid_dep_launch();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -128,10 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&amap);
   }
-  if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, S::kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_then_launch(&ctl->tmem_base, S::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -490,7 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb_begin = split * p.kb_per_split;
   const int nkb = min(p.kb_per_split, p.kblocks - kb_begin);  // >= 1 by the plan
   const Waits waits{&ctl->abort_flag, p.err, p.wait_ns};
-  grid_dep_launch();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -512,10 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&amap);
     tma_prefetch_map(&cmap);
   }
-  if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_then_launch(&ctl->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -820,7 +812,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int tiles = ((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const PairWaits waits{{&ctl->abort_flag, p.err, p.wait_ns}};
-  grid_dep_launch();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -843,12 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tma_prefetch_map(&amap);
     tma_prefetch_map(&cmap);
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc_pair_then_launch(&ctl->tmem_base, kTmemCols);
   tc_fence_before();
   fp8::cluster_sync();
   tc_fence_after();

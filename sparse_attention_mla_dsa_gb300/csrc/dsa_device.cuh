@@ -160,6 +160,10 @@ __device__ __forceinline__ uint4 ld_dep_u4(const uint4* p) {
                : "memory");
   return v;
 }
+// One thread's call counts for its CTA.  A kernel with tensor memory makes it from
+// the warp that allocates, behind the allocation, and nowhere else: tcgen05.alloc
+// waits without a limit until the SM has the columns, and a CTA of the next kernel
+// that took them first would keep them until this kernel has ended.
 __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -201,14 +205,24 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
 }
 
 // ------------------------------------------------------------------ tcgen05
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_u32(dst)),
-               "r"(ncols)
-               : "memory");
+// By one warp: takes the CTA's tensor memory, then lets the next kernel start (in
+// this order, see grid_dep_launch).
+__device__ __forceinline__ void tmem_alloc_then_launch(uint32_t* dst, uint32_t ncols) {
+  asm volatile(
+      "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+      "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::"r"(smem_u32(dst)),
+      "r"(ncols)
+      : "memory");
+  grid_dep_launch();
 }
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+// The same for a pair of CTAs (one warp of each), whose tensor memory is taken together.
+__device__ __forceinline__ void tmem_alloc_pair_then_launch(uint32_t* dst, uint32_t ncols) {
+  asm volatile(
+      "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+      "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)),
+      "r"(ncols)
+      : "memory");
+  grid_dep_launch();
 }
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)

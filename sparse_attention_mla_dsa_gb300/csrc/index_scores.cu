@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_launch();
 
   // ---------------------------------------------------------------- layout
   const int npad = p.npad;
@@ -349,12 +348,9 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
       }
     }
   }
-  // A direct launch allocates TMEM now (it reads no input); a persistent one
-  // once the scan has shown that the CTA has tiles.
-  if (kDirect && warp == 1) {
-    tmem_alloc(&ctl->tmem_base, p.tmem_cols);
-    tmem_relinquish();
-  }
+  // Before the wait also in a CTA that turns out to have no tiles: the next kernel
+  // must not start before (with more than 128 columns all of the SM's are taken).
+  if (warp == 1) tmem_alloc_then_launch(&ctl->tmem_base, p.tmem_cols);
   if ((kDirect || groups == 1) && !inputs_early) {
     const GroupRows gr = group_rows(p, kDirect ? blockIdx.y : 0);
     constexpr int kLine = kFp8 ? 128 : 32;  // elements of a 128-byte line
@@ -370,8 +366,8 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   // ---------------------------------------------------------------- this CTA's range
   // Warps 0-1 find the range -- pass 1: T = sum of T_g (CTA 0 records the
   // malformed rows); pass 2: the group holding tile `begin` -- then warp 1
-  // allocates TMEM and meets the epilogue warps at tmem_sync().  Groups are taken kScanThreads at a
-  // time, one per thread; the first kScanRegs rounds keep T_g and the base
+  // meets the epilogue warps at tmem_sync().  Groups are taken kScanThreads at
+  // a time, one per thread; the first kScanRegs rounds keep T_g and the base
   // for pass 2.  Meanwhile the epilogue warps build the q operand of a launch
   // with a single group, which needs no scan to be known.
   long long my_tiles = 0;
@@ -473,10 +469,6 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
     scan_sync();  // g0 / t0 / tg0 / base0 / my_tiles
    }
     if (warp == 1) {
-      if (!kDirect && my_tiles > 0) {
-        tmem_alloc(&ctl->tmem_base, p.tmem_cols);
-        tmem_relinquish();
-      }
       tc_fence_before();
       tmem_sync<kEpiThreads>();  // every path of warp 1 and of the epilogue warps passes it once
       tc_fence_after();
@@ -1005,9 +997,9 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   if (inputs_early) grid_dep_wait();
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && (kDirect || my_tiles > 0)) {
+  if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(kDirect ? ctl->tmem_base : tmem_base, p.tmem_cols);
+    tmem_dealloc(ctl->tmem_base, p.tmem_cols);
   }
 }
 

@@ -1262,13 +1262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&omap);
     if (kGather) tma_prefetch_map(&map16);
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-  grid_dep_launch();
+  if (warp == 1) tmem_alloc_pair_then_launch(&ctl->tmem_base, kTmemCols);
   grid_dep_wait();    // lengths, tables, latents and q come from kernels before
   const Place at = find_place<kThreads>(p, p.pairs, [&](int64_t per) { return per * pair; },
                                         reinterpret_cast<int64_t*>(smem), blockIdx.x == 0);

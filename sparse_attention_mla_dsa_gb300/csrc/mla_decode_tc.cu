@@ -269,8 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head0 = hg * kHeads;
   const int nheads = min(kHeads, p.heads - head0);
 
-  grid_dep_launch();
-
   // ---- set-up: barriers, TMEM (nothing here reads an input)
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -286,10 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_map(&pmap);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&ctl->tmem_base, kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == kMmaWarp) tmem_alloc_then_launch(&ctl->tmem_base, kTmemCols);
   if (tid < kHeads) ctl->mrun[tid] = -INFINITY;
   // Q may be the output of the kernel before (a projection), so by default it
   // is only prefetched into L2 here (a prefetch cannot make a later load
