@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      grid_dep_wait();  // no wait's clock starts before (the activations' copies do not)
       const uint32_t idesc = umma_idesc_bf16(kTileN, kRowsPad);
       const uint32_t base = smem_u32(smem);
       int done = 0;
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Epilogue: warp w reads TMEM lanes 32*(w%4) .. +31, i.e. those weight rows.
     const int quarter = warp & 3;
     const int n = n0 + quarter * 32 + lane;
+    grid_dep_wait();  // as above, and the kernel before may still read the output
     int ok = 1;
     if (lane == 0) ok = mbar_wait(&ctl->tfull, 0, p.wait_ns) ? 1 : 0;
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -172,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.0f;
     }
-    grid_dep_wait();  // the kernel before may still read the output
     if (write && n < p.n) {
       if (p.splits > 1) {
         float* dst = p.part + static_cast<int64_t>(split) * p.m * p.n + n;

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     if (fp8::elect_one()) {
+      grid_dep_wait();  // no wait's clock starts before (the copies do not)
       constexpr uint32_t idesc = fp8::idesc_e4m3(kTileN, kRows);
       const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
       uint32_t s = 0, round = 0;  // block i's stage, and how often that was filled before
@@ -543,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
     if (fp8::elect_one()) {
+      grid_dep_wait();  // no wait's clock starts before (the copies do not)
       constexpr uint32_t idesc = fp8::idesc_e4m3(kTile, kTile);
       const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
       uint32_t s = 0, round = 0;
@@ -580,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
+    grid_dep_wait();  // as above, and the kernel before may still read the output
     const uint32_t src = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
     // (After a wait that gave up the warps go on, with waits that no longer wait.)
     for (int kb0 = 0, g = 0, i = 0; kb0 < nkb; kb0 += kScaleBlocks, ++g) {
@@ -609,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->sempty[g & 1]);
     }
-    grid_dep_wait();  // the kernel before may still read the output
     const int row0 = m0 + quarter * 32, col0 = n0 + half * kCols;
     // The last accumulator has been read, so every copy and MMA is complete and the
     // stages are free.

@@ -116,7 +116,9 @@ static __device__ __noinline__ bool mbar_wait_polls(uint64_t* bar, uint32_t pari
 
 // Wait for the phase with the given parity to complete.  Gives up after
 // `limit_ns` of wall time (checked every 256 polls, every poll for a short
-// limit) or 2^30 polls, whichever comes first, and returns false then.
+// limit) or 2^30 polls, whichever comes first, and returns false then.  A
+// thread whose phase cannot complete before the kernel before has ended calls
+// grid_dep_wait() first: that kernel's time is not this one's stall.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   if (limit_ns >= kShortWaitNs && mbar_try_wait(bar, parity)) return true;
   return mbar_wait_polls(bar, parity, limit_ns);
