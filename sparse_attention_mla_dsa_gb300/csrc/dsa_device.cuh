@@ -130,7 +130,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 // previous kernel has completed and its writes are visible; every kernel here
 // calls it before it reads a predecessor's output or overwrites a buffer a
 // predecessor may still read.  grid_dep_launch() lets the next kernel start.
-// Both are no-ops for kernels launched without the attribute.
+// Both are no-ops for kernels launched without the attribute.  grid_dep_wait()
+// holds up its whole warp, lanes that are elsewhere too, and barriers of the CTA
+// and instructions on tensor memory are of whole warps: a warp of which one lane
+// plays a role meets (__syncwarp) before any of them.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Data written by an earlier kernel of the chain must be read with loads the
 // compiler keeps after grid_dep_wait(): plain loads, or these.  The

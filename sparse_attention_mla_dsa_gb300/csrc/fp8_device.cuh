@@ -144,6 +144,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Every thread of every CTA of the cluster; writes to shared memory before it
 // are seen by all after it.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Four floats at `p` in the CTA of rank `rank`.

@@ -58,11 +58,32 @@ def _bf16_product(api, m, n, k):
     return c, lambda: api.dsa_dense_mm_bf16(a, b, c, ws)
 
 
+def _scores(api, lens, per, fp8):
+    """Rows of sequences of ``lens`` keys; inputs_early."""
+    rows, total, top = len(lens) * per, sum(lens), max(lens)
+    seq = torch.tensor([n - per + 1 + i for n in lens for i in range(per)], dtype=torch.int32, device="cuda")
+    base = torch.tensor([sum(lens[:i]) for i in range(len(lens))], device="cuda").repeat_interleave(per)
+    gate = torch.rand(total, device="cuda").to(torch.bfloat16)
+    w = torch.rand((rows, 32), device="cuda")
+    out = torch.zeros((rows, top), device="cuda")
+    block = (seq, api.make_rows(seq))
+    if fp8:
+        q, k, ks = _codes(rows, 32, 128), _codes(total, 128), torch.rand(total, device="cuda")
+        qs = torch.rand((rows, 32), device="cuda")
+        return out, lambda: api.dsa_index_scores_fp8(block[1], q, qs, w, k, ks, gate, base, per, top, out, inputs_early=True)
+    q, k = torch.randn((rows, 32, 128), device="cuda"), torch.randn((total, 128), device="cuda").to(torch.bfloat16)
+    return out, lambda: api.dsa_index_scores(block[1], q, w, k, gate, base, per, top, out, inputs_early=True)
+
+
 CALLS = {
     "row tiles": lambda api: _product(api, 4, 2048, 4096),
     "tiles": lambda api: _product(api, 200, 4096, 2048),
     "pairs": lambda api: _product(api, 1280, 2048, 512),
     "bf16 product": lambda api: _bf16_product(api, 4, 2048, 4096),
+    "fp8 scores, a few tiles": lambda api: _scores(api, [5000], 1, True),
+    "fp8 scores, two tiles of several": lambda api: _scores(api, [60000], 2, True),
+    "bf16 scores, a few tiles": lambda api: _scores(api, [5000], 1, False),
+    "bf16 scores, two tiles of several": lambda api: _scores(api, [60000], 2, False),
 }
 
 
