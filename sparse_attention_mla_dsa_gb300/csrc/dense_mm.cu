@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

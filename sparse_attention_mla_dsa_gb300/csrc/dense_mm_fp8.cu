@@ -267,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
   if (p.splits == 1) {
     if (warp >= 2 && n0 + row_n < p.n) {
 #pragma unroll
@@ -626,7 +625,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
   tc_fence_before();
   __syncthreads();
   if (p.splits > 1) {
@@ -975,7 +973,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are complete
   }
 
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
   tc_fence_before();
   __syncthreads();
   // After a wait that gave up, copies of this CTA may be in flight that no barrier

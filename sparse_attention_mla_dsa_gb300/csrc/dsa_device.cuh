@@ -131,9 +131,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 // calls it before it reads a predecessor's output or overwrites a buffer a
 // predecessor may still read.  grid_dep_launch() lets the next kernel start.
 // Both are no-ops for kernels launched without the attribute.  grid_dep_wait()
-// holds up its whole warp, lanes that are elsewhere too, and barriers of the CTA
-// and instructions on tensor memory are of whole warps: a warp of which one lane
-// plays a role meets (__syncwarp) before any of them.
+// holds up its whole warp, lanes that are elsewhere too: a warp of which one lane
+// plays a role meets (__syncwarp) before the others call it.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Data written by an earlier kernel of the chain must be read with loads the
 // compiler keeps after grid_dep_wait(): plain loads, or these.  The
@@ -229,7 +228,9 @@ __device__ __forceinline__ void tmem_alloc_pair_then_launch(uint32_t* dst, uint3
       : "memory");
   grid_dep_launch();
 }
+// (Behind a barrier of the CTA, where the lanes of a warp need not be together.)
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  __syncwarp();
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }

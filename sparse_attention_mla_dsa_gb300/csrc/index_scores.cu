@@ -992,9 +992,9 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  // (A lane still in its role, as the MMAs' is, would stand still in another lane's
-  // wait: scores over a long kernel before took none of its time to work in.)
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
+  // A lane still in its role, as the MMAs' is, would stand still in the wait of its
+  // warp's others.
+  __syncwarp();
   // (inputs_early) No CTA completes before the kernel before has: whatever
   // waits for this kernel also waits for that one.
   if (inputs_early) grid_dep_wait();

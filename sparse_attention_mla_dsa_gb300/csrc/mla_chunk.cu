@@ -320,7 +320,6 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 __device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Address of `p` in the shared memory of CTA `rank` of the cluster.
@@ -1292,7 +1291,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     softmax(omap, p, ctl, qop, pop, blocks, tmem, warp, lane, rank, pair);
   }
 
-  __syncwarp();  // (a role of one lane is over: what follows is of whole warps)
   tc_fence_before();
   __syncthreads();
   if (rank == 1 && tid < kBlocks)
