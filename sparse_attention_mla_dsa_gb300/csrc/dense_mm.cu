@@ -92,21 +92,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
+    // Weights stream through once (evict first); the activation tiles are
+    // read by every weight tile of the launch (keep them).
+    const uint64_t w_policy = l2_policy_evict_first();
+    const uint64_t a_policy = l2_policy_evict_normal();
+    const int early = min(nkb, kStages);
     if (lane == 0) {
-      // Weights stream through once (evict first); the activation tiles are
-      // read by every weight tile of the launch (keep them).
-      const uint64_t w_policy = l2_policy_evict_first();
-      const uint64_t a_policy = l2_policy_evict_normal();
       // The weight is an input no kernel writes: the first stages' weight
       // tiles go out before the dependency wait (overlapping the tail of the
       // kernel before), their activation tiles after it, on the same barrier.
-      const int early = min(nkb, kStages);
       for (int i = 0; i < early; ++i) {
         mbar_arrive_expect_tx(&ctl->full[i], kStageBytes);
         tma_load_2d(smem + i * kStageBytes, &wmap, &ctl->full[i], (kb_begin + i) * kBlockK, n0,
                     w_policy);
       }
-      grid_dep_wait();  // the activations may come from the kernel before
+    }
+    __syncwarp();
+    grid_dep_wait();  // the activations may come from the kernel before
+    if (lane == 0) {
       for (int i = 0; i < early; ++i)
         tma_load_2d(smem + i * kStageBytes + kWBytes, &amap, &ctl->full[i], (kb_begin + i) * kBlockK,
                     0, a_policy);
@@ -130,8 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&ctl->full[i % kStages], (i / kStages) & 1, kDrainWaitNs);
     }
   } else if (warp == 1) {
+    grid_dep_wait();  // no wait's clock starts before (the activations' copies do not)
     if (lane == 0) {
-      grid_dep_wait();  // no wait's clock starts before (the activations' copies do not)
       const uint32_t idesc = umma_idesc_bf16(kTileN, kRowsPad);
       const uint32_t base = smem_u32(smem);
       int done = 0;

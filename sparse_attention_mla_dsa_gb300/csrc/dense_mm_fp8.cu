@@ -134,15 +134,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = ctl->tmem_base;
 
   if (warp == 0) {
+    // Any operand may come from the kernel before (a weight just quantised), so
+    // nothing is loaded before the dependency wait; the first tiles of the weight
+    // are on their way to L2 meanwhile, where a write of that kernel lands too.
+    if (lane == 0)
+      for (int i = 0; i < min(nkb, S::kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);
+    __syncwarp();
+    grid_dep_wait();
     if (lane == 0) {
       const uint64_t w_policy = l2_policy_evict_first();
       uint64_t a_policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(a_policy));
-      // Any operand may come from the kernel before (a weight just quantised), so
-      // nothing is loaded before the dependency wait; the first tiles of the weight
-      // are on their way to L2 meanwhile, where a write of that kernel lands too.
-      for (int i = 0; i < min(nkb, S::kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);
-      grid_dep_wait();
       int issued = 0;
       for (; issued < nkb; ++issued) {
         if (aborted(&ctl->abort_flag)) break;
@@ -162,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_wait(&ctl->full[i % S::kStages], (i / S::kStages) & 1, kDrainWaitNs);
     }
   } else if (warp == 1) {
+    grid_dep_wait();  // no wait's clock starts before (the copies do not)
     if (fp8::elect_one()) {
-      grid_dep_wait();  // no wait's clock starts before (the copies do not)
       constexpr uint32_t idesc = fp8::idesc_e4m3(kTileN, kRows);
       const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
       uint32_t s = 0, round = 0;  // block i's stage, and how often that was filled before
@@ -520,6 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quarter = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
   if (warp == 0) {
     // -------------------------------------------------------------- copies
+    if (lane == 0)
+      for (int i = 0; i < min(nkb, kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);  // (as above)
+    __syncwarp();
+    grid_dep_wait();
     if (fp8::elect_one()) {
       uint64_t policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
@@ -527,8 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = i % kStages;
         tma_load_2d(smem + s * kStageBytes + at, map, &ctl->full[s], (kb_begin + i) * kBlock, row, policy);
       };
-      for (int i = 0; i < min(nkb, kStages); ++i) tma_prefetch_l2_2d(&wmap, (kb_begin + i) * kBlock, n0);  // (as above)
-      grid_dep_wait();
       int issued = 0;
       for (; issued < nkb; ++issued) {
         const int s = issued % kStages;
@@ -543,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
+    grid_dep_wait();  // no wait's clock starts before (the copies do not)
     if (fp8::elect_one()) {
-      grid_dep_wait();  // no wait's clock starts before (the copies do not)
       constexpr uint32_t idesc = fp8::idesc_e4m3(kTile, kTile);
       const uint32_t desc0 = static_cast<uint32_t>(umma_desc_sw128_kmajor(smem_u32(smem)));
       uint32_t s = 0, round = 0;

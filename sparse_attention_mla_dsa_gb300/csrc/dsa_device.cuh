@@ -131,8 +131,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 // calls it before it reads a predecessor's output or overwrites a buffer a
 // predecessor may still read.  grid_dep_launch() lets the next kernel start.
 // Both are no-ops for kernels launched without the attribute.  grid_dep_wait()
-// holds up its whole warp, lanes that are elsewhere too: a warp of which one lane
-// plays a role meets (__syncwarp) before the others call it.
+// holds up its whole warp, so whole warps call it: not one lane in its role (which
+// leaves the operands of MMAs and copies in registers of the warp), nor the others
+// while it is there (__syncwarp first).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Data written by an earlier kernel of the chain must be read with loads the
 // compiler keeps after grid_dep_wait(): plain loads, or these.  The

@@ -301,10 +301,13 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   // gates of an indexer write, q and the head weights of a projection, row
   // metadata written on the device), so by default nothing is loaded before
   // grid_dep_wait().  When the caller declares the inputs complete before the
-  // kernel before started (inputs_early), the wait moves to the epilogue's
-  // first score store and to the exit: the loads, MMAs and score arithmetic
-  // then overlap that kernel, and the scores buffer -- which a kernel before
-  // may still read -- is written after it completes.  What overlaps the
+  // kernel before started (inputs_early), the wait of a direct launch moves to
+  // the epilogue's first score store and to the exit: the loads, MMAs and score
+  // arithmetic then overlap that kernel, and the scores buffer -- which a kernel
+  // before may still read -- is written after it completes.  A persistent
+  // launch, whose pipeline runs on past its first stores, waits in every role
+  // before the role's first timed wait: the scan, the first tiles' loads and the
+  // first q operand overlap.  What overlaps the
   // kernel before in either case: barrier set-up, the
   // tensor map, and -- for a direct launch, or one of a single group, whose
   // split is known up to the row length -- L2 prefetches of the CTA's first
@@ -503,6 +506,8 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
                       &ctl->full[issued], sb * 64, y, policy);
       }
     }
+    __syncwarp();
+    if (inputs_early) grid_dep_wait();
     while (ok && remaining > 0 && g < groups) {
       // The group's rows, one per lane (at most 32 rows per group); every
       // lane's loads are issued before any is used.
@@ -588,95 +593,77 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
         mbar_wait(&ctl->full[i % stages], (i / stages) & 1, kDrainWaitNs);
   } else if (warp == 1 && my_tiles > 0) {
     // ============================================================ MMA issuer
-    if (kFp8) {
-      // Beside the epilogue's warps every instruction of this thread counts: operands
-      // by the low words of their descriptors, both barriers looked at together.
-      if (fp8::elect_one()) {
-        const uint32_t idesc = fp8::idesc_e4m3(kTileM, npad);
-        const uint32_t a0 = key_desc_low(smem_u32(stage_base)), b0 = key_desc_low(smem_u32(b_hi));
-        long long done = 0;
-        uint32_t i = 0, s = 0, round = 0;   // tile, its stage, and how often that was filled before
-        bool ok = true;
-        for (int k = 0; ok && done < my_tiles; ++k) {
-          const int slot = k % kSegRing;
-          if (aborted(ctl) || !mbar_wait(&ctl->segfull[slot], (k / kSegRing) & 1, p.wait_ns) ||
-              !mbar_wait(&ctl->qready, k & 1, p.wait_ns)) {
-            if (!aborted(ctl)) set_abort(ctl, p.err, -1);
-            break;
-          }
-          const int n = ctl->seg[slot].ntiles;
-          for (int j = 0; j < n; ++j, ++i) {
-            const uint32_t a = i & 1, empty_at = ((i >> 1) - 1) & 1;  // (i < 2: the phase before the first)
-            const uint32_t there = fp8::look2(&ctl->full[s], round & 1, &ctl->tempty[a], empty_at);
-            if (((there & 1) == 0 && !mbar_wait(&ctl->full[s], round & 1, p.wait_ns)) ||
-                ((there & 2) == 0 && !mbar_wait(&ctl->tempty[a], empty_at, p.wait_ns))) {
-              if (!aborted(ctl)) set_abort(ctl, p.err, -1);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a_low = a0 + s * (kStageBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kKSteps; ++kk)
-              fp8::umma_low<kKeyDescHigh<D>>(tmem_base + a * npad, a_low + kk * 2, b0 + kk * 2, idesc, kk != 0);
-            umma_commit(&ctl->empty[s]);
-            umma_commit(&ctl->tfull[a]);
-            if (++s == static_cast<uint32_t>(stages)) {
-              s = 0;
-              ++round;
-            }
-          }
-          done += n;
-        }
-        // Every MMA issued by this thread is complete before TMEM is released.
-        umma_commit(&ctl->drain);
-        mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+    // The whole warp waits and counts, one lane issues: what it hands to the tensor
+    // core lies in registers that the warp shares, so it must not stand in a wait
+    // with them while the other lanes go on.
+    if (!kDirect && inputs_early) grid_dep_wait();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      // Every lane looks, one goes on where it is not there yet.
+      const bool there = p.wait_ns >= kShortWaitNs && mbar_try_wait(bar, parity);
+      if (__all_sync(0xFFFFFFFFu, there)) return true;
+      int w = 1;
+      if (lane == 0) {
+        w = !aborted(ctl) && mbar_wait(bar, parity, p.wait_ns) ? 1 : 0;
+        if (!w && !aborted(ctl)) set_abort(ctl, p.err, -1);
       }
-    } else if (lane == 0) {
-      const uint32_t idesc = umma_idesc_bf16(kTileM, npad);
-      const uint32_t a0 = smem_u32(stage_base), bh = smem_u32(b_hi), bl = smem_u32(b_lo);
-      long long done = 0;
-      int i = 0;
-      bool ok = true;
-      for (int k = 0; ok && done < my_tiles; ++k) {
-        const int slot = k % kSegRing;
-        if (aborted(ctl) || !mbar_wait(&ctl->segfull[slot], (k / kSegRing) & 1, p.wait_ns) ||
-            !mbar_wait(&ctl->qready, k & 1, p.wait_ns)) {
-          if (!aborted(ctl)) set_abort(ctl, p.err, -1);
+      __syncwarp();
+      return __shfl_sync(0xFFFFFFFFu, w, 0) != 0;
+    };
+    const uint32_t idesc = kFp8 ? fp8::idesc_e4m3(kTileM, npad) : umma_idesc_bf16(kTileM, npad);
+    long long done = 0;
+    uint32_t i = 0, s = 0, round = 0;   // tile, its stage, and how often that was filled before
+    bool ok = true;
+    for (int k = 0; ok && done < my_tiles; ++k) {
+      const int slot = k % kSegRing;
+      if (!wait(&ctl->segfull[slot], (k / kSegRing) & 1) || !wait(&ctl->qready, k & 1)) break;
+      const int n = ctl->seg[slot].ntiles;
+      for (int j = 0; j < n; ++j, ++i) {
+        // Beside the epilogue's warps every instruction here counts: both barriers
+        // looked at together, FP8 operands by the low words of their descriptors.
+        const uint32_t a = i & 1, empty_at = ((i >> 1) - 1) & 1;  // (i < 2: the phase before the first)
+        const uint32_t there = fp8::look2(&ctl->full[s], round & 1, &ctl->tempty[a], empty_at);
+        if (!__all_sync(0xFFFFFFFFu, there == 3) && !(wait(&ctl->full[s], round & 1) && wait(&ctl->tempty[a], empty_at))) {
+          ok = false;
           break;
         }
-        const int n = ctl->seg[slot].ntiles;
-        for (int j = 0; j < n; ++j, ++i) {
-          const int s = i % stages, a = i & 1;
-          if (aborted(ctl) || !mbar_wait(&ctl->full[s], (i / stages) & 1, p.wait_ns) ||
-              (i >= 2 && !mbar_wait(&ctl->tempty[a], ((i >> 1) - 1) & 1, p.wait_ns))) {
-            if (!aborted(ctl)) set_abort(ctl, p.err, -1);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        tc_fence_after();
+        if (fp8::elect_one()) {
           const uint32_t d_tmem = tmem_base + a * npad;
-          const uint32_t a_stage = a0 + s * kStageBytes;
+          if constexpr (kFp8) {
+            const uint32_t a_low = key_desc_low(smem_u32(stage_base)) + s * (kStageBytes >> 4);
+            const uint32_t b_low = key_desc_low(smem_u32(b_hi));
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t b_base = half ? bl : bh;
+            for (int kk = 0; kk < kKSteps; ++kk)
+              fp8::umma_low<kKeyDescHigh<D>>(d_tmem, a_low + kk * 2, b_low + kk * 2, idesc, kk != 0);
+          } else {
+            const uint32_t a_stage = smem_u32(stage_base) + s * kStageBytes;
 #pragma unroll
-            for (int kk = 0; kk < kKSteps; ++kk) {
-              const uint32_t a_addr = a_stage + (kk >> 2) * (kTileM * 128) + (kk & 3) * 32;
-              const uint32_t b_addr = b_base + (kk >> 2) * (npad * 128) + (kk & 3) * 32;
-              umma_bf16(d_tmem, umma_desc_sw128_kmajor(a_addr), umma_desc_sw128_kmajor(b_addr),
-                        idesc, (half | kk) != 0);
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t b_base = smem_u32(half ? b_lo : b_hi);
+#pragma unroll
+              for (int kk = 0; kk < kKSteps; ++kk) {
+                const uint32_t a_addr = a_stage + (kk >> 2) * (kTileM * 128) + (kk & 3) * 32;
+                const uint32_t b_addr = b_base + (kk >> 2) * (npad * 128) + (kk & 3) * 32;
+                umma_bf16(d_tmem, umma_desc_sw128_kmajor(a_addr), umma_desc_sw128_kmajor(b_addr),
+                          idesc, (half | kk) != 0);
+              }
             }
           }
           umma_commit(&ctl->empty[s]);
           umma_commit(&ctl->tfull[a]);
         }
-        done += n;
+        __syncwarp();
+        if (++s == static_cast<uint32_t>(stages)) {
+          s = 0;
+          ++round;
+        }
       }
-      // Every MMA issued by this thread is complete before TMEM is released.
-      umma_commit(&ctl->drain);
-      mbar_wait(&ctl->drain, 0, kDrainWaitNs);
+      done += n;
     }
+    // Every MMA issued is complete before TMEM is released.
+    if (fp8::elect_one()) umma_commit(&ctl->drain);
+    __syncwarp();
+    if (lane == 0) mbar_wait(&ctl->drain, 0, kDrainWaitNs);
   } else if (warp >= 2) {
     // ============================================================ q build + epilogue
     // Every epilogue warp passes the same named barriers in the same order
@@ -797,7 +784,8 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
       build_q(gr.r0, gr.nrows);
     }
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    bool waited = !inputs_early;
+    if (!kDirect && inputs_early) grid_dep_wait();
+    bool waited = !kDirect || !inputs_early;   // (of the warp: its first tile waits, whoever stores)
     long long done = 0;
     int i = 0;        // tiles consumed by this CTA so far (TMEM buffer and phase)
     bool ok = true;
@@ -898,13 +886,12 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
               }
               left -= 32;
               if (left == 0) {
-                if (t < sg.row_len[jr]) {
-                  if (!waited) {
-                    grid_dep_wait();
-                    waited = true;
-                  }
-                  *dst = gt * ((part[0] + part[1]) + (part[2] + part[3]));
+                if (!waited) {
+                  grid_dep_wait();
+                  waited = true;
                 }
+                if (t < sg.row_len[jr]) *dst = gt * ((part[0] + part[1]) + (part[2] + part[3]));
+                __syncwarp();  // the next read of tensor memory is of the whole warp
                 part[0] = part[1] = part[2] = part[3] = 0.0f;
                 left = heads;
                 dst += p.max_len;
@@ -970,13 +957,12 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
             }
           }
           }
-          if (t < sg.row_len[jr]) {
-            if (!waited) {  // (inputs_early) the first store waits for the kernel before
-              grid_dep_wait();
-              waited = true;
-            }
-            p.scores[static_cast<int64_t>(r0 + jr) * p.max_len + t] = gt * sum;
+          if (!waited) {  // (inputs_early) the first store waits for the kernel before
+            grid_dep_wait();
+            waited = true;
           }
+          if (t < sg.row_len[jr]) p.scores[static_cast<int64_t>(r0 + jr) * p.max_len + t] = gt * sum;
+          __syncwarp();  // (as above)
         }
         if (!scored) free_acc(a);
         if (!kFp8 && __shfl_sync(0xFFFFFFFFu, aborted(ctl) ? 1 : 0, 0)) {
@@ -992,9 +978,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  // A lane still in its role, as the MMAs' is, would stand still in the wait of its
-  // warp's others.
-  __syncwarp();
+  __syncwarp();  // (grid_dep_wait is of whole warps)
   // (inputs_early) No CTA completes before the kernel before has: whatever
   // waits for this kernel also waits for that one.
   if (inputs_early) grid_dep_wait();

@@ -82,8 +82,14 @@ CALLS = {
     "bf16 product": lambda api: _bf16_product(api, 4, 2048, 4096),
     "fp8 scores, a few tiles": lambda api: _scores(api, [5000], 1, True),
     "fp8 scores, two tiles of several": lambda api: _scores(api, [60000], 2, True),
+    "fp8 scores, one sequence": lambda api: _scores(api, [200000], 2, True),
+    "fp8 scores, many sequences": lambda api: _scores(api, [3000 + 97 * i for i in range(40)], 2, True),
+    "fp8 scores, short sequences": lambda api: _scores(api, [2 + i % 90 for i in range(900)], 1, True),
     "bf16 scores, a few tiles": lambda api: _scores(api, [5000], 1, False),
     "bf16 scores, two tiles of several": lambda api: _scores(api, [60000], 2, False),
+    "bf16 scores, one sequence": lambda api: _scores(api, [200000], 2, False),
+    "bf16 scores, many sequences": lambda api: _scores(api, [3000 + 97 * i for i in range(40)], 2, False),
+    "bf16 scores, short sequences": lambda api: _scores(api, [2 + i % 90 for i in range(900)], 1, False),
 }
 
 
