@@ -1091,7 +1091,7 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 }  // namespace
 
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
-  p.kblocks = (p.k + kBlock - 1) / kBlock;
+  p.kblocks = ceil_div(p.k, kBlock);
   // Up to 64 rows: row tiles.  More: pairs from more than one tile of 128 x 128 an SM
   // on (1,024 x 4,096 x 4,096: 17.7 us, by CTAs 22.6; 512 x 4,096 x 4,096, 128 tiles,
   // 17.3 and 11.9), below that a CTA or some for each of those tiles (777 x 1,024 x

@@ -584,7 +584,7 @@ dsa_status dsa_quantize_fp8(const void* x, int32_t x_fp32, int32_t rows, int32_t
   p.scales = scales;
   p.rows = rows;
   p.k = k;
-  p.kblocks = (k + 127) / 128;
+  p.kblocks = ceil_div(k, 128);
   p.block_rows = block_rows;
   p.x_fp32 = x_fp32;
   if (static_cast<int64_t>(rows) * p.kblocks > INT32_MAX ||

@@ -27,6 +27,9 @@ inline cudaLaunchAttribute dependent_launch_attr() {
 // take away what another has set and not launched yet.
 constexpr int kMaxSmemBytes = 227 * 1024;
 
+// ceil(a / b) for a >= 0 up to the type's largest value.
+inline int32_t ceil_div(int32_t a, int32_t b) { return a / b + (a % b != 0 ? 1 : 0); }
+
 // Lets `kernel` have `bytes` (always the same) of shared memory on the current device:
 // asked once a device, of which `done` keeps a bit each, as the call takes 0.4 us.
 inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
