@@ -231,12 +231,12 @@ __global__ void __launch_bounds__(256) dense_mm_reduce_kernel(const DenseMmParam
 }  // namespace
 
 void plan_dense_mm(DenseMmParams& p, int num_sms) {
-  p.tiles = (p.n + kTileN - 1) / kTileN;
-  p.kblocks = (p.k + kBlockK - 1) / kBlockK;
+  p.tiles = ceil_div(p.n, kTileN);
+  p.kblocks = ceil_div(p.k, kBlockK);
   // Split K only when the weight tiles alone leave SMs idle, and keep at
   // least four K blocks (64 KB of weight) per CTA.
   int splits = 1;
-  if (p.tiles < num_sms) splits = (num_sms + p.tiles - 1) / p.tiles;
+  if (p.tiles < num_sms) splits = ceil_div(num_sms, p.tiles);
   const int max_splits = p.kblocks / 4 > 1 ? p.kblocks / 4 : 1;
   splits = splits < max_splits ? splits : max_splits;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
