@@ -199,6 +199,9 @@ __device__ __forceinline__ bool row_ok(const IndexParams& p, int len, int64_t rb
          len <= written;
 }
 
+// Key tiles of n tokens (any int: n + kTileM may not be one).
+__device__ __forceinline__ int tiles_of(int n) { return n / kTileM + (n % kTileM != 0 ? 1 : 0); }
+
 // Key tiles and arena base of group g (one thread).  The loads of every row
 // are issued before any result is used (no store in between); the reasons
 // for malformed rows are recorded in a second pass over them.
@@ -217,7 +220,7 @@ __device__ int group_tiles(const IndexParams& p, int g, bool report, int64_t& ba
   }
   if (report && bad)
     for (int j = 0; j < gr.nrows; ++j) row_len_checked(p, gr.r0 + j, base, written, true);
-  return (m + kTileM - 1) / kTileM;
+  return tiles_of(m);
 }
 
 // Named barrier of the two scan warps.
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
     // below; thread 0's prefetch still starts the first tiles' DRAM reads a
     // little sooner, which measured faster than skipping it.)
     if (kDirect || groups == 1) {
-      const long long tg = (p.max_len + kTileM - 1) / kTileM;
+      const long long tg = tiles_of(p.max_len);
       const long long b0 = kDirect ? static_cast<long long>(blockIdx.x) * p.direct_tiles : tg * c / ctas;
       const long long b1 = kDirect ? b0 + p.direct_tiles : tg * (c + 1) / ctas;
       const int64_t base_hint = *reinterpret_cast<const volatile int64_t*>(
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
       int m = len;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const int tg = (m + kTileM - 1) / kTileM;
+      const int tg = tiles_of(m);
       my_tiles = max(0, min(p.direct_tiles, tg - t0));
       if (my_tiles > 0) {
         Seg& sg = ctl->seg[0];
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
       int m = len;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const int tg = (m + kTileM - 1) / kTileM;
+      const int tg = tiles_of(m);
       if (tg <= t0) {  // a group with no tiles (never the first: it holds tile `begin`)
         ++g;
         t0 = 0;
@@ -816,14 +819,14 @@ __global__ void __launch_bounds__(64 + kEpiOf<kFp8>, kFp8 ? 2 : 1)
       // the caller declared them complete before it).
       // (kFp8: the key's scale likewise.)
       auto load_gate = [&](int j) {
-        const int t = (t_first + j) * kTileM + lane_tok;
         if constexpr (kFp8)
           if (p.gate == nullptr) return static_cast<uint16_t>(0x3F80);  // 1
-        return (j < n && t < max_len_group) ? p.gate[base + t] : static_cast<uint16_t>(0);
+        const uint32_t t = static_cast<uint32_t>(t_first + j) * kTileM + lane_tok;  // (past the last tile it may leave int)
+        return (j < n && t < static_cast<uint32_t>(max_len_group)) ? p.gate[base + t] : static_cast<uint16_t>(0);
       };
       auto load_scale = [&](int j) {
-        const int t = (t_first + j) * kTileM + lane_tok;
-        return (j < n && t < max_len_group) ? p.k_scale[base + t] : 0.0f;
+        const uint32_t t = static_cast<uint32_t>(t_first + j) * kTileM + lane_tok;
+        return (j < n && t < static_cast<uint32_t>(max_len_group)) ? p.k_scale[base + t] : 0.0f;
       };
       // A set's first tile of the segment.
       const int j_first = kSets == 1 ? 0 : (i ^ set) & 1;
