@@ -28,8 +28,9 @@ def _dev(a: np.ndarray, device) -> torch.Tensor:
 
 class DeviceWorkload:
     """All inputs of a workload resident on one CUDA device, plus outputs.
-    ``index_fp8``: the indexer's keys are kept as E4M3 codes with a scale a key
-    (half the bytes that S1 reads), and S1 quantises the step's queries."""
+    ``index_fp8``: the indexer's keys are kept as E4M3 codes with a scale a key alone
+    (half the bytes that S1 reads; ``idx_k`` is None), and S1 quantises the step's
+    queries, a launch more: for batches and long contexts, where the keys' bytes count."""
 
     def __init__(self, wl, device: str | torch.device = "cuda", pool: torch.Tensor | None = None,
                  _clone_of: "DeviceWorkload | None" = None, index_fp8: bool = False):
@@ -68,6 +69,7 @@ class DeviceWorkload:
             self.q8 = torch.empty(self.q_idx.shape, dtype=torch.uint8, device=d)
             self.q_scale = torch.empty(self.q_idx.shape[:2], dtype=torch.float32, device=d)
             api.dsa_quantize_fp8(self.idx_k, self.idx_k8, self.idx_scale)
+            self.idx_k = None
         self.out_target = None      # where S3 writes; None = self.out
         self.rows = api.make_rows(self.seq_lens, self.block_table, wl.block_size, self.slots,
                                   self.positions, shared_table=(wl.bt_stride == 0))
@@ -90,8 +92,8 @@ class DeviceWorkload:
         return DeviceWorkload(self.wl, _clone_of=self)
 
     def input_bytes(self) -> int:
-        return sum(getattr(self, n).numel() * getattr(self, n).element_size()
-                   for n in ("pool", "idx_k", "idx_gate", "Q", "q_idx"))
+        held = (getattr(self, n) for n in ("pool", "idx_k", "idx_k8", "idx_scale", "idx_gate", "Q", "q_idx"))
+        return sum(t.numel() * t.element_size() for t in held if t is not None)
 
     # ---- the four steps
     def latent_write(self, stream=None):
