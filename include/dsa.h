@@ -523,8 +523,8 @@ dsa_status dsa_indexer_write_fp8(const dsa_rows *rows, const uint16_t *k_raw, co
  * code takes its head out of the sum.
  * Numerics: the products are exact and accumulate in FP32 on the tensor cores; the
  * heads are added in FP32, every fourth one in order into one of four sums, and
- * (s0 + s1) + (s2 + s3) is multiplied by the product of gate and scale.  Each row's result does not depend on rows_per_seq or on the other rows
- * (bit for bit).
+ * (s0 + s1) + (s2 + s3) is multiplied by the product of gate and scale.  Each row's
+ * result does not depend on rows_per_seq or on the other rows (bit for bit).
  */
 dsa_status dsa_index_scores_fp8(const dsa_rows *rows, const uint8_t *q, const float *q_scale,
                                 const float *head_w, const uint8_t *idx_k, const float *idx_scale,
@@ -700,7 +700,8 @@ int64_t dsa_bt_entries_needed(int64_t seq_len, int64_t k, int64_t block_size);
 
 /*
  * Limit, in nanoseconds of wall time, on every pipeline wait inside the
- * kernels launched after this call (0 restores the default, 500 ms).  A wait
+ * kernels launched after this call (0 restores the default, 500 ms; the time that
+ * the kernel before still runs does not count).  A wait
  * that runs out records DSA_DEVERR_TIMEOUT, the CTA stops its pipeline and
  * its results are zero; the CTA still waits for its own copies and MMAs in
  * flight (that drain keeps its own 500 ms limit) before it exits, so a short

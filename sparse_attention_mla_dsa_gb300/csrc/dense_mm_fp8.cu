@@ -17,8 +17,11 @@
 // sums through distributed shared memory in the order of the ranges: one launch,
 // no workspace.
 //
-// Bound by the weight's bytes (32 x 4,096 x 32,768: 21.8 us, 6.2 TB/s); one token by
-// the launch and the first loads (1 x 2,048 x 4,096: 4.3 us).
+// Bound by the weight's bytes (32 x 4,096 x 32,768: 22.2 us, 6.1 TB/s); one token by
+// the launch and the first loads (1 x 2,048 x 4,096: 4.4 us).
+//
+// Times in this file are of captured calls, up to eight weights in turn (those above
+// 16 MB then come from HBM); two for one shape were measured on one box in turn.
 //
 // CTA roles (192 threads): warp 0 issues TMA, warp 1 owns TMEM and issues the
 // MMAs (one thread), warps 2-5 are the epilogue (one TMEM lane quarter each).
@@ -434,12 +437,12 @@ __device__ __forceinline__ void store_tile(const Fp8MmParams& p, const CUtensorM
 //   D = 128 x 128 FP32 (lane = activation row, column = weight row), four in turn
 // so a thread of the epilogue has one row and columns of one row of weight scales: one
 // factor a block of k, where row tiles read one for every column from shared memory,
-// whose bandwidth then bounds them (256 x 4,096 x 32,768: 69 us by row tiles).  Up to
+// whose bandwidth then bounds them (256 x 4,096 x 32,768: 40.6 us, by row tiles 69.4).  Up to
 // four CTAs, a cluster, share a tile's blocks of k as above.
 //
 // Bound by 32 KB from L2 for each block and CTA and the epilogue's reads of TMEM (512 x
 // 4,096 x 4,096: 11.9 us, 1.4 PFLOP/s).  Where k is not a multiple of 128 a block of a
-// row lies in two lines of L2 (777 x 1,003 with k 4,112: 12.8 us, with 4,224 10.9).
+// row lies in two lines of L2 (777 x 1,003 with k 4,112: 12.7 us, with 4,224 10.8).
 //
 // Roles (384 threads): warp 0 copies, warp 1 issues the MMAs, warps 2-3 fetch the
 // activation scales and turn them in shared memory, warps 4-11 are the epilogue (a
@@ -684,12 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // What bounds it is how soon an accumulator is read, scaled and free again (by
 // halves the MMAs of three others, not of one, run meanwhile) and that the epilogue's
-// reads of TMEM take turns with the MMAs: without them the MMAs of a block take 660
-// clocks beside their copies, with them 820.  Eight epilogue warps of 128 columns and
-// not sixteen of 64 (108 us for 1,024 x 4,096 x 32,768, 111 with sixteen): beside
+// reads of TMEM take turns with the MMAs.  Eight epilogue warps of 128 columns and
+// not sixteen of 64 (1,024 x 4,096 x 32,768: 108 us, 111 with sixteen): beside
 // their instructions the one thread that issues the MMAs has to find room, which is
 // also why it looks at three barriers at once and adds to descriptors' low words only
-// (one after the other, 121 us).  The activation scales come through shared memory,
+// (one after the other 121 us for 108; a whole warp that waits, with a lane elected
+// for the MMAs alone, 120.6 for 103.2, and 13.8 for 10.8 at 300 x 4,096 x 4,096).  The activation scales come through shared memory,
 // turned there by two warps: a load by the epilogue would touch a line for each row.
 // The outputs leave through shared memory by TMA, behind the next tile's MMAs.
 //
@@ -749,9 +752,8 @@ struct PairWaits : Waits {
     return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
   }
 };
-// Which of three phases are complete (bits 0-2).  A look at a barrier takes ~140
-// clocks beside the epilogue's warps; three in a row, and not one after the other's
-// answer, leave the issuing thread time for the MMAs.
+// Which of three phases are complete (bits 0-2): three looks in a row, and not one
+// after the other's answer, for which a thread waits long beside the epilogue's warps.
 __device__ __forceinline__ uint32_t look3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint64_t* b2, uint32_t p12) {
   uint32_t r;
   asm volatile(
@@ -1093,11 +1095,15 @@ cudaError_t launch_rows(const Fp8MmParams& p, const CUtensorMap& wmap, const CUt
 void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   p.kblocks = ceil_div(p.k, kBlock);
   // Up to 64 rows: row tiles.  More: pairs from more than one tile of 128 x 128 an SM
-  // on (1,024 x 4,096 x 4,096: 17.7 us, by CTAs 22.6; 512 x 4,096 x 4,096, 128 tiles,
-  // 17.3 and 11.9), below that a CTA or some for each of those tiles (777 x 1,024 x
-  // 2,048: 7.3 us, by row tiles 8.9; 1,000 x 2,048 x 512 4.2 and 5.7), unless they are
-  // fewer than eight, where k can be split further for row tiles (65 x 128 x 16,384: 9.3
-  // us, by 128 x 128 11.3; 100 x 512 x 2,048 5.2 and 5.6).
+  // on (1,024 x 4,096 x 4,096: 18.0 us, by CTAs 22.4; 129 x 16,384 x 4,096 20.4 and 24.4;
+  // 512 x 4,096 x 4,096, 128 tiles, 17.5 and 11.9), below that a CTA or some for each of
+  // those tiles (777 x 1,024 x 2,048: 7.2 us, by row tiles 8.9; 1,000 x 2,048 x 512 4.2
+  // and 5.6), unless they are fewer than eight, where k can be split further for row
+  // tiles (65 x 128 x 16,384: 9.4 us, by 128 x 128 11.0; 100 x 512 x 2,048 5.1 and 5.5).
+  // Up to 128 rows the second CTA of each pair has none: pairs are ahead there only
+  // where k is short and the outputs count (100 x 65,536 x 512: 15.7 us, by CTAs 18.3;
+  // 128 x 32,768 x 1,536 17.6 and 16.5, x 4,096 35.9 and 30.3; 100 x 20,000 x 4,096 33.4
+  // and 26.6), which this rule does not see.
   const int64_t mt = (p.m + block::kTile - 1) / block::kTile, nt = (p.n + block::kTile - 1) / block::kTile;
   p.pairs = 0;
   p.row_tile = p.m <= 16 ? 16 : p.m <= 32 ? 32 : 64;
@@ -1111,11 +1117,11 @@ void plan_fp8_mm(Fp8MmParams& p, int num_sms) {
   }
   if (p.m > 64 && mt * nt >= 8) p.row_tile = 128;
   // k is split as far as the launch's clusters run at once, with two blocks of k in each
-  // range at least (32 rows, 4,096 x 32,768: 24.9 us; 28.3 with ranges for one CTA an SM
-  // and a few more, 31.8 for fewer; 4,096 of k by ranges of 4, 8 and 16 blocks: 5.0, 6.1,
-  // 9.0 us; 40 clusters of 7 row tiles, which take two turns, 12.2 us, of 6 8.2; 48 of 3
-  // tiles of 128 x 128 15.6, of 2 9.1).  Two CTAs of row tiles fit an SM.  Up to 64 rows
-  // the split must not depend on m.
+  // range at least (32 x 4,096 x 32,768 in eight, four and two ranges: 22.2, 27.0, 45.8 us;
+  // 1 x 2,048 x 4,096 4.4, 5.1, 6.9; 20 x 5,120 x 4,096 in clusters of 7 row tiles, which
+  // take two turns, 11.1 us, of 6 7.0; 300 x 2,048 x 4,096 in clusters of 3 tiles of 128 x
+  // 128 15.4, of 2 9.3).  Two CTAs of row tiles fit an SM.  Up to 64 rows the split must
+  // not depend on m.
   const int64_t tiles = static_cast<int64_t>((p.n + kTileN - 1) / kTileN) * ((p.m + p.row_tile - 1) / p.row_tile);
   const ClustersAtOnce& at_once = clusters_at_once(num_sms);
   const bool rows = p.row_tile <= 64;

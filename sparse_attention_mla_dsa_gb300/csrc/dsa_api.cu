@@ -105,7 +105,8 @@ void set_index_rows(IndexParams& p, const DeviceInfo& dev, const dsa_rows& rows,
   // count that is not a multiple of 16 runs one row per launch group so that
   // no 16-column TMEM load straddles two rows.
   // FP8 keys have two sets of epilogue warps and no query split in two, so groups of
-  // 128 columns (1,024 rows of 32 heads over 9,000 keys: 66 us then, 84 with 64).
+  // 128 columns (1,024 rows of 32 heads over 9,000 keys: 57.5 us, 71.0 with 64; eight
+  // verifies of 4 rows over 65k to 131k keys 23.2 and 26.3).
   int sub = (p.q_codes != nullptr ? 128 : 64) / index_heads;
   if (index_heads % 16 != 0) sub = 1;
   sub = sub < 1 ? 1 : (sub > 32 ? 32 : sub);
@@ -624,8 +625,8 @@ dsa_status dsa_dense_mm_fp8(const uint8_t* a, const float* a_scale, const uint8_
 
   // Boxes of 128 bytes of k (the swizzle span, one block of scales); rows and
   // columns past the tensors read as zero.  Fetched into L2 by 128 bytes, by 256 for
-  // pairs (777 x 1,003 x 4,112: 12.8 us, 14.0 by 256; 32 x 4,096 x 32,768 23.4 and 23.6;
-  // 1,024 x 4,096 x 8,192, pairs, 30.5 and 30.2).
+  // pairs (777 x 1,003 x 4,112: 12.7 us, 14.0 by 256; 32 x 4,096 x 32,768 22.2 and 22.7;
+  // 1,024 x 4,096 x 8,192, pairs, 30.4 by 128 and 30.2; captured, weights in turn).
   CUtensorMap wmap, amap;
   auto map = [&](CUtensorMap* out, const uint8_t* t, int32_t rows, int32_t box_rows) {
     const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};

@@ -54,16 +54,19 @@ __device__ __forceinline__ void umma_low(uint32_t d_tmem, uint32_t a, uint32_t b
 }
 
 // One lane of the whole warp.  A branch on it leaves the operands of MMAs and copies
-// in uniform registers, one on lane == 0 does not.
+// in uniform registers, which the warp shares; one on lane == 0 does not.  So where
+// the lane waits inside, the others must stand still before those are set: its first
+// wait is one that cannot be over yet (for copies that have only begun), and what
+// follows the branch is a barrier of the CTA, no operation of the warp.  Otherwise
+// the warp waits as a whole and the branch holds the instructions alone.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
 }
 
-// Which of two phases are complete (bits 0-1).  A look at a barrier takes ~140
-// clocks beside an epilogue's warps; two in a row, and not one after the other's
-// answer, leave an issuing thread time for the MMAs.
+// Which of two phases are complete (bits 0-1): two looks in a row, and not one after
+// the other's answer, for which a thread waits long beside an epilogue's warps.
 __device__ __forceinline__ uint32_t look2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
   uint32_t r;
   asm volatile(

@@ -32,7 +32,7 @@
 //   warp 0     walks the CTA's segments (row lengths checked per segment,
 //              one record per segment in a small ring) and issues the key
 //              TMA loads (lane 0);
-//   warp 1     owns TMEM and issues the MMAs (lane 0);
+//   warp 1     owns TMEM and issues the MMAs (it waits as a whole, one lane issues);
 //   warps 2-5  build each segment's q operand and head weights, then run the
 //              epilogue (one TMEM lane quarter each); with FP8 keys warps 2-9, two
 //              sets that take the tiles in turn.
@@ -42,16 +42,16 @@
 // kFp8 is the same over an FP8 key cache (dsa_index_scores_fp8): keys and
 // queries are E4M3 codes with one FP32 scale a key and a (row, head),
 //     s_r(t) = gate(t) ks(t) * sum_h (w_r[h] qs_r[h]) * relu(q8_r[h] . k8(t))
-// (a scale is not negative, so it passes through the ReLU), whose products one
+// (the scales stand outside the ReLU), whose products one
 // FP8 MMA forms exactly: half the key bytes and a quarter of the MMA time, the
 // query operand is copied, not split, and the scales ride on the head weights
 // and the gate.  A decode is bound by the key bytes (64 requests of 4k to 128k, 64
-// heads, 296 MB: 47.9 us, 6.2 TB/s).  A prompt's chunk, whose rows share the keys, is
+// heads, 296 MB: 46.1 to 48.1 us, 6.2 to 6.4 TB/s).  A prompt's chunk, whose rows share the keys, is
 // bound by the epilogue, a maximum and an addition for every head and token beside
 // the reads of TMEM and of the head weights (1,024 rows of 32 heads over 9,000 keys:
-// 62.3 us, where the MMAs alone would take 18): hence two sets of epilogue warps on
-// different tiles (the rows of each tile shared out between them: 78 us for 66),
-// accumulators that are free once read, not once added up, and four sums a row.
+// 57.5 us, where the MMAs alone would take 18): hence two sets of epilogue warps on
+// different tiles (the rows of each tile shared out between them: 78 us where this
+// took 66), accumulators that are free once read, not once added up, and four sums a row.
 #include <climits>
 
 #include "dsa_internal.h"
