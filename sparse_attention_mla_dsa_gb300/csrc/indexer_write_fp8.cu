@@ -14,7 +14,7 @@
 // border it lies.  It is taken in FP32 with a bound on its error; a row where that
 // leaves a code or the scale open (0.6 % of rows of normal inputs), or that FP32
 // does not hold, is taken again in double.  In double throughout, 4,001 rows took
-// 34 us (7.2 now) and four rows 4.9 (1.6): the FP64 rate is a small part of the FP32 one.
+// 34 us (7.4 now) and four rows 4.9 (1.7): the FP64 rate is a small part of the FP32 one.
 //   mean      two FP32 words (sums that keep their rounding errors), so x - mean
 //             is good to 2^-23 of itself however far the mean is from 0
 //   variance  d^2 2^-22, nine additions of positive terms 9 * 2^-24: 2^-20.2

@@ -12,7 +12,7 @@
 // Bound by memory: 3 bytes an element from bf16, 5 from FP32.  Rows of 1: a
 // block is 16 bytes of each of 16 lanes (bf16) or of 32 (FP32), its largest
 // element is found by shuffles and its values stay in registers in between (1,024 x
-// 32,768 bf16: 14.9 us, 6.8 TB/s, with part of the codes still in L2; 17.8 where every
+// 32,768 bf16: 15.1 us, 6.7 TB/s, with part of the codes still in L2; 17.8 where every
 // byte comes from and goes to other buffers).  Maxima are of the bits without signs,
 // two bf16 values at a time, and infinities and NaN are taken out only in a warp that
 // has one: by a test of every value, 16.8 us.  Tiles of 128 rows: one CTA a tile, which

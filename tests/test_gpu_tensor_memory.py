@@ -133,3 +133,30 @@ def test_calls_right_behind_scores_that_take_all_of_it(api, scores, D):
     for c in calls:
         c.check()
     assert api.dsa_get_error(reset=True)[0] == 0
+
+
+def test_two_streams_at_once(api):
+    # each stream's kernels beside the other's on the same SMs, clusters among them
+    def calls(seed):
+        return [Fp8Scores(api, [6000, 2500, 6500, 5000], 64, seed), Fp8Product(api, 60, 1024, 2048),
+                Fp8Scores(api, [700, 90], 64, seed + 1), Fp8Product(api, 16, 2048, 1024),
+                Bf16Scores(api, [3000, 9000, 4000], 64, seed + 2), Fp8Product(api, 40, 4096, 1024),
+                Bf16Product(api, 16, 1000, 1024), Fp8Product(api, 200, 512, 1024)]
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets, graphs = [calls(1), calls(11)[::-1]], []
+    for s, mine in zip(streams, sets):
+        s.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            for c in mine * 3:
+                c.call(api)
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for mine in sets:
+        for c in mine:
+            c.check()
+    assert api.dsa_get_error(reset=True)[0] == 0

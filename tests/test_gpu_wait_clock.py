@@ -102,7 +102,7 @@ def test_a_long_kernel_before_is_not_a_timeout(api, busy, name):
     assert api.dsa_get_error(reset=True)[0] == 0
     want = out.clone()
     try:
-        for _ in range(3):
+        for _ in range(20):
             out.zero_()
             busy()
             api.dsa_set_wait_limit_ns(LIMIT_NS)       # of the calls from here on
